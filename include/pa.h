@@ -68,7 +68,7 @@ const char* pa_version(void);
 /*
  * Synchronise `stream`, then read and clear the device error word of the
  * current device.  Returns PA_OK, or the first of PA_ERR_BAD_TABLE,
- * PA_ERR_BAD_SLOT, PA_ERR_BAD_CONTEXT, PA_ERR_TIMEOUT whose bit was set by a
+ * PA_ERR_BAD_SLOT, PA_ERR_BAD_CONTEXT, PA_ERR_POOL_EXHAUSTED, PA_ERR_TIMEOUT whose bit was set by a
  * kernel since the last check, or PA_ERR_CUDA if the stream failed.
  */
 int pa_check_error(void* stream);
@@ -460,6 +460,106 @@ int pa_stepper_set_call(pa_stepper* st, int slot, const pa_step_call* call);
 int pa_stepper_launch(pa_stepper* st, int step, size_t upload_bytes, int num_deltas);
 /* Block the host until the output of `step` has arrived in its slot's host buffer. */
 int pa_stepper_wait(pa_stepper* st, int step);
+
+/* ---- a serving step over an FP8 cache ------------------------------------------------- */
+/*
+ * pa_advance_tables — block tables, positions and slots of a step, built on the GPU from the
+ * requests' lengths (the block pool's release and append for a whole step at once, for requests
+ * whose blocks are their own: no shared blocks, no copy-on-write).  Request b holds context_lens[b]
+ * tokens; new_lens[b] >= 0 appends that many, new_lens[b] < 0 gives its blocks back.  free_blocks
+ * [num_blocks] int32 is a stack of *num_free ids.
+ *  - first the blocks of finished requests are pushed, by request, in table order; then the blocks
+ *    that the new tokens need are popped, by request, in position order (the ids that
+ *    pa_seq_release and pa_seq_append give in that order);
+ *  - block_tables [num_seqs, max_blocks_per_seq] receives the new blocks' entries, nothing else;
+ *  - context_lens_out [num_seqs] and num_free_out [1] receive the new lengths (0: finished) and
+ *    count; they may be context_lens and num_free;
+ *  - q_offsets [num_seqs + 1] receives the first row of each request's new tokens; positions and
+ *    slot_mapping [num_tokens] their positions and slots, by request; rows past the last new token
+ *    get position 0 and slot -1, so num_tokens may be an upper bound (a captured step).
+ * All arrays are device memory.  A step that cannot be done is refused as a whole: tables, lengths
+ * and count stay as they are, there are no new tokens (offsets 0, slots -1; the stack above its
+ * count may have been written), and the device error word says why: PA_ERR_POOL_EXHAUSTED;
+ * PA_ERR_BAD_CONTEXT (a negative length, one past max_blocks_per_seq * block_size, more than
+ * num_tokens new tokens); PA_ERR_BAD_TABLE (an id outside [0, num_blocks) in a table or on the
+ * stack, a count outside it).  num_seqs <= PA_MAX_STEP_SEQS.
+ */
+#define PA_MAX_STEP_SEQS 8192
+int pa_advance_tables(int32_t* block_tables, const int32_t* context_lens, const int32_t* new_lens, int32_t* free_blocks,
+                      const int32_t* num_free, int32_t* context_lens_out, int32_t* num_free_out, int32_t* q_offsets,
+                      int32_t* positions, int64_t* slot_mapping, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                      int block_size, int num_tokens, void* stream);
+
+/*
+ * pa_rope_write_kv — rotary positions of queries and keys, and pa_write_kv of the rotated keys and
+ * the values, in one launch.  For token t at position p = positions[t] (int32, any sign), pair
+ * i < rotary_dim / 2 of every query and key head, elements (i, i + rotary_dim / 2) (PA_ROPE_HALF) or
+ * (2i, 2i + 1) (PA_ROPE_INTERLEAVED), is turned by p * inv_freq[i]:
+ *     (x, y) -> factor * (x cos - y sin, x sin + y cos);
+ * elements at and past rotary_dim pass unchanged.  float32 arithmetic, one rounding to dtype; the
+ * angle is exact to 2^-32 turns for every position (inv_freq: device float64 [rotary_dim / 2]).
+ *  query      [num_tokens, num_heads, head_dim], key and value [num_tokens, num_kv_heads, head_dim]:
+ *             heads of a token contiguous, q_stride, k_stride and v_stride elements from token to
+ *             token (the views that a joint projection leaves).
+ *  query_out  contiguous [num_tokens, num_heads, head_dim]; may be query when that is contiguous.
+ *  slot_mapping, caches, dtype, errors: as pa_write_kv.  A row whose slot is negative still has its
+ *  query rotated.  head_dim even, at most 512; rotary_dim even, at most head_dim.
+ */
+enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 };
+int pa_rope_write_kv(void* query_out, const void* query, const void* key, const void* value, void* key_cache,
+                     void* value_cache, const double* inv_freq, const int32_t* positions, const int64_t* slot_mapping,
+                     int64_t q_stride, int64_t k_stride, int64_t v_stride, int num_tokens, int num_heads, int num_kv_heads,
+                     int head_dim, int rotary_dim, int layout, float factor, int block_size, int num_blocks, int dtype,
+                     void* stream);
+
+/*
+ * pa_rope_append_fp8 — the same into an FP8 cache, with block scales that follow the data.  The
+ * new tokens are given by request: rows q_offsets[b] .. q_offsets[b + 1] - 1 are the last positions
+ * of the context_lens[b] tokens of request b (the new ones included), in the blocks of its row of
+ * block_tables (what pa_advance_tables leaves).  For every block and kv head that new rows fall
+ * into, K and V each on their own, with a = the largest finite magnitude among those rows (K after
+ * its rotation, in float32):
+ *  - the block's offset 0 is among them: scale = max(a / 448, 2^-100);
+ *  - else scale = max(held scale, a / 448); if that is larger, the codes before the new rows are
+ *    brought to it: e4m3(code * held / scale);
+ *  - the new rows are stored as e4m3(x / scale): round to nearest even, magnitudes above 448
+ *    (infinities) saturating, NaN staying NaN.
+ * k_scale, v_scale and value_cache as pa_decode_fp8 (NULL value_cache: K and V records).  Rows
+ * behind q_offsets[num_seqs] are neither read nor written.  A block that takes new rows must belong
+ * to one request.  dtype PA_F32, PA_F16 or PA_BF16; rotary_dim 0: no rotation (inv_freq may be
+ * NULL).  Compiled for head_dim 64 and 128, block_size 16 and 32, rotary_dim a multiple of 4
+ * (PA_ERR_UNSUPPORTED otherwise).  A block id outside the pool skips its rows and sets
+ * PA_ERR_BAD_TABLE, a length outside its table or below its new rows those of the request and sets
+ * PA_ERR_BAD_CONTEXT, in the device error word.
+ */
+int pa_rope_append_fp8(void* query_out, const void* query, const void* key, const void* value, void* key_cache,
+                       void* value_cache, float* k_scale, float* v_scale, const double* inv_freq,
+                       const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_offsets,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, int num_seqs, int num_tokens, int num_heads,
+                       int num_kv_heads, int head_dim, int rotary_dim, int layout, float factor, int block_size,
+                       int max_blocks_per_seq, int num_blocks, int dtype, void* stream);
+
+/*
+ * pa_attend_fp8 — causal attention of ragged runs of new tokens over an FP8 cache: prompt chunks,
+ * verification and decode steps in one call.  Request b has n_b = q_offsets[b + 1] - q_offsets[b]
+ * rows of query [num_tokens, num_heads, head_dim], the last n_b of its context_lens[b] positions
+ * (their K and V are in the cache already); the row at position p attends positions 0 .. p, as
+ * pa_decode_multi.  n_b may be 0, and differ from request to request; a row before position 0 gets
+ * zeros; rows behind q_offsets[num_seqs] are left as they were.  Codes, scales and layouts as
+ * pa_decode_fp8; query and out f16 or bf16, contiguous, 16-byte aligned.  Scores, softmax and sums
+ * are float32.  Compiled for head_dim 64 and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED
+ * otherwise).  A block id outside the pool reads as masked positions and sets PA_ERR_BAD_TABLE, a length
+ * outside its table is clamped and sets PA_ERR_BAD_CONTEXT, in the device error word.
+ *  workspace  pa_attend_fp8_workspace_size() bytes, 256-byte aligned, no initialisation; calls that
+ *             share one must not overlap on the GPU.
+ */
+int pa_attend_fp8(void* out, const void* query, const void* key_cache, const void* value_cache, const float* k_scale,
+                  const float* v_scale, const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_offsets,
+                  int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                  int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                  void* stream);
+size_t pa_attend_fp8_workspace_size(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int max_blocks_per_seq, int dtype);
 
 /* ---- host block pool ----------------------------------------------------------------- */
 /*

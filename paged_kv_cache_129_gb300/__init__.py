@@ -36,6 +36,15 @@ from .binding import (  # noqa: F401
 
 
 from .step import DecodeStepper  # noqa: F401,E402
+from .step_ops import (  # noqa: F401,E402
+    TableStep,
+    advance_tables,
+    attend_fp8,
+    attend_fp8_workspace_size,
+    rope_append_fp8,
+    rope_frequencies,
+    rope_write_kv,
+)
 
 
 def build(force: bool = False) -> str:

@@ -96,6 +96,11 @@ _SIGNATURES = [
     ("pa_decode_static_scratch", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     ("pa_diag_force_restart", None, [_I]),
     ("pa_diag_merge_timeout", _I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, ctypes.c_ulonglong, _P]),
+    ("pa_advance_tables", _I, [_P] * 10 + [_I] * 5 + [_P]),
+    ("pa_rope_write_kv", _I, [_P] * 9 + [_I64] * 3 + [_I] * 6 + [_F] + [_I] * 3 + [_P]),
+    ("pa_rope_append_fp8", _I, [_P] * 12 + [_I64] * 3 + [_I] * 7 + [_F] + [_I] * 4 + [_P]),
+    ("pa_attend_fp8", _I, [_P] * 9 + [_I] * 8 + [_F, _I, _P, _SZ, _P]),
+    ("pa_attend_fp8_workspace_size", _SZ, [_I] * 8),
     ("pa_stepper_create", _I, [_I, _P, _P, _P, ctypes.POINTER(_P)]),
     ("pa_stepper_destroy", None, [_P]),
     ("pa_stepper_set_slot", _I, [_P, _I, _P, _P, _SZ, _P, _P, _SZ]),

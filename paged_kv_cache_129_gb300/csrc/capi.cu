@@ -411,6 +411,16 @@ int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int b
 }
 
 }  // namespace
+
+int device_state(unsigned** error_word, int* num_sms) {
+    DeviceState* dev = nullptr;
+    const int st = current_device_state(&dev);
+    if (st != PA_OK) return st;
+    *error_word = dev->error_word;
+    *num_sms = dev->num_sms;
+    return PA_OK;
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -439,6 +449,8 @@ int pa_check_error(void* stream) {
     if (word & kErrBadSlot) return fail(PA_ERR_BAD_SLOT, "a kernel met a slot past the pool (word 0x%x)", word);
     if (word & kErrBadContext)
         return fail(PA_ERR_BAD_CONTEXT, "a context length was negative or longer than its table (word 0x%x)", word);
+    if (word & kErrPoolExhausted)
+        return fail(PA_ERR_POOL_EXHAUSTED, "a step needed more free blocks than the stack holds (word 0x%x)", word);
     return fail(PA_ERR_TIMEOUT, "a kernel-internal wait gave up (word 0x%x)", word);
 }
 

@@ -17,6 +17,7 @@ enum : unsigned {
     kErrBadSlot = 2u,
     kErrBadContext = 4u,
     kErrTimeout = 8u,
+    kErrPoolExhausted = 16u,
 };
 
 // A wait on a shared-memory barrier gives up after this many nanoseconds
