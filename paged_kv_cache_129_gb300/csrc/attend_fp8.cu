@@ -1,7 +1,23 @@
-// Causal attention of ragged runs of new tokens over an FP8 (E4M3) paged cache.
+// Causal attention of ragged runs of new tokens over an FP8 (E4M3) paged cache, on tcgen05 tensor cores.
 //
 // Request b has the rows q_offsets[b] .. q_offsets[b + 1] - 1, the last n_b positions of its L_b; the row at
 // position p attends positions 0 .. p:  out = sum softmax(scale q k_j) v_j, with k_j, v_j = code * scale(block, head).
+//
+// Rows.  The g query heads of a kv head and the request's tokens form R = n_b * g rows (row v: token v / g, head
+// v % g), cut into tiles of 128, the M of the products; keys come in tiles of 128 tokens.  A CTA has two streams of
+// softmax warps, so that one's exponentials run under the other's products:
+//   paired  two row tiles share every key tile (it is widened once for both);
+//   split   a single row tile (few rows: verification, decode, the rest of a run): the streams take alternate key
+//           tiles and are joined in shared memory.
+// Work.  A unit is (request, pair of row tiles, kv head).  All units' key tiles are laid end to end, weighted by their
+// cost, and cut into one equal contiguous share per SM, so every SM works equally long whatever the length mix; units cut by a
+// share boundary leave float32 partial results (two slots per CTA), joined by a third kernel.
+// Numbers.  E4M3 codes widen to f16 exactly; a query row is moved into f16 range by a power of two (f16 queries as they
+// are), undone in the score factor.  A block's K scale multiplies its scores; its V scale multiplies P, relative to a power of
+// two near the largest seen, so that P stays in f16 range.  Scores, maxima, sums and the output accumulate in float32;
+// P alone is rounded to f16 (half a step 2^-11, below the half step 2^-9 of a bf16 output).  The maximum that exponents are
+// taken from follows the true one by steps of 2^8 at least: rescaling the output in tensor memory is rare that way.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_fp8.h>
@@ -13,74 +29,941 @@ namespace pa {
 
 namespace {
 
-// A warp per (token, query head): the running maximum and sum in float32, D / 32 elements of the head per lane.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_fp8_kernel(const AttendArgs a) {
+constexpr int kTile = 128;             // rows of a row tile, tokens of a key tile
+constexpr int kSoftmaxWarps = 8;       // four per stream
+constexpr int kLoadWarps = 4;
+constexpr int kThreads = (kSoftmaxWarps + kLoadWarps + 1) * 32;
+constexpr int kRing = 4;               // slots of per-tile side data (scales), see load_tiles()
+// Cost of a key tile in shares: a pair does twice the products and exponentials of a split tile, but loads and widens it once.
+constexpr int kPairedCost = 4, kSplitCost = 3;
+constexpr int kMinShare = 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
+
+// ---- work list (made by plan_kernel) ------------------------------------------------------------
+
+struct Entry {
+    long long first;  // cost before this entry
+    int seq, row0;    // request, first row
+    int tiles;        // key tiles, >= 1
+    int paired;
+};
+static_assert(sizeof(Entry) == 24, "packed");
+
+struct PlanHead {
+    long long cost;
+    int entries, pad;
+};
+
+struct Workspace {
+    PlanHead* head;
+    Entry* entries;   // [max_entries + 1], the last one a sentinel
+    float* records;   // [CTAs][2 slots][2 tiles][m 128 | l 128 | o 128 x D]
+};
+
+__host__ __device__ inline size_t record_floats(int D) { return (size_t)kTile * (D + 2); }
+inline size_t max_entries(int num_seqs, int num_tokens, int group) {
+    return (size_t)num_seqs + ((size_t)num_tokens * group) / (2 * kTile);
+}
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// ---- PTX ------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, int columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst_smem)), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, int columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+// 32 columns of this warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 load_stream(const void* p) {  // read once: keep it out of L1
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Operand tiles in shared memory: panels of 64 elements (128 bytes) by 128 rows, 128-byte swizzle (16-byte unit u of row r
+// at u ^ (r % 8)), 16 KB apart.  Descriptors: bits 0-13 address / 16, 16-29 and 32-45 byte offsets / 16, 46 version 1,
+// 61-63 the 128-byte swizzle (2).
+constexpr uint32_t kPanel = kTile * 128;
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t leading, uint32_t stride) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: f16 x f16 -> f32; bit 16: B is given with N contiguous (V: [token][d]).
+constexpr uint32_t idesc_of(int n, bool b_n_major) {
+    return (1u << 4) | ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+// ---- the plan ------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ int clamped_length(const AttendArgs& a, int b) {
+    return max(0, min(a.context_lens[b], a.max_blocks * a.block_size));
+}
+__device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {  // request b's new tokens
+    const int lo = max(0, a.q_offsets[b]), hi = min(a.num_tokens, a.q_offsets[b + 1]);
+    return max(0, hi - lo);
+}
+
+// Key tiles of rows row0 .. row0 + 255 of a request: up to the last row's position.
+__device__ __forceinline__ int tiles_of(int L, int n, int group, int row0) {
+    const int last = min(n * group, row0 + 2 * kTile) - 1;
+    const int bound = L - n + last / group;
+    return max(1, (bound + kTile) / kTile);
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive sum of x over the CTA; *total the whole.  scratch: 33 entries.
+__device__ __forceinline__ long long block_scan(long long x, long long* scratch, long long* total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    long long s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[wid] = s;
+    __syncthreads();
+    if (wid == 0) {
+        long long w = scratch[lane], t = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += y;
+        }
+        scratch[lane] = t - w;
+        if (lane == 31) scratch[32] = t;
+    }
+    __syncthreads();
+    *total = scratch[32];
+    return scratch[wid] + s - x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendArgs a, const Workspace ws, int entry_cap) {
+    extern __shared__ int first_entry[];  // [num_seqs + 1]
+    __shared__ long long scratch[33];
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (w >= (long long)a.num_tokens * a.num_heads) return;
-    const int t = (int)(w / a.num_heads), qh = (int)(w - (long long)t * a.num_heads);
-    int lo = -1, hi = a.num_seqs + 1;  // off[lo] <= t < off[hi]
+    const int group = a.num_heads / a.num_kv_heads, tid = threadIdx.x;
+    long long base = 0, total = 0;
+    for (int b0 = 0; b0 < a.num_seqs; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        long long n = 0;
+        if (b < a.num_seqs) {
+            const int L = a.context_lens[b];
+            if (L < 0 || L > a.max_blocks * a.block_size) atomicOr(a.err, kErrBadContext);
+            n = ((long long)rows_of(a, b) * group + 2 * kTile - 1) / (2 * kTile);
+        }
+        const long long at = base + block_scan(n, scratch, &total);
+        if (b < a.num_seqs) first_entry[b] = (int)min(at, (long long)entry_cap);
+        base += total;
+    }
+    int entries = (int)min(base, (long long)entry_cap);
+    if (base > entry_cap) {  // offsets that do not ascend
+        if (tid == 0) atomicOr(a.err, kErrBadContext);
+        entries = 0;
+    }
+    if (tid == 0) first_entry[a.num_seqs] = entries;
+    __syncthreads();
+    long long cost = 0;
+    for (int e0 = 0; e0 < entries; e0 += kPlanThreads) {
+        const int e = e0 + tid;
+        Entry x{};
+        long long c = 0;
+        if (e < entries) {
+            int lo = 0, hi = a.num_seqs;  // the last request whose first entry is <= e: one with rows
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first_entry[mid] <= e)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            const int n = rows_of(a, lo);
+            x.seq = lo;
+            x.row0 = (e - first_entry[lo]) * 2 * kTile;
+            x.paired = n * group - x.row0 > kTile;
+            x.tiles = tiles_of(clamped_length(a, lo), n, group, x.row0);
+            c = (long long)x.tiles * (x.paired ? kPairedCost : kSplitCost) * a.num_kv_heads;
+        }
+        x.first = cost + block_scan(c, scratch, &total);
+        cost += total;
+        if (e < entries) ws.entries[e] = x;
+    }
+    if (tid == 0) {
+        ws.entries[entries].first = cost;
+        ws.head->cost = cost;
+        ws.head->entries = entries;
+    }
+}
+
+__device__ __forceinline__ long long share_of(long long cost, int ctas) {
+    const long long s = (cost + ctas - 1) / ctas;
+    return s > kMinShare ? s : kMinShare;
+}
+
+// The entry that cost position x falls into; whole CTA or warp, any number of threads.
+__device__ __forceinline__ int find_entry(const Entry* e, int n, long long x) {
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.q_offsets[mid] <= t)
+        if (e[mid].first <= x)
             lo = mid;
         else
             hi = mid;
     }
-    if (lo < 0 || lo >= a.num_seqs) return;  // behind the last request
-    const int kvh = qh / (a.num_heads / a.num_kv_heads), bs = a.block_size;
-    int L = a.context_lens[lo];
-    if (L < 0 || L > a.max_blocks * bs) {
-        if (lane == 0) atomicOr(a.err, kErrBadContext);
-        L = max(0, min(L, a.max_blocks * bs));
-    }
-    const int seen = L - (a.q_offsets[lo + 1] - t) + 1;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        q[i] = to_float(static_cast<const T*>(a.query)[((size_t)t * a.num_heads + qh) * D + lane * E + i]) * a.scale;
-        o[i] = 0.f;
-    }
-    const bool both = a.value_cache == nullptr;
-    for (int p = 0; p < seen; ++p) {
-        const int blk = a.block_tables[(size_t)lo * a.max_blocks + p / bs];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) atomicOr(a.err, kErrBadTable);
-            continue;
+    return lo;
+}
+
+// The part of one unit that a share covers: key tiles [begin, end) of `tiles`.
+struct Piece {
+    int seq, row0, kvh, tiles, begin, end;
+    bool paired;
+};
+
+// Walks over the pieces of share [pos, stop) of the plan.
+struct Walk {
+    const Entry* entries;
+    int count, heads, e, kvh;
+    long long pos, stop;
+    __device__ __forceinline__ Walk(const Workspace& ws, int heads_, int cta, int ctas) : entries(ws.entries), heads(heads_) {
+        const long long cost = ws.head->cost, share = share_of(cost, ctas);
+        count = ws.head->entries;
+        pos = share * cta;
+        stop = min(pos + share, cost);
+        e = kvh = 0;
+        if (pos < stop) {
+            e = find_entry(entries, count, pos);
+            const Entry x = entries[e];
+            kvh = (int)((pos - x.first) / ((long long)x.tiles * (x.paired ? kPairedCost : kSplitCost)));
         }
-        const size_t si = (size_t)blk * a.num_kv_heads + kvh;
-        const uint8_t* k = a.key_cache + ((both ? 2 * si : si) * bs + p % bs) * D + lane * E;
-        const uint8_t* v = both ? k + (size_t)bs * D : a.value_cache + (si * bs + p % bs) * D + lane * E;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s += q[i] * __half2float(__half(__nv_cvt_fp8_to_halfraw(k[i], __NV_E4M3)));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.k_scale[si];
-        const float mn = fmaxf(m, s), f = __expf(m - mn), e = __expf(s - mn), ev = e * a.v_scale[si];
-        m = mn;
-        l = l * f + e;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = o[i] * f + ev * __half2float(__half(__nv_cvt_fp8_to_halfraw(v[i], __NV_E4M3)));
     }
+    __device__ __forceinline__ bool next(Piece* p) {
+        while (pos < stop) {
+            const Entry x = entries[e];
+            const int w = x.paired ? kPairedCost : kSplitCost;
+            const long long unit = x.first + (long long)kvh * x.tiles * w;
+            const long long from = pos > unit ? pos - unit : 0, to = stop - unit;
+            p->seq = x.seq;
+            p->row0 = x.row0;
+            p->kvh = kvh;
+            p->tiles = x.tiles;
+            p->paired = x.paired != 0;
+            p->begin = (int)((from + w - 1) / w);
+            p->end = (int)min((long long)x.tiles, (to + w - 1) / w);
+            pos = unit + (long long)x.tiles * w;
+            if (++kvh == heads) {
+                kvh = 0;
+                ++e;
+            }
+            if (p->begin < p->end) return true;
+        }
+        return false;
+    }
+};
+
+// ---- shared memory of the attention kernel -----------------------------------------------------------------
+
+template <int D>
+struct Smem {
+    static constexpr int kOperand = kTile * D * 2;  // one f16 tile
+    unsigned char q[2][kOperand];  // at the end of a split piece: stream 1's output
+    unsigned char k[2][kOperand];
+    unsigned char v[2][kOperand];
+    float ks[kRing][8], vs[kRing][8];        // scales of the tile's blocks
+    unsigned masked_blocks[kRing];           // blocks of the tile whose id is outside the pool
+    unsigned nan_any[kRing][kLoadWarps];     // whether a load warp found NaN in V of a tile that some row sees in part,
+    uint16_t nan_at[kRing][kTile][D / 16];   // and where: per token and 16 elements
+    float m1[kTile], l1[kTile];              // stream 1's state at the end of a split piece
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], x_full, x_empty, drain;
+    uint32_t tmem;
+    volatile int abort;
+};
+
+// mbar_wait_bounded by a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, abort));
+}
+
+// What a piece is to every role.
+struct Item {
+    int L, n, group, rows;  // length, new tokens, heads per kv head, rows of the request
+    int first_token;        // row of the request's first new token in query / out
+    int jobs;               // score tiles: two streams take them in turn
+};
+__device__ __forceinline__ Item item_of(const AttendArgs& a, const Piece& p) {
+    Item it;
+    it.L = clamped_length(a, p.seq);
+    it.n = rows_of(a, p.seq);
+    it.group = a.num_heads / a.num_kv_heads;
+    it.rows = it.n * it.group;
+    it.first_token = max(0, a.q_offsets[p.seq]);
+    it.jobs = (p.end - p.begin) * (p.paired ? 2 : 1);
+    return it;
+}
+
+// Sixteen E4M3 codes as f16 (exact), to units u and u + 1 of a swizzled row.
+__device__ __forceinline__ void widen_store(unsigned char* row, int u, int r7, uint4 c, bool odd_first) {
+    uint32_t h[8];
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-        static_cast<T*>(a.out)[((size_t)t * a.num_heads + qh) * D + lane * E + i] = from_float<T>(l == 0.f ? 0.f : o[i] / l);
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] & 0xffffu), __NV_E4M3);
+        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> 16), __NV_E4M3);
+        h[2 * i] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
+        h[2 * i + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+    }
+    const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+    // The lanes of a row hold chunks of two panels, whose banks coincide: one half stores its odd unit first.
+    *reinterpret_cast<uint4*>(row + (((odd_first ? u + 1 : u) ^ r7) << 4)) = odd_first ? b : a;
+    *reinterpret_cast<uint4*>(row + (((odd_first ? u : u + 1) ^ r7) << 4)) = odd_first ? a : b;
+}
+
+// Per byte of w: 0x80 where the code is NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// The four load warps: widen key tile after key tile into the two K and two V stages.  Codes are on their way in registers
+// while the previous tile's are widened (V of a tile under K's stores, the next K under V's).
+// Side data of tile i sits in ring slot i % 4 and is read by the softmax of tile i, which ends before V stage i % 2 is
+// free again; slot i % 4 is written again with tile i + 4, after V of tile i + 3 has been stored, so after that.
+template <int D>
+__device__ __forceinline__ void load_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    constexpr int CPR = D / 16, RPP = 128 / CPR, N = kTile / RPP;  // chunks per row, rows per pass, passes
+    const int tid = threadIdx.x - kSoftmaxWarps * 32, lane = tid & 31;
+    const int chunk = tid % CPR, row0 = tid / CPR;
+    const int bs = a.block_size, shift = bs == 16 ? 4 : 5, pages = kTile >> shift;
+    const bool both = a.value_cache == nullptr;
+    volatile int* abort = &sm.abort;
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned count = 0;  // tiles so far
+    const bool odd_first = chunk >= 4;
+    const uint32_t panel = (chunk / 4) * kPanel;
+    const int u = (chunk % 4) * 2;
+    while (walk.next(&p)) {
+        const Item it = item_of(a, p);
+        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
+        const int used = (it.L + bs - 1) >> shift;
+        const int seen_by_all = it.L - it.n + p.row0 / it.group;  // the first row's position
+        // block of page `lane` of a tile: -1 none, -2 an id outside the pool
+        auto block_of = [&](int tile) {
+            int id = -1;
+            const int page = tile * pages + lane;
+            if (lane < pages && page < used && tile < p.end) {
+                id = table[page];
+                if (id < 0 || id >= a.num_blocks) {
+                    atomicOr(a.err, kErrBadTable);
+                    id = -2;
+                }
+            }
+            return id;
+        };
+        auto load = [&](uint4 (&raw)[N], int ids, int tile, bool value) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = row0 + i * RPP, id = __shfl_sync(0xffffffffu, ids, r >> shift);
+                raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (id >= 0 && tile * kTile + r < it.L) {
+                    const size_t rec = (size_t)id * a.num_kv_heads + p.kvh;
+                    const size_t at = both ? (2 * rec + (value ? 1 : 0)) * bs : rec * bs;
+                    const uint8_t* base = value && !both ? a.value_cache : a.key_cache;
+                    raw[i] = load_stream(base + (at + (r & (bs - 1))) * D + chunk * 16);
+                }
+            }
+        };
+        auto scales_of = [&](int id, float* ks, float* vs) {  // the first load warp has them, a block per lane
+            *ks = *vs = 0.f;
+            if (tid < 32 && id >= 0) {
+                const size_t si = (size_t)id * a.num_kv_heads + p.kvh;
+                *ks = a.k_scale[si];
+                *vs = a.v_scale[si];
+            }
+        };
+        uint4 kr[N], vr[N];
+        float ks, vs;
+        int ids = block_of(p.begin);
+        load(kr, ids, p.begin, false);
+        scales_of(ids, &ks, &vs);
+        for (int tile = p.begin; tile < p.end; ++tile, ++count) {
+            const int stage = count & 1, slot = count % kRing;
+            const unsigned parity = (count >> 1) & 1;
+            const int next_ids = block_of(tile + 1);
+            load(vr, ids, tile, true);
+            if (tid < 32) {
+                const unsigned masked = __ballot_sync(0xffffffffu, ids == -2);
+                if (lane < 8) {
+                    sm.ks[slot][lane] = ks;
+                    sm.vs[slot][lane] = vs;
+                }
+                if (lane == 0) sm.masked_blocks[slot] = masked;
+            }
+            if (!warp_wait(&sm.k_empty[stage], parity ^ 1, a.err, abort)) return;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = row0 + i * RPP;
+                widen_store(sm.k[stage] + panel + r * 128, u, r & 7, kr[i], odd_first);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.k_full[stage]);
+            if (tile + 1 < p.end) load(kr, next_ids, tile + 1, false);
+            scales_of(next_ids, &ks, &vs);
+            if (!warp_wait(&sm.v_empty[stage], parity ^ 1, a.err, abort)) return;
+            bool any = false;
+            if (tile * kTile + kTile - 1 > seen_by_all) {
+                // Some row sees this tile in part: a NaN behind its position must not reach it through 0 * NaN.
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&vr[i]);
+                    unsigned at = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t t = nan_bytes(w[k]);
+                        at |= (((t >> 7) * 0x01020408u >> 24) & 0xfu) << (4 * k);
+                        w[k] &= ~((t >> 7) * 0xffu);
+                    }
+                    any |= at != 0;
+                    sm.nan_at[slot][row0 + i * RPP][chunk] = (uint16_t)at;
+                }
+            }
+            any = __any_sync(0xffffffffu, any);
+            if (lane == 0) sm.nan_any[slot][tid >> 5] = any;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = row0 + i * RPP;
+                widen_store(sm.v[stage] + panel + r * 128, u, r & 7, vr[i], odd_first);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.v_full[stage]);
+            ids = next_ids;
+        }
+    }
+}
+
+// One thread issues every product.  Job j of a piece is a score tile of stream j % 2; its scores are issued two jobs ahead of
+// its output, right behind the output of the stream's previous job, which has then read the P that the scores overwrite.
+template <int D>
+__device__ __forceinline__ void issue_products(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    volatile int* abort = &sm.abort;
+    const uint32_t tmem = sm.tmem;
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned tiles = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};
+    while (walk.next(&p)) {
+        const int jobs = (p.end - p.begin) * (p.paired ? 2 : 1);
+        auto scores = [&](int j) {
+            const int t = j & 1;
+            const unsigned tile = tiles + (p.paired ? j >> 1 : j), stage = tile & 1;
+            if (!mbar_wait_bounded(&sm.k_full[stage], (tile >> 1) & 1, a.err, abort)) return false;
+            if (j < 2 && !mbar_wait_bounded(&sm.q_full[t], pieces[t] & 1, a.err, abort)) return false;
+            tc_fence_after();
+            const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.k[stage]), 16, 1024);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
+                mma_ss(tmem + t * kTile, qd + off, kd + off, idesc_of(kTile, false), k > 0);
+            }
+            if (!p.paired || t == 1) tc_commit(&sm.k_empty[stage]);
+            tc_commit(&sm.s_full[t]);
+            return true;
+        };
+        for (int j = 0; j < min(jobs, 2); ++j)
+            if (!scores(j)) return;
+        for (int j = 0; j < jobs; ++j) {
+            const int t = j & 1;
+            const unsigned tile = tiles + (p.paired ? j >> 1 : j), stage = tile & 1;
+            if (!mbar_wait_bounded(&sm.v_full[stage], (tile >> 1) & 1, a.err, abort)) return;
+            if (!mbar_wait_bounded(&sm.p_full[t], steps[t]++ & 1, a.err, abort)) return;
+            tc_fence_after();
+            const uint64_t vd = desc_of(smem_addr(sm.v[stage]), kPanel, 1024);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
+            if (!p.paired || t == 1) tc_commit(&sm.v_empty[stage]);
+            if (j + 2 >= jobs) tc_commit(&sm.o_full[t]);
+            if (j + 2 < jobs && !scores(j + 2)) return;
+        }
+        tiles += p.end - p.begin;
+        ++pieces[0];
+        if (jobs > 1) ++pieces[1];
+    }
+}
+
+// A softmax warp: 32 rows of a stream's row tile, one per lane.
+template <typename T, int D>
+__device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
+    volatile int* abort = &sm.abort;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = sm.tmem + lanes + t * kTile, o_at = sm.tmem + lanes + 2 * kTile + t * D;
+    const int shift = a.block_size == 16 ? 4 : 5;
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned pieces = 0, steps = 0, splits = 0, tiles_before = 0;
+    while (walk.next(&p)) {
+        const Item it = item_of(a, p);
+        const int v = p.row0 + (p.paired ? t * kTile : 0) + r;  // row of the request
+        const bool live = v < it.rows;
+        const bool warp_live = p.row0 + (p.paired ? t * kTile : 0) + (warp & 3) * 32 < it.rows;
+        const int token = live ? v / it.group : 0;
+        const int bound = live ? it.L - it.n + token : -1;  // last position that the row sees
+        const size_t row_at = ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D;
+        const int my_jobs = (it.jobs + 1 - t) / 2;
+        if (p.paired || my_jobs > 0) {
+            // the query row to f16
+            uint4 raw[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                raw[i] = live ? *reinterpret_cast<const uint4*>(static_cast<const T*>(a.query) + row_at + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+            float mul = a.scale < 0.f ? -1.f : 1.f;
+            int e = 0;
+            if (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    float x[8];
+                    unpack16<T>(raw[i], x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[k]));
+                }
+                if (most > 0.f && most <= 3.402823466e38f) {
+                    int ex;
+                    frexpf(most, &ex);  // most = f * 2^ex, f in [0.5, 1): the row's largest goes to [2^14, 2^15)
+                    e = min(max(15 - ex, -126), 126);
+                }
+                mul *= __int_as_float((e + 127) << 23);
+            }
+            unsigned char* dst = sm.q[t] + r * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                float x[8];
+                unpack16<T>(raw[i], x);
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 y = __floats2half2_rn(x[2 * k] * mul, x[2 * k + 1] * mul);
+                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                *reinterpret_cast<uint4*>(dst + (i / 8) * kPanel + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.q_full[t]);
+            const float qf = fabsf(a.scale) * 1.4426950408889634f * __int_as_float((127 - e) << 23);
+
+            float m = -INFINITY, l = 0.f, vref = 0.f;
+            uint32_t nan_cols[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) nan_cols[i] = 0;
+            for (int step = 0; step < my_jobs; ++step, ++steps) {
+                const int local = p.paired ? step : 2 * step + t;
+                const unsigned count = tiles_before + local;
+                const int p0 = (p.begin + local) * kTile, slot = count % kRing;
+                if (!warp_wait(&sm.s_full[t], steps & 1, a.err, abort)) return;
+                tc_fence_after();
+                if (warp_live) {
+                    const unsigned masked_blocks = sm.masked_blocks[slot];
+                    const bool whole = __all_sync(0xffffffffu, !live || p0 + kTile - 1 <= bound) && masked_blocks == 0;
+                    // columns of the tile that the row sees
+                    const int cols = min(kTile, bound - p0 + 1);
+                    float top = -INFINITY;
+                    uint32_t s[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(s_at + 32 * c, s);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int hb = 0; hb < 2; ++hb) {
+                            const int blk = (32 * c + 16 * hb) >> shift;
+                            float x = -INFINITY;
+                            if (whole) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) x = fmaxf(x, __uint_as_float(s[16 * hb + k]));
+                            } else if (!(masked_blocks >> blk & 1)) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    x = fmaxf(x, 32 * c + 16 * hb + k < cols ? __uint_as_float(s[16 * hb + k]) : -INFINITY);
+                            }
+                            if (x != -INFINITY) top = fmaxf(top, x * (sm.ks[slot][blk] * qf));
+                        }
+                    }
+                    // the power of two that P's V scales are relative to
+                    float vmax = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) vmax = fmaxf(vmax, sm.vs[slot][k]);
+                    const float v2 = __int_as_float(__float_as_int(fmaxf(vmax, 7.888609052210118e-31f)) & 0x7f800000);
+                    const float vnew = fmaxf(vref, v2);
+                    const bool rescale = step > 0 && (vnew > vref || top > m + 8.f);
+                    if (step == 0) {
+                        m = top;
+                        vref = vnew;
+                    } else if (__any_sync(0xffffffffu, rescale)) {
+                        const float mn = fmaxf(m, top);
+                        const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                        const float of = f * (vref / vnew);
+                        l *= f;
+                        m = mn;
+                        vref = vnew;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            tmem_ld32(o_at + 32 * c, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * of);
+                            tmem_st32(o_at + 32 * c, s);
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float vinv = __int_as_float(0x7f000000 - __float_as_int(vref));  // 1 / vref, a power of two
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(s_at + 32 * c, s);
+                        tc_wait_ld();
+                        uint32_t out[16];
+#pragma unroll
+                        for (int hb = 0; hb < 2; ++hb) {
+                            const int blk = (32 * c + 16 * hb) >> shift;
+                            const float kf = sm.ks[slot][blk] * qf, vf = sm.vs[slot][blk] * vinv;
+                            const bool gone = masked_blocks >> blk & 1;
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                float x0 = fmaf(__uint_as_float(s[16 * hb + k]), kf, -mu);
+                                float x1 = fmaf(__uint_as_float(s[16 * hb + k + 1]), kf, -mu);
+                                if (!whole) {
+                                    if (gone || 32 * c + 16 * hb + k >= cols) x0 = -INFINITY;
+                                    if (gone || 32 * c + 16 * hb + k + 1 >= cols) x1 = -INFINITY;
+                                }
+                                const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
+                                l += e0 + e1;
+                                const __half2 h = __floats2half2_rn(e0 * vf, e1 * vf);
+                                out[8 * hb + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                        }
+                        tmem_st16(s_at + 16 * c, out);
+                    }
+                    if (!whole) {
+                        if (!warp_wait(&sm.v_full[count & 1], (count >> 1) & 1, a.err, abort)) return;
+                        if (sm.nan_any[slot][0] | sm.nan_any[slot][1] | sm.nan_any[slot][2] | sm.nan_any[slot][3]) {
+                            for (int k = 0; k < cols; ++k)
+                                if (!(masked_blocks >> (k >> shift) & 1))
+#pragma unroll
+                                    for (int i = 0; i < D / 32; ++i)
+                                        nan_cols[i] |= (uint32_t)sm.nan_at[slot][k][2 * i] | ((uint32_t)sm.nan_at[slot][k][2 * i + 1] << 16);
+                        }
+                    }
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[t]);
+            }
+
+            // the piece's result
+            if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+            tc_fence_after();
+            ++pieces;
+            const bool cut = p.begin > 0 || p.end < p.tiles;
+            float* rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
+            float a0 = 1.f, a1 = 0.f;  // weights of this stream's and stream 1's outputs
+            bool joined = false;
+            if (!p.paired && it.jobs > 1) {
+                // both streams have a part of the same rows: stream 1 leaves its own in the query tiles, which are done with
+                float4* x = reinterpret_cast<float4*>(&sm.q[0][0]);
+                if (t == 1) {
+                    // stream 0's last scores must be done with the tiles as well: its output is issued after them
+                    if (!warp_wait(&sm.x_empty, splits & 1, a.err, abort)) return;
+                    if (warp_live) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t s[32];
+                            tmem_ld32(o_at + 32 * c, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                float4 y;
+                                float* yf = reinterpret_cast<float*>(&y);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    yf[i] = (nan_cols[c] >> (4 * k + i) & 1) ? __int_as_float(0x7fc00000) : __uint_as_float(s[4 * k + i]) * vref;
+                                x[(8 * c + k) * kTile + r] = y;
+                            }
+                        }
+                        sm.m1[r] = m;
+                        sm.l1[r] = l;
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&sm.x_full);
+                    ++splits;
+                    tiles_before += p.end - p.begin;
+                    // the query tiles may be written again once stream 0 has read them
+                    if (!warp_wait(&sm.x_empty, splits & 1, a.err, abort)) return;
+                    ++splits;
+                    continue;
+                }
+                mbar_arrive(&sm.x_empty);  // stream 0's scores are done
+                if (!warp_wait(&sm.x_full, (splits >> 1) & 1, a.err, abort)) return;
+                if (warp_live) {
+                    const float m1 = sm.m1[r], mn = fmaxf(m, m1);
+                    a0 = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                    a1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - mn);
+                    // a state that holds NaN without a maximum keeps it
+                    if (l != l) a0 = 1.f;
+                    const float l1 = sm.l1[r];
+                    if (l1 != l1) a1 = 1.f;
+                    l = l * a0 + l1 * a1;
+                    m = mn;
+                    joined = true;
+                }
+            }
+            if (warp_live) {
+                const float inv = cut ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                const float f0 = a0 * vref;
+                const float4* x = reinterpret_cast<const float4*>(&sm.q[0][0]);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(o_at + 32 * c, s);
+                    tc_wait_ld();
+                    float o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = (nan_cols[c] >> k & 1) ? __int_as_float(0x7fc00000) : __uint_as_float(s[k]) * f0;
+                    if (joined) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 y = x[(8 * c + k) * kTile + r];
+                            o[4 * k] += y.x * a1;
+                            o[4 * k + 1] += y.y * a1;
+                            o[4 * k + 2] += y.z * a1;
+                            o[4 * k + 3] += y.w * a1;
+                        }
+                    }
+                    if (live) {
+                        if (cut) {
+                            float4* d = reinterpret_cast<float4*>(rec + 2 * kTile + (size_t)r * D + 32 * c);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        } else {
+                            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row_at + 32 * c);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                T y[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[i] = from_float<T>(o[8 * k + i] * inv);
+                                d[k] = *reinterpret_cast<const uint4*>(y);
+                            }
+                        }
+                    }
+                }
+                if (cut && live) {
+                    rec[r] = m;
+                    rec[kTile + r] = l;
+                }
+            }
+            if (!p.paired && it.jobs > 1) {
+                mbar_arrive(&sm.x_empty);
+                // nobody writes query tiles before all of stream 0 has read the output that lies there
+                if (!warp_wait(&sm.x_empty, 1, a.err, abort)) return;
+                splits += 2;
+            }
+            tc_fence_before();
+        }
+        tiles_before += p.end - p.begin;
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArgs a, const Workspace ws) {
+    extern __shared__ unsigned char raw_smem[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(((uintptr_t)raw_smem + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 128);
+            mbar_init(&sm.k_full[i], kLoadWarps * 32);
+            mbar_init(&sm.v_full[i], kLoadWarps * 32);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        mbar_init(&sm.x_full, 128);
+        mbar_init(&sm.x_empty, 128);
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kSoftmaxWarps + kLoadWarps) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp < kSoftmaxWarps) {
+        softmax_rows<T, D>(a, ws, sm);
+    } else if (warp < kSoftmaxWarps + kLoadWarps) {
+        load_tiles<D>(a, ws, sm);
+    } else if ((threadIdx.x & 31) == 0) {
+        issue_products<D>(a, ws, sm);
+        if (sm.abort) {  // products still in flight read shared and tensor memory
+            int never = 0;
+            tc_commit(&sm.drain);
+            mbar_wait_bounded(&sm.drain, 0, a.err, &never);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftmaxWarps + kLoadWarps) tmem_free(sm.tmem, 512);
+}
+
+// Joins the partial results of the units that share boundaries cut.  CTA (boundary, rows): the first boundary inside a unit
+// has it; a warp per row, D / 32 elements per lane.
+constexpr int kJoinThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, const Workspace ws, int ctas) {
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int E = D / 32;
+    const long long cost = ws.head->cost, share = share_of(cost, ctas);
+    const int c1 = blockIdx.x + 1;  // boundary: the start of CTA c1's share
+    const long long x = share * c1;
+    if (x >= cost) return;
+    const Entry en = ws.entries[find_entry(ws.entries, ws.head->entries, x)];
+    const int w = en.paired ? kPairedCost : kSplitCost;
+    const long long unit_cost = (long long)en.tiles * w;
+    const int kvh = (int)((x - en.first) / unit_cost);
+    const long long unit = en.first + kvh * unit_cost, end = unit + unit_cost;
+    if (x == unit || share * (c1 - 1) > unit) return;  // not inside, or not the first inside
+    // pieces: CTA c has tiles [cut(c), cut(c + 1))
+    auto cut = [&](int c) {
+        const long long from = share * c - unit;
+        return from <= 0 ? 0 : (int)min((long long)en.tiles, (from + w - 1) / w);
+    };
+    const int first = c1 - 1, last = (int)((end - 1) / share);
+    if (cut(first + 1) >= en.tiles) return;  // one piece after all
+    const int n = rows_of(a, en.seq), group = a.num_heads / a.num_kv_heads;
+    const int rows = min(n * group - en.row0, 2 * kTile);
+    const int lane = threadIdx.x & 31;
+    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.y * (kJoinThreads / 32)) {
+        const int tile = r / kTile, rr = r % kTile;
+        float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = 0.f;
+        for (int c = first; c <= last; ++c) {
+            const int from = cut(c);
+            if (from >= cut(c + 1)) continue;
+            const float* rec = ws.records + ((size_t)c * 4 + (from > 0 ? 0 : 2) + tile) * record_floats(D);
+            const float mc = rec[rr], lc = rec[kTile + rr];
+            const float mn = fmaxf(m, mc);
+            float f = m == -INFINITY ? 0.f : exp2_approx(m - mn), fc = mc == -INFINITY ? 0.f : exp2_approx(mc - mn);
+            if (l != l) f = 1.f;
+            if (lc != lc) fc = 1.f;
+            l = l * f + lc * fc;
+            m = mn;
+            const float* src = rec + 2 * kTile + (size_t)rr * D + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = o[i] * f + src[i] * fc;
+        }
+        const int v = en.row0 + r, token = v / group;
+        T* dst = static_cast<T*>(a.out) +
+                 ((size_t)(max(0, a.q_offsets[en.seq]) + token) * a.num_heads + kvh * group + (v - token * group)) * D + lane * E;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < E; ++i) dst[i] = from_float<T>(o[i] * inv);
+    }
 }
 
 template <typename T, int D>
 cudaError_t attend_typed(const AttendArgs& a, cudaStream_t stream) {
-    const long long warps = (long long)a.num_tokens * a.num_heads;
-    return launch_pdl(attend_fp8_kernel<T, D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, a);
+    const int group = a.num_heads / a.num_kv_heads, ctas = a.num_sms;
+    const size_t cap = max_entries(a.num_seqs, a.num_tokens, group);
+    char* base = static_cast<char*>(a.workspace);
+    Workspace ws;
+    ws.head = reinterpret_cast<PlanHead*>(base);
+    ws.entries = reinterpret_cast<Entry*>(base + 256);
+    ws.records = reinterpret_cast<float*>(base + 256 + align256((cap + 1) * sizeof(Entry)));
+    cudaError_t e = launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)(a.num_seqs + 1) * sizeof(int), stream, a, ws,
+                               (int)cap);
+    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(Smem<D>) + 1024;
+    e = cudaFuncSetAttribute(attend_fp8_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attend_fp8_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws);
+    if (e != cudaSuccess || ctas < 2) return e;
+    return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 4), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
 
 }  // namespace
 
-size_t attend_fp8_workspace_bytes(int, int, int, int, int, int, int, int) { return 0; }
+size_t attend_fp8_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim, int,
+                                  int) {
+    const size_t cap = max_entries(num_seqs, num_tokens, num_heads / num_kv_heads);
+    return 256 + align256((cap + 1) * sizeof(Entry)) + (size_t)num_sms * 4 * record_floats(head_dim) * sizeof(float);
+}
 
 cudaError_t attend_fp8_launch(const AttendArgs& a, cudaStream_t stream) {
     if (a.dtype == 1) return a.head_dim == 128 ? attend_typed<__half, 128>(a, stream) : attend_typed<__half, 64>(a, stream);

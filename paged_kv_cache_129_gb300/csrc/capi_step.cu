@@ -221,9 +221,9 @@ int pa_attend_fp8(void* out, const void* query, const void* key_cache, const voi
     if ((head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32))
         return fail(PA_ERR_UNSUPPORTED, "pa_attend_fp8: compiled for head_dim 64 and 128, block_size 16 and 32 (head_dim=%d block_size=%d)",
                     head_dim, block_size);
-    if (!fits_int((long long)max_blocks_per_seq * block_size) || !fits_int((long long)num_blocks * num_kv_heads * block_size) ||
+    if (!fits_int((long long)max_blocks_per_seq * block_size + 1024) || !fits_int((long long)num_blocks * num_kv_heads * block_size) ||
         !fits_int((long long)num_tokens * num_heads))
-        return fail(PA_ERR_INVALID_ARG, "pa_attend_fp8: max_blocks_per_seq * block_size, num_blocks * num_kv_heads * block_size "
+        return fail(PA_ERR_INVALID_ARG, "pa_attend_fp8: max_blocks_per_seq * block_size + 1024, num_blocks * num_kv_heads * block_size "
                                         "and num_tokens * num_heads must be < 2^31");
     if (num_seqs > kMaxStepSeqs) return fail(PA_ERR_UNSUPPORTED, "pa_attend_fp8: num_seqs=%d > %d", num_seqs, kMaxStepSeqs);
     if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "pa_attend_fp8: scale is not finite");

@@ -37,7 +37,9 @@ def attend(q, k_codes, v_codes, ks, vs, tables, lens, offsets, scale, dtype):
     The bound, with A = sum p |v| of an element and S = the largest sum |q k| of the row's scores: half a step of the
     output (eps / 2 relative; below the smallest normal number steps are that number times eps, f16: 2^-24); P in f16,
     half a step 2^-11 of A; scores from float32 sums of d exact products, each off by 2^-23 of S in the worst order,
-    d <= 128, which moves p by twice that; and L / 16 + 16 sums of A in float32."""
+    d <= 128, which moves p by twice that; and L / 16 + 16 sums of A in float32.  P of a small exponential, or of a block
+    whose V scale is far below the largest, is subnormal in f16: off by half a step 2^-25 of the largest scale W seen by the
+    request's rows, times |code|, with the exponentials' sum at least 1: 2^-25 W sum |code|."""
     out = np.full(q.shape, np.nan)
     bound = np.full(q.shape, np.nan)
     hq, hkv = q.shape[1], k_codes.shape[1]
@@ -50,6 +52,9 @@ def attend(q, k_codes, v_codes, ks, vs, tables, lens, offsets, scale, dtype):
             continue
         for h in range(hkv):
             k, v = gather(k_codes, ks, tables[b], L, h), gather(v_codes, vs, tables[b], L, h)
+            ids = np.asarray(tables[b])[:(L + k_codes.shape[2] - 1) // k_codes.shape[2]]
+            codes = np.abs(gather(v_codes, np.ones_like(vs), tables[b], L, h)).cumsum(0)
+            small = 2.0 ** -25 * float(vs[ids, h].max(initial=0)) * codes
             for t in range(n):
                 seen = L - n + t + 1
                 rows = q[lo + t, h * g:(h + 1) * g]
@@ -65,7 +70,7 @@ def attend(q, k_codes, v_codes, ks, vs, tables, lens, offsets, scale, dtype):
                 big = (abs(scale) * np.abs(rows) @ np.abs(k[:seen]).T).max(1, keepdims=True)
                 out[lo + t, h * g:(h + 1) * g] = o
                 bound[lo + t, h * g:(h + 1) * g] = eps / 2 * np.abs(o) * 1.01 + mass * (
-                    2.0 ** -11 + 2 * big * 128 * 2.0 ** -23 + (L / 16 + 16) * 2.0 ** -23) + tiny
+                    2.0 ** -11 + 2 * big * 128 * 2.0 ** -23 + (L / 16 + 16) * 2.0 ** -23) + small[seen - 1] + tiny
     return out, bound
 
 
