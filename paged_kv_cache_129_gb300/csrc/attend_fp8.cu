@@ -31,9 +31,12 @@ namespace {
 
 constexpr int kTile = 128;             // rows of a row tile, tokens of a key tile
 constexpr int kSoftmaxWarps = 8;       // four per stream
-constexpr int kLoadWarps = 4;
-constexpr int kThreads = (kSoftmaxWarps + kLoadWarps + 1) * 32;
-constexpr int kRing = 4;               // slots of per-tile side data (scales), see load_tiles()
+constexpr int kWidenWarps = 4;
+constexpr int kIssueWarp = kSoftmaxWarps + kWidenWarps, kCopyWarp = kIssueWarp + 1;
+constexpr int kThreads = (kCopyWarp + 1) * 32;
+constexpr int kBuffers = 3;            // f16 operand tiles (K or V) in shared memory
+constexpr int kRing = 8;               // slots of per-tile side data (scales), see copy_tiles()
+constexpr int kNanRing = 4;
 // Cost of a key tile in shares: a pair does twice the products and exponentials of a split tile, but loads and widens it once.
 constexpr int kPairedCost = 4, kSplitCost = 3;
 constexpr int kMinShare = 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
@@ -138,10 +141,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint4 load_stream(const void* p) {  // read once: keep it out of L1
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+// size bytes (a multiple of 16, both addresses 16-byte aligned) into shared memory, completion on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned size, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+                 "l"(src), "r"(size), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 // Operand tiles in shared memory: panels of 64 elements (128 bytes) by 128 rows, 128-byte swizzle (16-byte unit u of row r
@@ -330,23 +334,50 @@ struct Walk {
 
 template <int D>
 struct Smem {
-    static constexpr int kOperand = kTile * D * 2;  // one f16 tile
-    unsigned char q[2][kOperand];  // at the end of a split piece: stream 1's output
-    unsigned char k[2][kOperand];
-    unsigned char v[2][kOperand];
-    float ks[kRing][8], vs[kRing][8];        // scales of the tile's blocks
-    unsigned masked_blocks[kRing];           // blocks of the tile whose id is outside the pool
-    unsigned nan_any[kRing][kLoadWarps];     // whether a load warp found NaN in V of a tile that some row sees in part,
-    uint16_t nan_at[kRing][kTile][D / 16];   // and where: per token and 16 elements
-    float m1[kTile], l1[kTile];              // stream 1's state at the end of a split piece
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], x_full, x_empty, drain;
+    static constexpr int kOperand = kTile * D * 2;      // one f16 tile
+    static constexpr int kRaw = D == 128 ? 3 : 6;       // tiles of codes on their way or waiting: 48 KB in flight per SM
+    unsigned char q[2][kOperand];                       // at the end of a split piece: stream 1's output
+    unsigned char kv[kBuffers][kOperand];
+    unsigned char raw[kRaw][kTile * D];
+    float ks[kRing][8], vs[kRing][8];                   // scales of the tile's blocks
+    unsigned present[kRing], masked[kRing];             // blocks of the tile: copied; with an id outside the pool
+    unsigned nan_any[kNanRing][kWidenWarps];            // whether a warp found NaN in V of a tile that some row sees in part,
+    uint16_t nan_at[kNanRing][kTile][D / 16];           // and where: per token and 16 elements
+    float m1[kTile], l1[kTile];                         // stream 1's state at the end of a split piece
+    uint64_t q_full[2], raw_full[kRaw], raw_empty[kRaw], kv_full[kBuffers], kv_empty[kBuffers];
+    uint64_t s_full[2], p_full[2], o_full[2], x_full, x_empty, drain;
     uint32_t tmem;
     volatile int abort;
 };
 
-// mbar_wait_bounded by a whole warp: all lanes go on, or none.
+// The order in which a piece's n key tiles go through the buffers.  Paired: K0 V0 K1 V1 ...  Split: K one tile ahead, K0 K1 V0 K2
+// V1 ... V(n-2) V(n-1), because the scores of a tile are issued before the output of the tile before it.
+struct Fill {
+    int tile;
+    bool value;
+};
+__device__ __forceinline__ Fill fill_of(bool paired, int n, int i) {
+    if (paired) return {i >> 1, (i & 1) != 0};
+    if (i == 2 * n - 1) return {n - 1, true};
+    if (i == 0) return {0, false};
+    return (i & 1) ? Fill{(i + 1) >> 1, false} : Fill{(i >> 1) - 1, true};
+}
+__device__ __forceinline__ int key_fill(bool paired, int tile) { return paired ? 2 * tile : tile == 0 ? 0 : 2 * tile - 1; }
+__device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
+    return paired ? 2 * tile + 1 : tile == n - 1 ? 2 * n - 1 : 2 * tile + 2;
+}
+
+// mbar_wait_bounded, with the clock and the abort flag read only now and then: waiting warps share their scheduler with warps
+// that work.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, err, abort);
+}
+// The same by a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, abort));
+    return __all_sync(0xffffffffu, wait_for(bar, parity, err, abort));
 }
 
 // What a piece is to every role.
@@ -366,8 +397,8 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, const Piece& p) {
     return it;
 }
 
-// Sixteen E4M3 codes as f16 (exact), to units u and u + 1 of a swizzled row.
-__device__ __forceinline__ void widen_store(unsigned char* row, int u, int r7, uint4 c, bool odd_first) {
+// Sixteen E4M3 codes as f16 (exact), in two 16-byte units.
+__device__ __forceinline__ void widen_store(unsigned char* unit0, unsigned char* unit1, uint4 c) {
     uint32_t h[8];
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -377,129 +408,165 @@ __device__ __forceinline__ void widen_store(unsigned char* row, int u, int r7, u
         h[2 * i] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
         h[2 * i + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
     }
-    const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-    // The lanes of a row hold chunks of two panels, whose banks coincide: one half stores its odd unit first.
-    *reinterpret_cast<uint4*>(row + (((odd_first ? u + 1 : u) ^ r7) << 4)) = odd_first ? b : a;
-    *reinterpret_cast<uint4*>(row + (((odd_first ? u : u + 1) ^ r7) << 4)) = odd_first ? a : b;
+    *reinterpret_cast<uint4*>(unit0) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(unit1) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
 // Per byte of w: 0x80 where the code is NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// The four load warps: widen key tile after key tile into the two K and two V stages.  Codes are on their way in registers
-// while the previous tile's are widened (V of a tile under K's stores, the next K under V's).
-// Side data of tile i sits in ring slot i % 4 and is read by the softmax of tile i, which ends before V stage i % 2 is
-// free again; slot i % 4 is written again with tile i + 4, after V of tile i + 3 has been stored, so after that.
-template <int D>
-__device__ __forceinline__ void load_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
-    constexpr int CPR = D / 16, RPP = 128 / CPR, N = kTile / RPP;  // chunks per row, rows per pass, passes
-    const int tid = threadIdx.x - kSoftmaxWarps * 32, lane = tid & 31;
-    const int chunk = tid % CPR, row0 = tid / CPR;
-    const int bs = a.block_size, shift = bs == 16 ? 4 : 5, pages = kTile >> shift;
+// The copy warp: every block's K or V rows (contiguous) into the raw ring by one bulk copy per block, a lane each, and the tile's
+// scales into the side ring.  Registers and L1 could not hold what has to be in flight: with 206 KB of shared memory taken, L1
+// has room for about 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.
+// Side data of tile i sits in slot i % 8.  When K of tile i is copied, the raw slot that it takes was widened, so the f16 buffer
+// three fills before that one was free: scores of tile i - 3 at least are done, so the softmax of tile i - 5, and slot i % 8 is
+// tile i - 8's.
+template <int D, int BS>
+__device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    constexpr int BLOCKS = kTile / BS, RAW = Smem<D>::kRaw;
+    const int lane = threadIdx.x & 31;
     const bool both = a.value_cache == nullptr;
-    volatile int* abort = &sm.abort;
+    const size_t stride = (size_t)(both ? 2 : 1) * BS * D;  // K of a (block, head) begins at record * stride
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
-    unsigned count = 0;  // tiles so far
-    const bool odd_first = chunk >= 4;
-    const uint32_t panel = (chunk / 4) * kPanel;
-    const int u = (chunk % 4) * 2;
+    unsigned fills = 0, tiles = 0;
+    bool ok = true;
+    while (ok && walk.next(&p)) {
+        const int n = p.end - p.begin, L = clamped_length(a, p.seq), used = (L + BS - 1) / BS;
+        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
+        // Lane j < BLOCKS has block j of a tile: its id, one tile ahead of its use, then scales and record.
+        auto wanted = [&](int tile) { return lane < BLOCKS && tile < n && (p.begin + tile) * BLOCKS + lane < used; };
+        auto fetch = [&](int tile) { return wanted(tile) ? table[(p.begin + tile) * BLOCKS + lane] : -1; };
+        int next_id = fetch(0);
+        size_t rec[2] = {0, 0};  // of even and odd tiles: V of a tile is copied after K of the next one
+        bool have[2] = {false, false};
+        for (int i = 0; i < 2 * n; ++i, ++fills) {
+            const Fill f = fill_of(p.paired, n, i);
+            const int odd = f.tile & 1, slot = fills % RAW;
+            float ks = 0.f, vs = 0.f;
+            bool bad = false;
+            if (!f.value) {
+                const int id = next_id;
+                next_id = fetch(f.tile + 1);
+                const bool in = id >= 0 && id < a.num_blocks && wanted(f.tile);
+                bad = wanted(f.tile) && !in;
+                const size_t r = (size_t)(in ? id : 0) * a.num_kv_heads + p.kvh;
+                if (odd)
+                    rec[1] = r, have[1] = in;
+                else
+                    rec[0] = r, have[0] = in;
+                if (in) {
+                    ks = a.k_scale[r];
+                    vs = a.v_scale[r];
+                }
+                if (bad) atomicOr(a.err, kErrBadTable);
+            }
+            const bool in = odd ? have[1] : have[0];
+            const size_t r = odd ? rec[1] : rec[0];
+            const unsigned present = __ballot_sync(0xffffffffu, in), masked = __ballot_sync(0xffffffffu, bad);
+            if (!warp_wait(&sm.raw_empty[slot], ((fills / RAW) & 1) ^ 1, a.err, &sm.abort)) {
+                ok = false;
+                break;
+            }
+            if (!f.value) {
+                const int side = (tiles + f.tile) % kRing;
+                if (lane < 8) {
+                    sm.ks[side][lane] = ks;
+                    sm.vs[side][lane] = vs;
+                }
+                if (lane == 0) {
+                    sm.present[side] = present;
+                    sm.masked[side] = masked;
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(present) * BS * D);
+            __syncwarp();
+            if (in) {
+                const uint8_t* src = f.value ? (both ? a.key_cache + r * stride + BS * D : a.value_cache + r * stride)
+                                             : a.key_cache + r * stride;
+                bulk_load(sm.raw[slot] + lane * BS * D, src, BS * D, &sm.raw_full[slot]);
+            }
+        }
+        tiles += n;
+    }
+    if (!ok) {  // copies still under way must land before the CTA's shared memory goes
+        int never = 0;
+        for (unsigned f = fills > RAW ? fills - RAW : 0; f < fills; ++f)
+            mbar_wait_bounded(&sm.raw_full[f % RAW], (f / RAW) & 1, a.err, &never);
+    }
+}
+
+// The four widen warps: tile after tile of codes from the raw ring to a swizzled f16 buffer.
+template <int D, int BS>
+__device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    constexpr int RPP = 128 / (D / 16), N = kTile / RPP, RAW = Smem<D>::kRaw;  // rows per pass, passes
+    const int tid = threadIdx.x - kSoftmaxWarps * 32, lane = tid & 31;
+    // A thread's sixteen codes of a row, the same in every pass.  The eight lanes that load or store together hold half a row each
+    // of an even and an odd row, the halves apart: eight different 16-byte columns of the codes (128-byte lines), and
+    // eight different swizzled units of the buffer.
+    const int chunk = D == 128 ? (lane & 3) + 4 * ((lane >> 2 ^ lane >> 3) & 1) : lane & 3;
+    const int row0 = D == 128 ? 4 * (tid >> 5) + (lane >> 2 & 1) + 2 * (lane >> 4) : tid >> 2;
+    const uint32_t line = (chunk / 4) * kPanel + row0 * 128, u = (chunk % 4) * 2;
+    const uint32_t unit0 = line + ((u ^ (row0 & 7)) << 4), unit1 = line + (((u + 1) ^ (row0 & 7)) << 4);
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned fills = 0, tiles = 0;
     while (walk.next(&p)) {
         const Item it = item_of(a, p);
-        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
-        const int used = (it.L + bs - 1) >> shift;
+        const int n = p.end - p.begin;
         const int seen_by_all = it.L - it.n + p.row0 / it.group;  // the first row's position
-        // block of page `lane` of a tile: -1 none, -2 an id outside the pool
-        auto block_of = [&](int tile) {
-            int id = -1;
-            const int page = tile * pages + lane;
-            if (lane < pages && page < used && tile < p.end) {
-                id = table[page];
-                if (id < 0 || id >= a.num_blocks) {
-                    atomicOr(a.err, kErrBadTable);
-                    id = -2;
+        for (int i = 0; i < 2 * n; ++i, ++fills) {
+            const Fill f = fill_of(p.paired, n, i);
+            const int slot = fills % RAW, buf = fills % kBuffers, p0 = (p.begin + f.tile) * kTile;
+            if (!warp_wait(&sm.raw_full[slot], (fills / RAW) & 1, a.err, &sm.abort)) return;
+            const unsigned present = sm.present[(tiles + f.tile) % kRing];
+            const int left = it.L - p0;  // rows of the tile inside the context; the others' codes may be anything
+            uint4 c[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int r = row0 + k * RPP;
+                c[k] = *reinterpret_cast<const uint4*>(sm.raw[slot] + r * D + chunk * 16);
+            }
+            if (left < kTile || present != (1u << (kTile / BS)) - 1) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int r = row0 + k * RPP;
+                    if (r >= left || !(present >> (r / BS) & 1)) c[k] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
-            return id;
-        };
-        auto load = [&](uint4 (&raw)[N], int ids, int tile, bool value) {
+            if (!warp_wait(&sm.kv_empty[buf], ((fills / kBuffers) & 1) ^ 1, a.err, &sm.abort)) return;
+            if (f.value) {
+                bool any = false;
+                const int at_slot = (tiles + f.tile) % kNanRing;
+                if (p0 + kTile - 1 > seen_by_all) {
+                    // Some row sees this tile in part: a NaN behind its position must not reach it through 0 * NaN.
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int r = row0 + i * RPP, id = __shfl_sync(0xffffffffu, ids, r >> shift);
-                raw[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (id >= 0 && tile * kTile + r < it.L) {
-                    const size_t rec = (size_t)id * a.num_kv_heads + p.kvh;
-                    const size_t at = both ? (2 * rec + (value ? 1 : 0)) * bs : rec * bs;
-                    const uint8_t* base = value && !both ? a.value_cache : a.key_cache;
-                    raw[i] = load_stream(base + (at + (r & (bs - 1))) * D + chunk * 16);
-                }
-            }
-        };
-        auto scales_of = [&](int id, float* ks, float* vs) {  // the first load warp has them, a block per lane
-            *ks = *vs = 0.f;
-            if (tid < 32 && id >= 0) {
-                const size_t si = (size_t)id * a.num_kv_heads + p.kvh;
-                *ks = a.k_scale[si];
-                *vs = a.v_scale[si];
-            }
-        };
-        uint4 kr[N], vr[N];
-        float ks, vs;
-        int ids = block_of(p.begin);
-        load(kr, ids, p.begin, false);
-        scales_of(ids, &ks, &vs);
-        for (int tile = p.begin; tile < p.end; ++tile, ++count) {
-            const int stage = count & 1, slot = count % kRing;
-            const unsigned parity = (count >> 1) & 1;
-            const int next_ids = block_of(tile + 1);
-            load(vr, ids, tile, true);
-            if (tid < 32) {
-                const unsigned masked = __ballot_sync(0xffffffffu, ids == -2);
-                if (lane < 8) {
-                    sm.ks[slot][lane] = ks;
-                    sm.vs[slot][lane] = vs;
-                }
-                if (lane == 0) sm.masked_blocks[slot] = masked;
-            }
-            if (!warp_wait(&sm.k_empty[stage], parity ^ 1, a.err, abort)) return;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int r = row0 + i * RPP;
-                widen_store(sm.k[stage] + panel + r * 128, u, r & 7, kr[i], odd_first);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&sm.k_full[stage]);
-            if (tile + 1 < p.end) load(kr, next_ids, tile + 1, false);
-            scales_of(next_ids, &ks, &vs);
-            if (!warp_wait(&sm.v_empty[stage], parity ^ 1, a.err, abort)) return;
-            bool any = false;
-            if (tile * kTile + kTile - 1 > seen_by_all) {
-                // Some row sees this tile in part: a NaN behind its position must not reach it through 0 * NaN.
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&vr[i]);
-                    unsigned at = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t t = nan_bytes(w[k]);
-                        at |= (((t >> 7) * 0x01020408u >> 24) & 0xfu) << (4 * k);
-                        w[k] &= ~((t >> 7) * 0xffu);
+                    for (int k = 0; k < N; ++k) {
+                        unsigned at = 0;
+                        auto clean = [&](uint32_t w, int j) {
+                            const uint32_t t = nan_bytes(w) >> 7;
+                            at |= ((t * 0x01020408u >> 24) & 0xfu) << (4 * j);
+                            return w & ~(t * 0xffu);
+                        };
+                        c[k] = make_uint4(clean(c[k].x, 0), clean(c[k].y, 1), clean(c[k].z, 2), clean(c[k].w, 3));
+                        any |= at != 0;
+                        sm.nan_at[at_slot][row0 + k * RPP][chunk] = (uint16_t)at;
                     }
-                    any |= at != 0;
-                    sm.nan_at[slot][row0 + i * RPP][chunk] = (uint16_t)at;
                 }
+                any = __any_sync(0xffffffffu, any);
+                if (lane == 0) sm.nan_any[at_slot][tid >> 5] = any;
             }
-            any = __any_sync(0xffffffffu, any);
-            if (lane == 0) sm.nan_any[slot][tid >> 5] = any;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.raw_empty[slot]);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int r = row0 + i * RPP;
-                widen_store(sm.v[stage] + panel + r * 128, u, r & 7, vr[i], odd_first);
-            }
+            for (int k = 0; k < N; ++k)
+                widen_store(sm.kv[buf] + unit0 + k * RPP * 128, sm.kv[buf] + unit1 + k * RPP * 128, c[k]);
             fence_proxy_async_smem();
-            mbar_arrive(&sm.v_full[stage]);
-            ids = next_ids;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.kv_full[buf]);
         }
+        tiles += n;
     }
 }
 
@@ -511,22 +578,22 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
     const uint32_t tmem = sm.tmem;
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
-    unsigned tiles = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};
+    unsigned fills = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};
     while (walk.next(&p)) {
-        const int jobs = (p.end - p.begin) * (p.paired ? 2 : 1);
+        const int n = p.end - p.begin, jobs = n * (p.paired ? 2 : 1);
         auto scores = [&](int j) {
             const int t = j & 1;
-            const unsigned tile = tiles + (p.paired ? j >> 1 : j), stage = tile & 1;
-            if (!mbar_wait_bounded(&sm.k_full[stage], (tile >> 1) & 1, a.err, abort)) return false;
-            if (j < 2 && !mbar_wait_bounded(&sm.q_full[t], pieces[t] & 1, a.err, abort)) return false;
+            const unsigned f = fills + key_fill(p.paired, p.paired ? j >> 1 : j), buf = f % kBuffers;
+            if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return false;
+            if (j < 2 && !wait_for(&sm.q_full[t], pieces[t] & 1, a.err, abort)) return false;
             tc_fence_after();
-            const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.k[stage]), 16, 1024);
+            const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
                 mma_ss(tmem + t * kTile, qd + off, kd + off, idesc_of(kTile, false), k > 0);
             }
-            if (!p.paired || t == 1) tc_commit(&sm.k_empty[stage]);
+            if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
             tc_commit(&sm.s_full[t]);
             return true;
         };
@@ -534,35 +601,34 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
             if (!scores(j)) return;
         for (int j = 0; j < jobs; ++j) {
             const int t = j & 1;
-            const unsigned tile = tiles + (p.paired ? j >> 1 : j), stage = tile & 1;
-            if (!mbar_wait_bounded(&sm.v_full[stage], (tile >> 1) & 1, a.err, abort)) return;
-            if (!mbar_wait_bounded(&sm.p_full[t], steps[t]++ & 1, a.err, abort)) return;
+            const unsigned f = fills + value_fill(p.paired, n, p.paired ? j >> 1 : j), buf = f % kBuffers;
+            if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+            if (!wait_for(&sm.p_full[t], steps[t]++ & 1, a.err, abort)) return;
             tc_fence_after();
-            const uint64_t vd = desc_of(smem_addr(sm.v[stage]), kPanel, 1024);
+            const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
                 mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
-            if (!p.paired || t == 1) tc_commit(&sm.v_empty[stage]);
+            if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
             if (j + 2 >= jobs) tc_commit(&sm.o_full[t]);
             if (j + 2 < jobs && !scores(j + 2)) return;
         }
-        tiles += p.end - p.begin;
+        fills += 2 * n;
         ++pieces[0];
         if (jobs > 1) ++pieces[1];
     }
 }
 
 // A softmax warp: 32 rows of a stream's row tile, one per lane.
-template <typename T, int D>
+template <typename T, int D, int BS>
 __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
     volatile int* abort = &sm.abort;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = sm.tmem + lanes + t * kTile, o_at = sm.tmem + lanes + 2 * kTile + t * D;
-    const int shift = a.block_size == 16 ? 4 : 5;
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
-    unsigned pieces = 0, steps = 0, splits = 0, tiles_before = 0;
+    unsigned pieces = 0, steps = 0, splits = 0, tiles_before = 0;  // so far
     while (walk.next(&p)) {
         const Item it = item_of(a, p);
         const int v = p.row0 + (p.paired ? t * kTile : 0) + r;  // row of the request
@@ -624,7 +690,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                 if (!warp_wait(&sm.s_full[t], steps & 1, a.err, abort)) return;
                 tc_fence_after();
                 if (warp_live) {
-                    const unsigned masked_blocks = sm.masked_blocks[slot];
+                    const unsigned masked_blocks = sm.masked[slot];
                     const bool whole = __all_sync(0xffffffffu, !live || p0 + kTile - 1 <= bound) && masked_blocks == 0;
                     // columns of the tile that the row sees
                     const int cols = min(kTile, bound - p0 + 1);
@@ -636,7 +702,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                         tc_wait_ld();
 #pragma unroll
                         for (int hb = 0; hb < 2; ++hb) {
-                            const int blk = (32 * c + 16 * hb) >> shift;
+                            const int blk = (32 * c + 16 * hb) / BS;
                             float x = -INFINITY;
                             if (whole) {
 #pragma unroll
@@ -684,7 +750,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                         uint32_t out[16];
 #pragma unroll
                         for (int hb = 0; hb < 2; ++hb) {
-                            const int blk = (32 * c + 16 * hb) >> shift;
+                            const int blk = (32 * c + 16 * hb) / BS;
                             const float kf = sm.ks[slot][blk] * qf, vf = sm.vs[slot][blk] * vinv;
                             const bool gone = masked_blocks >> blk & 1;
 #pragma unroll
@@ -704,13 +770,15 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                         tmem_st16(s_at + 16 * c, out);
                     }
                     if (!whole) {
-                        if (!warp_wait(&sm.v_full[count & 1], (count >> 1) & 1, a.err, abort)) return;
-                        if (sm.nan_any[slot][0] | sm.nan_any[slot][1] | sm.nan_any[slot][2] | sm.nan_any[slot][3]) {
+                        const unsigned f = 2 * tiles_before + value_fill(p.paired, p.end - p.begin, local);
+                        if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
+                        const int at_slot = count % kNanRing;
+                        if (sm.nan_any[at_slot][0] | sm.nan_any[at_slot][1] | sm.nan_any[at_slot][2] | sm.nan_any[at_slot][3]) {
                             for (int k = 0; k < cols; ++k)
-                                if (!(masked_blocks >> (k >> shift) & 1))
+                                if (!(masked_blocks >> (k / BS) & 1))
 #pragma unroll
                                     for (int i = 0; i < D / 32; ++i)
-                                        nan_cols[i] |= (uint32_t)sm.nan_at[slot][k][2 * i] | ((uint32_t)sm.nan_at[slot][k][2 * i + 1] << 16);
+                                        nan_cols[i] |= (uint32_t)sm.nan_at[at_slot][k][2 * i] | ((uint32_t)sm.nan_at[at_slot][k][2 * i + 1] << 16);
                         }
                     }
                     tc_wait_st();
@@ -833,7 +901,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArgs a, const Workspace ws) {
     extern __shared__ unsigned char raw_smem[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(((uintptr_t)raw_smem + 1023) & ~(uintptr_t)1023);
@@ -841,13 +909,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 128);
-            mbar_init(&sm.k_full[i], kLoadWarps * 32);
-            mbar_init(&sm.v_full[i], kLoadWarps * 32);
-            mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_full[i], 1);
+        }
+        for (int i = 0; i < Smem<D>::kRaw; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], kWidenWarps);
+        }
+        for (int i = 0; i < kBuffers; ++i) {
+            mbar_init(&sm.kv_full[i], kWidenWarps);
+            mbar_init(&sm.kv_empty[i], 1);
         }
         mbar_init(&sm.x_full, 128);
         mbar_init(&sm.x_empty, 128);
@@ -855,16 +927,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
         sm.abort = 0;
         fence_barrier_init();
     }
-    if (warp == kSoftmaxWarps + kLoadWarps) tmem_alloc(&sm.tmem, 512);
+    if (warp == kIssueWarp) tmem_alloc(&sm.tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     griddep_wait();
     griddep_launch_dependents();
     if (warp < kSoftmaxWarps) {
-        softmax_rows<T, D>(a, ws, sm);
-    } else if (warp < kSoftmaxWarps + kLoadWarps) {
-        load_tiles<D>(a, ws, sm);
+        softmax_rows<T, D, BS>(a, ws, sm);
+    } else if (warp < kSoftmaxWarps + kWidenWarps) {
+        widen_tiles<D, BS>(a, ws, sm);
+    } else if (warp == kCopyWarp) {
+        copy_tiles<D, BS>(a, ws, sm);
     } else if ((threadIdx.x & 31) == 0) {
         issue_products<D>(a, ws, sm);
         if (sm.abort) {  // products still in flight read shared and tensor memory
@@ -877,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kSoftmaxWarps + kLoadWarps) tmem_free(sm.tmem, 512);
+    if (warp == kIssueWarp) tmem_free(sm.tmem, 512);
 }
 
 // Joins the partial results of the units that share boundaries cut.  CTA (boundary, rows): the first boundary inside a unit
@@ -937,7 +1011,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int BS>
 cudaError_t attend_typed(const AttendArgs& a, cudaStream_t stream) {
     const int group = a.num_heads / a.num_kv_heads, ctas = a.num_sms;
     const size_t cap = max_entries(a.num_seqs, a.num_tokens, group);
@@ -950,9 +1024,9 @@ cudaError_t attend_typed(const AttendArgs& a, cudaStream_t stream) {
                                (int)cap);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(Smem<D>) + 1024;
-    e = cudaFuncSetAttribute(attend_fp8_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(attend_fp8_kernel<T, D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_fp8_kernel<T, D>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws);
+    e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws);
     if (e != cudaSuccess || ctas < 2) return e;
     return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 4), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
@@ -966,8 +1040,17 @@ size_t attend_fp8_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int
 }
 
 cudaError_t attend_fp8_launch(const AttendArgs& a, cudaStream_t stream) {
-    if (a.dtype == 1) return a.head_dim == 128 ? attend_typed<__half, 128>(a, stream) : attend_typed<__half, 64>(a, stream);
-    return a.head_dim == 128 ? attend_typed<__nv_bfloat16, 128>(a, stream) : attend_typed<__nv_bfloat16, 64>(a, stream);
+    const int pick = (a.dtype == 1 ? 4 : 0) + (a.head_dim == 64 ? 2 : 0) + (a.block_size == 32 ? 1 : 0);
+    switch (pick) {
+        case 0: return attend_typed<__nv_bfloat16, 128, 16>(a, stream);
+        case 1: return attend_typed<__nv_bfloat16, 128, 32>(a, stream);
+        case 2: return attend_typed<__nv_bfloat16, 64, 16>(a, stream);
+        case 3: return attend_typed<__nv_bfloat16, 64, 32>(a, stream);
+        case 4: return attend_typed<__half, 128, 16>(a, stream);
+        case 5: return attend_typed<__half, 128, 32>(a, stream);
+        case 6: return attend_typed<__half, 64, 16>(a, stream);
+        default: return attend_typed<__half, 64, 32>(a, stream);
+    }
 }
 
 }  // namespace pa
