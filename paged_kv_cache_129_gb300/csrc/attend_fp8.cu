@@ -19,6 +19,7 @@
 // taken from follows the true one by steps of 2^8 at least: rescaling the output in tensor memory is rare that way.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -343,6 +344,7 @@ struct Smem {
     unsigned present[kRing], masked[kRing];             // blocks of the tile: copied; with an id outside the pool
     unsigned nan_any[kNanRing][kWidenWarps];            // whether a warp found NaN in V of a tile that some row sees in part,
     uint16_t nan_at[kNanRing][kTile][D / 16];           // and where: per token and 16 elements
+    uint32_t nan_row[2][kTile][D / 32];                 // per row: elements of the output that are NaN, if its thread says so
     float m1[kTile], l1[kTile];                         // stream 1's state at the end of a split piece
     uint64_t q_full[2], raw_full[kRaw], raw_empty[kRaw], kv_full[kBuffers], kv_empty[kBuffers];
     uint64_t s_full[2], p_full[2], o_full[2], x_full, x_empty, drain;
@@ -543,6 +545,10 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
                     // Some row sees this tile in part: a NaN behind its position must not reach it through 0 * NaN.
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
+                        if (!(nan_bytes(c[k].x) | nan_bytes(c[k].y) | nan_bytes(c[k].z) | nan_bytes(c[k].w))) {
+                            sm.nan_at[at_slot][row0 + k * RPP][chunk] = 0;
+                            continue;
+                        }
                         unsigned at = 0;
                         auto clean = [&](uint32_t w, int j) {
                             const uint32_t t = nan_bytes(w) >> 7;
@@ -578,48 +584,104 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
     const uint32_t tmem = sm.tmem;
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
-    unsigned fills = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};
+    unsigned fills = 0, pieces0 = 0, pieces1 = 0, steps0 = 0, steps1 = 0;
     while (walk.next(&p)) {
         const int n = p.end - p.begin, jobs = n * (p.paired ? 2 : 1);
-        auto scores = [&](int j) {
-            const int t = j & 1;
-            const unsigned f = fills + key_fill(p.paired, p.paired ? j >> 1 : j), buf = f % kBuffers;
-            if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return false;
-            if (j < 2 && !wait_for(&sm.q_full[t], pieces[t] & 1, a.err, abort)) return false;
-            tc_fence_after();
-            const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
+        for (int j = -2; j < jobs; ++j) {
+            if (j >= 0) {
+                const int t = j & 1;
+                const unsigned f = fills + value_fill(p.paired, n, p.paired ? j >> 1 : j), buf = f % kBuffers;
+                if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+                if (!wait_for(&sm.p_full[t], (t ? steps1++ : steps0++) & 1, a.err, abort)) return;
+                tc_fence_after();
+                const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
-                mma_ss(tmem + t * kTile, qd + off, kd + off, idesc_of(kTile, false), k > 0);
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
+                if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
+                if (j + 2 >= jobs) tc_commit(&sm.o_full[t]);
             }
-            if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
-            tc_commit(&sm.s_full[t]);
-            return true;
-        };
-        for (int j = 0; j < min(jobs, 2); ++j)
-            if (!scores(j)) return;
-        for (int j = 0; j < jobs; ++j) {
-            const int t = j & 1;
-            const unsigned f = fills + value_fill(p.paired, n, p.paired ? j >> 1 : j), buf = f % kBuffers;
-            if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-            if (!wait_for(&sm.p_full[t], steps[t]++ & 1, a.err, abort)) return;
-            tc_fence_after();
-            const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
+            const int next = j + 2;
+            if (next < jobs) {
+                const int t = next & 1;
+                const unsigned f = fills + key_fill(p.paired, p.paired ? next >> 1 : next), buf = f % kBuffers;
+                if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+                if (next < 2 && !wait_for(&sm.q_full[t], (t ? pieces1 : pieces0) & 1, a.err, abort)) return;
+                tc_fence_after();
+                const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
-            if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
-            if (j + 2 >= jobs) tc_commit(&sm.o_full[t]);
-            if (j + 2 < jobs && !scores(j + 2)) return;
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
+                    mma_ss(tmem + t * kTile, qd + off, kd + off, idesc_of(kTile, false), k > 0);
+                }
+                if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
+                tc_commit(&sm.s_full[t]);
+            }
         }
         fills += 2 * n;
-        ++pieces[0];
-        if (jobs > 1) ++pieces[1];
+        ++pieces0;
+        if (jobs > 1) ++pieces1;
     }
 }
 
-// A softmax warp: 32 rows of a stream's row tile, one per lane.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
+        "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
+        "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
+        "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return d;
+}
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
+
+// A query row to f16 in the swizzled tile; returns what undoes its power of two.
+template <typename T, int D>
+__device__ __forceinline__ float stage_query(const T* src, bool live, bool negate, unsigned char* tile, int r) {
+    float mul = negate ? -1.f : 1.f;
+    int e = 0;
+    if (!std::is_same<T, __half>::value) {
+        float most = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            float x[8];
+            unpack16<T>(live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[k]));
+        }
+        if (most > 0.f && most <= 3.402823466e38f) {
+            int ex;
+            frexpf(most, &ex);  // most = f * 2^ex, f in [0.5, 1): the row's largest goes to [2^14, 2^15)
+            e = min(max(15 - ex, -126), 126);
+        }
+        mul *= __int_as_float((e + 127) << 23);
+    }
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        float x[8];
+        unpack16<T>(live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), x);
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 y = __floats2half2_rn(x[2 * k] * mul, x[2 * k + 1] * mul);
+            h[k] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        *reinterpret_cast<uint4*>(tile + r * 128 + (i / 8) * kPanel + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return __int_as_float((127 - e) << 23);
+}
+
+// A softmax warp: 32 rows of a stream's row tile, one per lane.  Its code is kept short (loops over 32 columns that are not
+// unrolled further): five roles run at once, and what the instruction caches cannot hold costs more than the loops.
 template <typename T, int D, int BS>
 __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -631,273 +693,221 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
     unsigned pieces = 0, steps = 0, splits = 0, tiles_before = 0;  // so far
     while (walk.next(&p)) {
         const Item it = item_of(a, p);
-        const int v = p.row0 + (p.paired ? t * kTile : 0) + r;  // row of the request
-        const bool live = v < it.rows;
-        const bool warp_live = p.row0 + (p.paired ? t * kTile : 0) + (warp & 3) * 32 < it.rows;
+        const int first = p.row0 + (p.paired ? t * kTile : 0);
+        const int v = first + r;  // row of the request
+        const bool live = v < it.rows, warp_live = first + (warp & 3) * 32 < it.rows;
         const int token = live ? v / it.group : 0;
         const int bound = live ? it.L - it.n + token : -1;  // last position that the row sees
         const size_t row_at = ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D;
-        const int my_jobs = (it.jobs + 1 - t) / 2;
-        if (p.paired || my_jobs > 0) {
-            // the query row to f16
-            uint4 raw[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                raw[i] = live ? *reinterpret_cast<const uint4*>(static_cast<const T*>(a.query) + row_at + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-            float mul = a.scale < 0.f ? -1.f : 1.f;
-            int e = 0;
-            if (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-                float most = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    float x[8];
-                    unpack16<T>(raw[i], x);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[k]));
-                }
-                if (most > 0.f && most <= 3.402823466e38f) {
-                    int ex;
-                    frexpf(most, &ex);  // most = f * 2^ex, f in [0.5, 1): the row's largest goes to [2^14, 2^15)
-                    e = min(max(15 - ex, -126), 126);
-                }
-                mul *= __int_as_float((e + 127) << 23);
-            }
-            unsigned char* dst = sm.q[t] + r * 128;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                float x[8];
-                unpack16<T>(raw[i], x);
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __half2 y = __floats2half2_rn(x[2 * k] * mul, x[2 * k + 1] * mul);
-                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                *reinterpret_cast<uint4*>(dst + (i / 8) * kPanel + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&sm.q_full[t]);
-            const float qf = fabsf(a.scale) * 1.4426950408889634f * __int_as_float((127 - e) << 23);
+        const int n = p.end - p.begin, my_jobs = (it.jobs + 1 - t) / 2;
+        if (my_jobs == 0) {  // a single tile in a split piece is stream 0's
+            tiles_before += n;
+            continue;
+        }
+        const float undo = stage_query<T, D>(static_cast<const T*>(a.query) + (live ? row_at : 0), live, a.scale < 0.f, sm.q[t], r);
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.q_full[t]);
+        const float qf = fabsf(a.scale) * 1.4426950408889634f * undo;
 
-            float m = -INFINITY, l = 0.f, vref = 0.f;
-            uint32_t nan_cols[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) nan_cols[i] = 0;
-            for (int step = 0; step < my_jobs; ++step, ++steps) {
-                const int local = p.paired ? step : 2 * step + t;
-                const unsigned count = tiles_before + local;
-                const int p0 = (p.begin + local) * kTile, slot = count % kRing;
-                if (!warp_wait(&sm.s_full[t], steps & 1, a.err, abort)) return;
-                tc_fence_after();
-                if (warp_live) {
-                    const unsigned masked_blocks = sm.masked[slot];
-                    const bool whole = __all_sync(0xffffffffu, !live || p0 + kTile - 1 <= bound) && masked_blocks == 0;
-                    // columns of the tile that the row sees
-                    const int cols = min(kTile, bound - p0 + 1);
-                    float top = -INFINITY;
-                    uint32_t s[32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32(s_at + 32 * c, s);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int hb = 0; hb < 2; ++hb) {
-                            const int blk = (32 * c + 16 * hb) / BS;
-                            float x = -INFINITY;
-                            if (whole) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) x = fmaxf(x, __uint_as_float(s[16 * hb + k]));
-                            } else if (!(masked_blocks >> blk & 1)) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    x = fmaxf(x, 32 * c + 16 * hb + k < cols ? __uint_as_float(s[16 * hb + k]) : -INFINITY);
-                            }
-                            if (x != -INFINITY) top = fmaxf(top, x * (sm.ks[slot][blk] * qf));
-                        }
-                    }
-                    // the power of two that P's V scales are relative to
-                    float vmax = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) vmax = fmaxf(vmax, sm.vs[slot][k]);
-                    const float v2 = __int_as_float(__float_as_int(fmaxf(vmax, 7.888609052210118e-31f)) & 0x7f800000);
-                    const float vnew = fmaxf(vref, v2);
-                    const bool rescale = step > 0 && (vnew > vref || top > m + 8.f);
-                    if (step == 0) {
-                        m = top;
-                        vref = vnew;
-                    } else if (__any_sync(0xffffffffu, rescale)) {
-                        const float mn = fmaxf(m, top);
-                        const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-                        const float of = f * (vref / vnew);
-                        l *= f;
-                        m = mn;
-                        vref = vnew;
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            tmem_ld32(o_at + 32 * c, s);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * of);
-                            tmem_st32(o_at + 32 * c, s);
-                        }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const float vinv = __int_as_float(0x7f000000 - __float_as_int(vref));  // 1 / vref, a power of two
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32(s_at + 32 * c, s);
-                        tc_wait_ld();
-                        uint32_t out[16];
-#pragma unroll
-                        for (int hb = 0; hb < 2; ++hb) {
-                            const int blk = (32 * c + 16 * hb) / BS;
-                            const float kf = sm.ks[slot][blk] * qf, vf = sm.vs[slot][blk] * vinv;
-                            const bool gone = masked_blocks >> blk & 1;
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                float x0 = fmaf(__uint_as_float(s[16 * hb + k]), kf, -mu);
-                                float x1 = fmaf(__uint_as_float(s[16 * hb + k + 1]), kf, -mu);
-                                if (!whole) {
-                                    if (gone || 32 * c + 16 * hb + k >= cols) x0 = -INFINITY;
-                                    if (gone || 32 * c + 16 * hb + k + 1 >= cols) x1 = -INFINITY;
-                                }
-                                const float e0 = exp2_approx(x0), e1 = exp2_approx(x1);
-                                l += e0 + e1;
-                                const __half2 h = __floats2half2_rn(e0 * vf, e1 * vf);
-                                out[8 * hb + k / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                            }
-                        }
-                        tmem_st16(s_at + 16 * c, out);
-                    }
-                    if (!whole) {
-                        const unsigned f = 2 * tiles_before + value_fill(p.paired, p.end - p.begin, local);
-                        if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
-                        const int at_slot = count % kNanRing;
-                        if (sm.nan_any[at_slot][0] | sm.nan_any[at_slot][1] | sm.nan_any[at_slot][2] | sm.nan_any[at_slot][3]) {
-                            for (int k = 0; k < cols; ++k)
-                                if (!(masked_blocks >> (k / BS) & 1))
-#pragma unroll
-                                    for (int i = 0; i < D / 32; ++i)
-                                        nan_cols[i] |= (uint32_t)sm.nan_at[at_slot][k][2 * i] | ((uint32_t)sm.nan_at[at_slot][k][2 * i + 1] << 16);
-                        }
-                    }
-                    tc_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[t]);
-            }
-
-            // the piece's result
-            if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+        float m = -INFINITY, l = 0.f, vref = 0.f;
+        bool has_nan = false;
+        for (int step = 0; step < my_jobs; ++step, ++steps) {
+            const int local = p.paired ? step : 2 * step + t;
+            const unsigned count = tiles_before + local;
+            const int p0 = (p.begin + local) * kTile, slot = count % kRing;
+            if (!warp_wait(&sm.s_full[t], steps & 1, a.err, abort)) return;
             tc_fence_after();
-            ++pieces;
-            const bool cut = p.begin > 0 || p.end < p.tiles;
-            float* rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
-            float a0 = 1.f, a1 = 0.f;  // weights of this stream's and stream 1's outputs
-            bool joined = false;
-            if (!p.paired && it.jobs > 1) {
-                // both streams have a part of the same rows: stream 1 leaves its own in the query tiles, which are done with
-                float4* x = reinterpret_cast<float4*>(&sm.q[0][0]);
-                if (t == 1) {
-                    // stream 0's last scores must be done with the tiles as well: its output is issued after them
-                    if (!warp_wait(&sm.x_empty, splits & 1, a.err, abort)) return;
-                    if (warp_live) {
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t s[32];
-                            tmem_ld32(o_at + 32 * c, s);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                float4 y;
-                                float* yf = reinterpret_cast<float*>(&y);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    yf[i] = (nan_cols[c] >> (4 * k + i) & 1) ? __int_as_float(0x7fc00000) : __uint_as_float(s[4 * k + i]) * vref;
-                                x[(8 * c + k) * kTile + r] = y;
-                            }
-                        }
-                        sm.m1[r] = m;
-                        sm.l1[r] = l;
-                    }
-                    tc_fence_before();
-                    mbar_arrive(&sm.x_full);
-                    ++splits;
-                    tiles_before += p.end - p.begin;
-                    // the query tiles may be written again once stream 0 has read them
-                    if (!warp_wait(&sm.x_empty, splits & 1, a.err, abort)) return;
-                    ++splits;
-                    continue;
-                }
-                mbar_arrive(&sm.x_empty);  // stream 0's scores are done
-                if (!warp_wait(&sm.x_full, (splits >> 1) & 1, a.err, abort)) return;
-                if (warp_live) {
-                    const float m1 = sm.m1[r], mn = fmaxf(m, m1);
-                    a0 = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-                    a1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - mn);
-                    // a state that holds NaN without a maximum keeps it
-                    if (l != l) a0 = 1.f;
-                    const float l1 = sm.l1[r];
-                    if (l1 != l1) a1 = 1.f;
-                    l = l * a0 + l1 * a1;
-                    m = mn;
-                    joined = true;
-                }
-            }
             if (warp_live) {
-                const float inv = cut ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-                const float f0 = a0 * vref;
-                const float4* x = reinterpret_cast<const float4*>(&sm.q[0][0]);
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(o_at + 32 * c, s);
+                const unsigned masked = sm.masked[slot];
+                const int cols = min(kTile, bound - p0 + 1);  // columns of the tile that the row sees
+                const bool whole = __all_sync(0xffffffffu, !live || cols == kTile) && masked == 0;
+                float top = -INFINITY;
+                uint32_t s[32];
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(s_at + 32 * c, s);
                     tc_wait_ld();
-                    float o[32];
+                    if (!whole) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = (nan_cols[c] >> k & 1) ? __int_as_float(0x7fc00000) : __uint_as_float(s[k]) * f0;
-                    if (joined) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 y = x[(8 * c + k) * kTile + r];
-                            o[4 * k] += y.x * a1;
-                            o[4 * k + 1] += y.y * a1;
-                            o[4 * k + 2] += y.z * a1;
-                            o[4 * k + 3] += y.w * a1;
-                        }
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= cols || (masked >> ((32 * c + k) / BS) & 1)) s[k] = 0xff800000u;  // -inf
                     }
-                    if (live) {
-                        if (cut) {
-                            float4* d = reinterpret_cast<float4*>(rec + 2 * kTile + (size_t)r * D + 32 * c);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                        } else {
-                            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row_at + 32 * c);
+                    for (int hb = 0; hb < 32 / BS; ++hb) {
+                        float x = -INFINITY;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                T y[8];
+                        for (int k = 0; k < BS; ++k) x = fmaxf(x, __uint_as_float(s[BS * hb + k]));
+                        if (x != -INFINITY) top = fmaxf(top, x * (sm.ks[slot][32 / BS * c + hb] * qf));
+                    }
+                }
+                // the power of two that P's V scales are relative to
+                float vmax = 0.f;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) y[i] = from_float<T>(o[8 * k + i] * inv);
-                                d[k] = *reinterpret_cast<const uint4*>(y);
+                for (int k = 0; k < kTile / BS; ++k) vmax = fmaxf(vmax, sm.vs[slot][k]);
+                const float vnew = fmaxf(vref, __int_as_float(__float_as_int(fmaxf(vmax, 7.888609052210118e-31f)) & 0x7f800000));
+                if (step == 0) {
+                    m = top;
+                    vref = vnew;
+                } else if (__any_sync(0xffffffffu, vnew > vref || top > m + 8.f)) {
+                    const float mn = fmaxf(m, top);
+                    const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                    const float of = f * (vref / vnew);
+                    l *= f;
+                    m = mn;
+                    vref = vnew;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        tmem_ld32(o_at + 32 * c, s);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * of);
+                        tmem_st32(o_at + 32 * c, s);
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+                const float vinv = __int_as_float(0x7f000000 - __float_as_int(vref));  // 1 / vref, a power of two
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(s_at + 32 * c, s);
+                    tc_wait_ld();
+                    uint32_t out[16];
+#pragma unroll
+                    for (int hb = 0; hb < 32 / BS; ++hb) {
+                        const float kf = sm.ks[slot][32 / BS * c + hb] * qf, vf = sm.vs[slot][32 / BS * c + hb] * vinv;
+#pragma unroll
+                        for (int k = 0; k < BS; k += 2) {
+                            const int i = BS * hb + k;
+                            const float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf, kf),
+                                                  make_float2(-mu, -mu));
+                            s[i] = __float_as_uint(x.x);
+                            s[i + 1] = __float_as_uint(x.y);
+                        }
+                        if (!whole) {
+#pragma unroll
+                            for (int k = 0; k < BS; ++k) {
+                                const int i = BS * hb + k;
+                                if (32 * c + i >= cols || (masked >> (32 / BS * c + hb) & 1)) s[i] = 0xff800000u;
                             }
                         }
+#pragma unroll
+                        for (int k = 0; k < BS; k += 2) {
+                            const int i = BS * hb + k;
+                            const float2 e = make_float2(exp2_approx(__uint_as_float(s[i])), exp2_approx(__uint_as_float(s[i + 1])));
+                            sum = add2(sum, e);
+                            const float2 w = mul2(e, make_float2(vf, vf));
+                            const __half2 h = __floats2half2_rn(w.x, w.y);
+                            out[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                    tmem_st16(s_at + 16 * c, out);
+                }
+                l += sum.x + sum.y;
+                if (!whole) {
+                    const unsigned f = 2 * tiles_before + value_fill(p.paired, n, local);
+                    if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
+                    const int at_slot = count % kNanRing;
+                    if (sm.nan_any[at_slot][0] | sm.nan_any[at_slot][1] | sm.nan_any[at_slot][2] | sm.nan_any[at_slot][3]) {
+#pragma unroll 1
+                        for (int i = 0; i < D / 32; ++i) {
+                            uint32_t bits = has_nan ? sm.nan_row[t][r][i] : 0u;
+#pragma unroll 1
+                            for (int k = 0; k < cols; ++k)
+                                if (!(masked >> (k / BS) & 1))
+                                    bits |= (uint32_t)sm.nan_at[at_slot][k][2 * i] | ((uint32_t)sm.nan_at[at_slot][k][2 * i + 1] << 16);
+                            sm.nan_row[t][r][i] = bits;
+                        }
+                        has_nan = true;
                     }
                 }
-                if (cut && live) {
-                    rec[r] = m;
-                    rec[kTile + r] = l;
-                }
-            }
-            if (!p.paired && it.jobs > 1) {
-                mbar_arrive(&sm.x_empty);
-                // nobody writes query tiles before all of stream 0 has read the output that lies there
-                if (!warp_wait(&sm.x_empty, 1, a.err, abort)) return;
-                splits += 2;
+                tc_wait_st();
             }
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[t]);
         }
-        tiles_before += p.end - p.begin;
+
+        // The piece's result.  In a split piece both streams have a part of the same rows: stream 1 leaves its own in the query
+        // tiles, once stream 0's scores are done with them too, and stream 0 joins the two.
+        if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+        tc_fence_after();
+        ++pieces;
+        const bool join = !p.paired && it.jobs > 1, give = join && t == 1, take = join && t == 0;
+        const bool cut = p.begin > 0 || p.end < p.tiles;
+        float* rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
+        float4* exchange = reinterpret_cast<float4*>(&sm.q[0][0]);
+        float f0 = vref, f1 = 0.f;  // factors of this stream's and of stream 1's output
+        if (give) {
+            if (!warp_wait(&sm.x_empty, splits & 1, a.err, abort)) return;
+            sm.m1[r] = m;
+            sm.l1[r] = l;
+        }
+        if (take) {
+            mbar_arrive(&sm.x_empty);
+            if (!warp_wait(&sm.x_full, (splits >> 1) & 1, a.err, abort)) return;
+            const float m1 = sm.m1[r], l1 = sm.l1[r], mn = fmaxf(m, m1);
+            // a state without a maximum is empty, unless its sum is NaN
+            const float a0 = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2_approx(m - mn);
+            f1 = m1 == -INFINITY ? (l1 != l1 ? 1.f : 0.f) : exp2_approx(m1 - mn);
+            f0 = vref * a0;
+            l = l * a0 + l1 * f1;
+            m = mn;
+        }
+        if (warp_live) {
+            const float inv = cut || give ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            uint32_t s[32];
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                tmem_ld32(o_at + 32 * c, s);
+                tc_wait_ld();
+                const uint32_t nan = has_nan ? sm.nan_row[t][r][c] : 0u;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint((nan >> k & 1) ? quiet_nan() : __uint_as_float(s[k]) * f0);
+                if (take) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 y = exchange[(8 * c + k) * kTile + r];
+                        s[4 * k] = __float_as_uint(fmaf(y.x, f1, __uint_as_float(s[4 * k])));
+                        s[4 * k + 1] = __float_as_uint(fmaf(y.y, f1, __uint_as_float(s[4 * k + 1])));
+                        s[4 * k + 2] = __float_as_uint(fmaf(y.z, f1, __uint_as_float(s[4 * k + 2])));
+                        s[4 * k + 3] = __float_as_uint(fmaf(y.w, f1, __uint_as_float(s[4 * k + 3])));
+                    }
+                }
+                if (give || cut) {
+                    uint4* d = give ? reinterpret_cast<uint4*>(exchange + 8 * c * kTile + r)
+                                    : reinterpret_cast<uint4*>(rec + 2 * kTile + (size_t)r * D + 32 * c);
+                    const int step = give ? kTile : 1;
+                    if (give || live) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[k * step] = make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
+                    }
+                } else if (live) {
+                    uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row_at + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        T y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = from_float<T>(__uint_as_float(s[8 * k + i]) * inv);
+                        d[k] = *reinterpret_cast<const uint4*>(y);
+                    }
+                }
+            }
+            if (cut && live && !give) {
+                rec[r] = m;
+                rec[kTile + r] = l;
+            }
+        }
+        tc_fence_before();
+        if (join) {
+            // nobody writes query tiles before all of stream 0 has read the output that lies there
+            if (give)
+                mbar_arrive(&sm.x_full);
+            else
+                mbar_arrive(&sm.x_empty);
+            if (!warp_wait(&sm.x_empty, 1, a.err, abort)) return;
+            splits += 2;
+        }
+        tiles_before += n;
     }
 }
 
