@@ -117,15 +117,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
@@ -404,12 +402,11 @@ __device__ __forceinline__ void widen_store(unsigned char* unit0, unsigned char*
     uint32_t h[8];
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] & 0xffffu), __NV_E4M3);
-        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> 16), __NV_E4M3);
-        h[2 * i] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
-        h[2 * i + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
-    }
+    for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+            : "r"(w[i]));
     *reinterpret_cast<uint4*>(unit0) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(unit1) = make_uint4(h[4], h[5], h[6], h[7]);
 }
@@ -524,50 +521,48 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
             if (!warp_wait(&sm.raw_full[slot], (fills / RAW) & 1, a.err, &sm.abort)) return;
             const unsigned present = sm.present[(tiles + f.tile) % kRing];
             const int left = it.L - p0;  // rows of the tile inside the context; the others' codes may be anything
-            uint4 c[N];
+            if (!warp_wait(&sm.kv_empty[buf], ((fills / kBuffers) & 1) ^ 1, a.err, &sm.abort)) return;
+            const unsigned char* from = sm.raw[slot] + row0 * D + chunk * 16;
+            unsigned char *to0 = sm.kv[buf] + unit0, *to1 = sm.kv[buf] + unit1;
+            const bool seen_in_part = p0 + kTile - 1 > seen_by_all;
+            if (left >= kTile && present == (1u << (kTile / BS)) - 1 && !(f.value && seen_in_part)) {
+#pragma unroll 1
+                for (int k = 0; k < N; k += 4) {
+                    uint4 c[4];
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int r = row0 + k * RPP;
-                c[k] = *reinterpret_cast<const uint4*>(sm.raw[slot] + r * D + chunk * 16);
-            }
-            if (left < kTile || present != (1u << (kTile / BS)) - 1) {
+                    for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(from + (k + j) * RPP * D);
 #pragma unroll
+                    for (int j = 0; j < 4; ++j) widen_store(to0 + (k + j) * RPP * 128, to1 + (k + j) * RPP * 128, c[j]);
+                }
+                if (f.value && lane == 0) sm.nan_any[(tiles + f.tile) % kNanRing][tid >> 5] = 0;
+            } else {
+                // Rows past the context are zeros.  Where some row sees the tile in part, a NaN of V behind its position must not
+                // reach it through 0 * NaN: NaN become zeros too, and the softmax warps are told where they were.
+                const int at_slot = (tiles + f.tile) % kNanRing;
+                bool any = false;
+#pragma unroll 1
                 for (int k = 0; k < N; ++k) {
                     const int r = row0 + k * RPP;
-                    if (r >= left || !(present >> (r / BS) & 1)) c[k] = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-            if (!warp_wait(&sm.kv_empty[buf], ((fills / kBuffers) & 1) ^ 1, a.err, &sm.abort)) return;
-            if (f.value) {
-                bool any = false;
-                const int at_slot = (tiles + f.tile) % kNanRing;
-                if (p0 + kTile - 1 > seen_by_all) {
-                    // Some row sees this tile in part: a NaN behind its position must not reach it through 0 * NaN.
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        if (!(nan_bytes(c[k].x) | nan_bytes(c[k].y) | nan_bytes(c[k].z) | nan_bytes(c[k].w))) {
-                            sm.nan_at[at_slot][row0 + k * RPP][chunk] = 0;
-                            continue;
-                        }
+                    uint4 c = *reinterpret_cast<const uint4*>(from + k * RPP * D);
+                    if (r >= left || !(present >> (r / BS) & 1)) c = make_uint4(0u, 0u, 0u, 0u);
+                    if (f.value && seen_in_part) {
                         unsigned at = 0;
                         auto clean = [&](uint32_t w, int j) {
                             const uint32_t t = nan_bytes(w) >> 7;
                             at |= ((t * 0x01020408u >> 24) & 0xfu) << (4 * j);
                             return w & ~(t * 0xffu);
                         };
-                        c[k] = make_uint4(clean(c[k].x, 0), clean(c[k].y, 1), clean(c[k].z, 2), clean(c[k].w, 3));
+                        c = make_uint4(clean(c.x, 0), clean(c.y, 1), clean(c.z, 2), clean(c.w, 3));
                         any |= at != 0;
-                        sm.nan_at[at_slot][row0 + k * RPP][chunk] = (uint16_t)at;
+                        sm.nan_at[at_slot][r][chunk] = (uint16_t)at;
                     }
+                    widen_store(to0 + k * RPP * 128, to1 + k * RPP * 128, c);
                 }
                 any = __any_sync(0xffffffffu, any);
-                if (lane == 0) sm.nan_any[at_slot][tid >> 5] = any;
+                if (f.value && lane == 0) sm.nan_any[at_slot][tid >> 5] = any;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.raw_empty[slot]);
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                widen_store(sm.kv[buf] + unit0 + k * RPP * 128, sm.kv[buf] + unit1 + k * RPP * 128, c[k]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.kv_full[buf]);
@@ -595,7 +590,7 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
                 if (!wait_for(&sm.p_full[t], (t ? steps1++ : steps0++) & 1, a.err, abort)) return;
                 tc_fence_after();
                 const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < kTile / 16; ++k)
                     mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
                 if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
@@ -609,7 +604,7 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
                 if (next < 2 && !wait_for(&sm.q_full[t], (t ? pieces1 : pieces0) & 1, a.err, abort)) return;
                 tc_fence_after();
                 const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
                     mma_ss(tmem + t * kTile, qd + off, kd + off, idesc_of(kTile, false), k > 0);
@@ -680,8 +675,75 @@ __device__ __forceinline__ float stage_query(const T* src, bool live, bool negat
     return __int_as_float((127 - e) << 23);
 }
 
-// A softmax warp: 32 rows of a stream's row tile, one per lane.  Its code is kept short (loops over 32 columns that are not
-// unrolled further): five roles run at once, and what the instruction caches cannot hold costs more than the loops.
+// The largest score of a lane's row in one key tile, scales applied.  WHOLE: the row sees all of it.
+// This loop, row_exp() and the one in widen_tiles() run all the time, on every scheduler next to one another: they are short, so
+// that they stay in the instruction caches together.  Straight code over the 128 columns took five times its issue time.
+template <int BS, bool WHOLE>
+__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float qf, int cols, unsigned masked) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(s_at + c, s);
+        float kf[32 / BS];
+#pragma unroll
+        for (int h = 0; h < 32 / BS; ++h) kf[h] = ks[c / BS + h] * qf;
+        tc_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 32 / BS; ++h) {
+            float x = -INFINITY, y = -INFINITY;  // two chains
+#pragma unroll
+            for (int k = 0; k < BS; k += 2) {
+                const int i = BS * h + k;
+                if (!WHOLE && (c + i >= cols || (masked >> (c / BS + h) & 1))) s[i] = 0xff800000u;  // -inf
+                if (!WHOLE && (c + i + 1 >= cols || (masked >> (c / BS + h) & 1))) s[i + 1] = 0xff800000u;
+                x = fmaxf(x, __uint_as_float(s[i]));
+                y = fmaxf(y, __uint_as_float(s[i + 1]));
+            }
+            x = fmaxf(x, y);
+            top = fmaxf(top, x == -INFINITY ? x : x * kf[h]);
+        }
+    }
+    return top;
+}
+
+// P of a lane's row in one key tile: exp2(score - mu) times the block's V scale, as f16 over the scores that it comes from; returns
+// the sum of the exponentials.
+template <int BS, bool WHOLE>
+__device__ __forceinline__ float row_exp(uint32_t s_at, const float* ks, const float* vs, float qf, float mu, float vinv, int cols,
+                                         unsigned masked) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t s[32], out[16];
+        tmem_ld32(s_at + c, s);
+        float kf[32 / BS], vf[32 / BS];
+#pragma unroll
+        for (int h = 0; h < 32 / BS; ++h) {
+            kf[h] = ks[c / BS + h] * qf;
+            vf[h] = vs[c / BS + h] * vinv;
+        }
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const int h = i / BS;
+            float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf[h], kf[h]),
+                            make_float2(-mu, -mu));
+            if (!WHOLE && (c + i >= cols || (masked >> (c / BS + h) & 1))) x.x = -INFINITY;
+            if (!WHOLE && (c + i + 1 >= cols || (masked >> (c / BS + h) & 1))) x.y = -INFINITY;
+            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum = add2(sum, e);
+            const float2 w = mul2(e, make_float2(vf[h], vf[h]));
+            const __half2 p = __floats2half2_rn(w.x, w.y);
+            out[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        tmem_st16(s_at + c / 2, out);
+    }
+    return sum.x + sum.y;
+}
+
+// A softmax warp: 32 rows of a stream's row tile, one per lane.  What runs once in a piece is
+// kept short (loops that are not unrolled): five roles run at once, and code that the instruction caches cannot hold is slow.
 template <typename T, int D, int BS>
 __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -721,25 +783,8 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                 const unsigned masked = sm.masked[slot];
                 const int cols = min(kTile, bound - p0 + 1);  // columns of the tile that the row sees
                 const bool whole = __all_sync(0xffffffffu, !live || cols == kTile) && masked == 0;
-                float top = -INFINITY;
-                uint32_t s[32];
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(s_at + 32 * c, s);
-                    tc_wait_ld();
-                    if (!whole) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * c + k >= cols || (masked >> ((32 * c + k) / BS) & 1)) s[k] = 0xff800000u;  // -inf
-                    }
-#pragma unroll
-                    for (int hb = 0; hb < 32 / BS; ++hb) {
-                        float x = -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < BS; ++k) x = fmaxf(x, __uint_as_float(s[BS * hb + k]));
-                        if (x != -INFINITY) top = fmaxf(top, x * (sm.ks[slot][32 / BS * c + hb] * qf));
-                    }
-                }
+                float top = whole ? row_max<BS, true>(s_at, sm.ks[slot], qf, cols, masked)
+                                  : row_max<BS, false>(s_at, sm.ks[slot], qf, cols, masked);
                 // the power of two that P's V scales are relative to
                 float vmax = 0.f;
 #pragma unroll
@@ -756,53 +801,19 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                     m = mn;
                     vref = vnew;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        tmem_ld32(o_at + 32 * c, s);
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + 16 * c, o);
                         tc_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * of);
-                        tmem_st32(o_at + 32 * c, s);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * of);
+                        tmem_st16(o_at + 16 * c, o);
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
                 const float vinv = __int_as_float(0x7f000000 - __float_as_int(vref));  // 1 / vref, a power of two
-                float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(s_at + 32 * c, s);
-                    tc_wait_ld();
-                    uint32_t out[16];
-#pragma unroll
-                    for (int hb = 0; hb < 32 / BS; ++hb) {
-                        const float kf = sm.ks[slot][32 / BS * c + hb] * qf, vf = sm.vs[slot][32 / BS * c + hb] * vinv;
-#pragma unroll
-                        for (int k = 0; k < BS; k += 2) {
-                            const int i = BS * hb + k;
-                            const float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf, kf),
-                                                  make_float2(-mu, -mu));
-                            s[i] = __float_as_uint(x.x);
-                            s[i + 1] = __float_as_uint(x.y);
-                        }
-                        if (!whole) {
-#pragma unroll
-                            for (int k = 0; k < BS; ++k) {
-                                const int i = BS * hb + k;
-                                if (32 * c + i >= cols || (masked >> (32 / BS * c + hb) & 1)) s[i] = 0xff800000u;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < BS; k += 2) {
-                            const int i = BS * hb + k;
-                            const float2 e = make_float2(exp2_approx(__uint_as_float(s[i])), exp2_approx(__uint_as_float(s[i + 1])));
-                            sum = add2(sum, e);
-                            const float2 w = mul2(e, make_float2(vf, vf));
-                            const __half2 h = __floats2half2_rn(w.x, w.y);
-                            out[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                    }
-                    tmem_st16(s_at + 16 * c, out);
-                }
-                l += sum.x + sum.y;
+                l += whole ? row_exp<BS, true>(s_at, sm.ks[slot], sm.vs[slot], qf, mu, vinv, cols, masked)
+                           : row_exp<BS, false>(s_at, sm.ks[slot], sm.vs[slot], qf, mu, vinv, cols, masked);
                 if (!whole) {
                     const unsigned f = 2 * tiles_before + value_fill(p.paired, n, local);
                     if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
@@ -949,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
         widen_tiles<D, BS>(a, ws, sm);
     } else if (warp == kCopyWarp) {
         copy_tiles<D, BS>(a, ws, sm);
-    } else if ((threadIdx.x & 31) == 0) {
+    } else if (warp == kIssueWarp && (threadIdx.x & 31) == 0) {
         issue_products<D>(a, ws, sm);
         if (sm.abort) {  // products still in flight read shared and tensor memory
             int never = 0;
