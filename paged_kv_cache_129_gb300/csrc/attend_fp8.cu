@@ -8,7 +8,7 @@
 // softmax warps, so that one's exponentials run under the other's products:
 //   paired  two row tiles share every key tile (it is widened once for both);
 //   split   a single row tile (few rows: verification, decode, the rest of a run): the streams take alternate key
-//           tiles and are joined in shared memory.
+//           tiles, and join their results at the end.
 // Work.  A unit is (request, pair of row tiles, kv head).  All units' key tiles are laid end to end, weighted by their
 // cost, and cut into one equal contiguous share per SM, so every SM works equally long whatever the length mix; units cut by a
 // share boundary leave float32 partial results (two slots per CTA), joined by a third kernel.
@@ -33,8 +33,10 @@ namespace {
 constexpr int kTile = 128;             // rows of a row tile, tokens of a key tile
 constexpr int kSoftmaxWarps = 8;       // four per stream
 constexpr int kWidenWarps = 4;
-constexpr int kIssueWarp = kSoftmaxWarps + kWidenWarps, kCopyWarp = kIssueWarp + 1;
+constexpr int kIssueWarp = kSoftmaxWarps + kWidenWarps;  // two, one per stream
+constexpr int kCopyWarp = kIssueWarp + 2;
 constexpr int kThreads = (kCopyWarp + 1) * 32;
+constexpr int kAhead = 4;              // key tiles whose codes are on their way into L2 before they are copied
 constexpr int kBuffers = 3;            // f16 operand tiles (K or V) in shared memory
 constexpr int kRing = 8;               // slots of per-tile side data (scales), see copy_tiles()
 constexpr int kNanRing = 4;
@@ -145,6 +147,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned s
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
                  "l"(src), "r"(size), "r"(smem_addr(bar))
                  : "memory");
+}
+
+__device__ __forceinline__ void bulk_prefetch(const void* src, unsigned size) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(size) : "memory");
 }
 
 // Operand tiles in shared memory: panels of 64 elements (128 bytes) by 128 rows, 128-byte swizzle (16-byte unit u of row r
@@ -282,6 +288,12 @@ __device__ __forceinline__ int find_entry(const Entry* e, int n, long long x) {
     return lo;
 }
 
+// Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).
+__device__ __forceinline__ int tiles_in(long long x, int tiles, bool paired) {
+    const unsigned cost = (unsigned)min(x, (long long)tiles * (paired ? kPairedCost : kSplitCost));
+    return (int)(paired ? (cost + kPairedCost - 1) / kPairedCost : (cost + kSplitCost - 1) / kSplitCost);
+}
+
 // The part of one unit that a share covers: key tiles [begin, end) of `tiles`.
 struct Piece {
     int seq, row0, kvh, tiles, begin, end;
@@ -316,8 +328,8 @@ struct Walk {
             p->kvh = kvh;
             p->tiles = x.tiles;
             p->paired = x.paired != 0;
-            p->begin = (int)((from + w - 1) / w);
-            p->end = (int)min((long long)x.tiles, (to + w - 1) / w);
+            p->begin = tiles_in(from, x.tiles, p->paired);
+            p->end = tiles_in(to, x.tiles, p->paired);
             pos = unit + (long long)x.tiles * w;
             if (++kvh == heads) {
                 kvh = 0;
@@ -335,7 +347,7 @@ template <int D>
 struct Smem {
     static constexpr int kOperand = kTile * D * 2;      // one f16 tile
     static constexpr int kRaw = D == 128 ? 3 : 6;       // tiles of codes on their way or waiting: 48 KB in flight per SM
-    unsigned char q[2][kOperand];                       // at the end of a split piece: stream 1's output
+    unsigned char q[2][kOperand];
     unsigned char kv[kBuffers][kOperand];
     unsigned char raw[kRaw][kTile * D];
     float ks[kRing][8], vs[kRing][8];                   // scales of the tile's blocks
@@ -343,9 +355,9 @@ struct Smem {
     unsigned nan_any[kNanRing][kWidenWarps];            // whether a warp found NaN in V of a tile that some row sees in part,
     uint16_t nan_at[kNanRing][kTile][D / 16];           // and where: per token and 16 elements
     uint32_t nan_row[2][kTile][D / 32];                 // per row: elements of the output that are NaN, if its thread says so
-    float m1[kTile], l1[kTile];                         // stream 1's state at the end of a split piece
+    float4 state[2][kTile];                             // at the end of a split piece: both streams' m, l, vref, has_nan
     uint64_t q_full[2], raw_full[kRaw], raw_empty[kRaw], kv_full[kBuffers], kv_empty[kBuffers];
-    uint64_t s_full[2], p_full[2], o_full[2], x_full, x_empty, drain;
+    uint64_t s_full[2], p_full[2], o_full[2], join_full, join_done, drain[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -416,7 +428,8 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7
 
 // The copy warp: every block's K or V rows (contiguous) into the raw ring by one bulk copy per block, a lane each, and the tile's
 // scales into the side ring.  Registers and L1 could not hold what has to be in flight: with 206 KB of shared memory taken, L1
-// has room for about 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.
+// has room for about 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.  Three tiles of the ring do not cover the latency of
+// HBM either: tiles further ahead are prefetched into L2, and the copies take L2's latency.
 // Side data of tile i sits in slot i % 8.  When K of tile i is copied, the raw slot that it takes was widened, so the f16 buffer
 // three fills before that one was free: scores of tile i - 3 at least are done, so the softmax of tile i - 5, and slot i % 8 is
 // tile i - 8's.
@@ -436,7 +449,15 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
         // Lane j < BLOCKS has block j of a tile: its id, one tile ahead of its use, then scales and record.
         auto wanted = [&](int tile) { return lane < BLOCKS && tile < n && (p.begin + tile) * BLOCKS + lane < used; };
         auto fetch = [&](int tile) { return wanted(tile) ? table[(p.begin + tile) * BLOCKS + lane] : -1; };
-        int next_id = fetch(0);
+        auto prefetch = [&](int id) {
+            if (id < 0 || id >= a.num_blocks) return;
+            const size_t r = (size_t)id * a.num_kv_heads + p.kvh;
+            bulk_prefetch(a.key_cache + r * stride, (both ? 2 : 1) * BS * D);
+            if (!both) bulk_prefetch(a.value_cache + r * stride, BS * D);
+        };
+        int next_id = fetch(0), ahead_id = fetch(kAhead);
+#pragma unroll 1
+        for (int i = 1; i < kAhead; ++i) prefetch(fetch(i));
         size_t rec[2] = {0, 0};  // of even and odd tiles: V of a tile is copied after K of the next one
         bool have[2] = {false, false};
         for (int i = 0; i < 2 * n; ++i, ++fills) {
@@ -447,6 +468,8 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
             if (!f.value) {
                 const int id = next_id;
                 next_id = fetch(f.tile + 1);
+                prefetch(ahead_id);
+                ahead_id = fetch(f.tile + 1 + kAhead);
                 const bool in = id >= 0 && id < a.num_blocks && wanted(f.tile);
                 bad = wanted(f.tile) && !in;
                 const size_t r = (size_t)(in ? id : 0) * a.num_kv_heads + p.kvh;
@@ -571,51 +594,65 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
     }
 }
 
-// One thread issues every product.  Job j of a piece is a score tile of stream j % 2; its scores are issued two jobs ahead of
-// its output, right behind the output of the stream's previous job, which has then read the P that the scores overwrite.
+// One thread per stream issues its products; while one waits, the other's keep the tensor cores busy.  Job j of a piece is a
+// score tile of stream j % 2; its scores are issued right behind the output of the stream's previous job, which has then read
+// the P that they overwrite.
 template <int D>
-__device__ __forceinline__ void issue_products(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+__device__ __forceinline__ void issue_products(const AttendArgs& a, const Workspace& ws, Smem<D>& sm, int t) {
     volatile int* abort = &sm.abort;
-    const uint32_t tmem = sm.tmem;
+    const uint32_t s_at = sm.tmem + t * kTile, o_at = sm.tmem + 2 * kTile + t * D;
+    const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024);
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
-    unsigned fills = 0, pieces0 = 0, pieces1 = 0, steps0 = 0, steps1 = 0;
+    unsigned fills = 0, pieces = 0, steps = 0;
     while (walk.next(&p)) {
         const int n = p.end - p.begin, jobs = n * (p.paired ? 2 : 1);
-        for (int j = -2; j < jobs; ++j) {
+        // A buffer is free after two arrivals: one from either stream, or two from the only one that reads it.  A wait tells a
+        // phase from the one before it alone, so no thread may skip a buffer's turn without knowing that it came: within a
+        // piece the fills that a stream waits for are at most three apart, and a piece of one tile, stream 0's, is waited for
+        // and released by stream 1 too.
+        const bool alone = !p.paired && jobs > 1;
+        auto release = [&](unsigned buf) {
+            tc_commit(&sm.kv_empty[buf]);
+            if (alone) tc_commit(&sm.kv_empty[buf]);
+        };
+        if (jobs <= t) {
+            for (unsigned f = fills; f < fills + 2; ++f) {
+                if (!wait_for(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
+                mbar_arrive(&sm.kv_empty[f % kBuffers]);
+            }
+        }
+#pragma unroll 1
+        for (int j = t - 2; j < jobs; j += 2) {
             if (j >= 0) {
-                const int t = j & 1;
                 const unsigned f = fills + value_fill(p.paired, n, p.paired ? j >> 1 : j), buf = f % kBuffers;
                 if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-                if (!wait_for(&sm.p_full[t], (t ? steps1++ : steps0++) & 1, a.err, abort)) return;
+                if (!wait_for(&sm.p_full[t], steps++ & 1, a.err, abort)) return;
                 tc_fence_after();
                 const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
 #pragma unroll 2
                 for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
-                if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
+                    mma_ts(o_at, s_at + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
+                release(buf);
                 if (j + 2 >= jobs) tc_commit(&sm.o_full[t]);
             }
             const int next = j + 2;
             if (next < jobs) {
-                const int t = next & 1;
                 const unsigned f = fills + key_fill(p.paired, p.paired ? next >> 1 : next), buf = f % kBuffers;
                 if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-                if (next < 2 && !wait_for(&sm.q_full[t], (t ? pieces1 : pieces0) & 1, a.err, abort)) return;
+                if (next < 2 && !wait_for(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
                 tc_fence_after();
-                const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
+                const uint64_t kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
 #pragma unroll 2
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
-                    mma_ss(tmem + t * kTile, qd + off, kd + off, idesc_of(kTile, false), k > 0);
+                    mma_ss(s_at, qd + off, kd + off, idesc_of(kTile, false), k > 0);
                 }
-                if (!p.paired || t == 1) tc_commit(&sm.kv_empty[buf]);
+                release(buf);
                 tc_commit(&sm.s_full[t]);
             }
         }
         fills += 2 * n;
-        ++pieces0;
-        if (jobs > 1) ++pieces1;
     }
 }
 
@@ -637,7 +674,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         "l"(*reinterpret_cast<uint64_t*>(&b)));
     return d;
 }
-__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 
 // A query row to f16 in the swizzled tile; returns what undoes its power of two.
 template <typename T, int D>
@@ -742,49 +778,157 @@ __device__ __forceinline__ float row_exp(uint32_t s_at, const float* ks, const f
     return sum.x + sum.y;
 }
 
-// A softmax warp: 32 rows of a stream's row tile, one per lane.  What runs once in a piece is
-// kept short (loops that are not unrolled): five roles run at once, and code that the instruction caches cannot hold is slow.
+// A softmax warp: 32 rows of a stream's row tile, one per lane.
 template <typename T, int D, int BS>
 __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
     volatile int* abort = &sm.abort;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = sm.tmem + lanes + t * kTile, o_at = sm.tmem + lanes + 2 * kTile + t * D;
+    const uint32_t other_o_at = sm.tmem + lanes + 2 * kTile + (t ^ 1) * D;
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
-    Piece p;
-    unsigned pieces = 0, steps = 0, splits = 0, tiles_before = 0;  // so far
-    while (walk.next(&p)) {
-        const Item it = item_of(a, p);
-        const int first = p.row0 + (p.paired ? t * kTile : 0);
-        const int v = first + r;  // row of the request
-        const bool live = v < it.rows, warp_live = first + (warp & 3) * 32 < it.rows;
-        const int token = live ? v / it.group : 0;
-        const int bound = live ? it.L - it.n + token : -1;  // last position that the row sees
-        const size_t row_at = ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D;
-        const int n = p.end - p.begin, my_jobs = (it.jobs + 1 - t) / 2;
-        if (my_jobs == 0) {  // a single tile in a split piece is stream 0's
+    unsigned pieces = 0, steps = 0, joins = 0, tiles_before = 0;  // so far
+    // what the result of a piece needs; it is written after the next piece's queries are staged, which waits for nothing
+    struct Result {
+        size_t row_at;
+        float* rec;
+        bool live, warp_live, cut, join;
+    } res{};
+    float m = -INFINITY, l = 0.f, vref = 0.f;
+    bool has_nan = false, pending = false;
+#pragma unroll 1
+    for (;;) {
+        Piece p;
+        Item it{};
+        int n = 0, my_jobs = 0, bound = -1;
+        float qf = 0.f;
+        Result now{};
+        const bool have = walk.next(&p);
+        if (have) {
+            it = item_of(a, p);
+            n = p.end - p.begin;
+            my_jobs = (it.jobs + 1 - t) / 2;
+            if (my_jobs == 0 && !pending) {  // a single tile in a split piece is stream 0's
+                tiles_before += n;
+                continue;
+            }
+            const int first = p.row0 + (p.paired ? t * kTile : 0), v = first + r;  // row of the request
+            const int token = v / it.group;
+            now.live = v < it.rows;
+            now.warp_live = first + (warp & 3) * 32 < it.rows;
+            now.cut = p.begin > 0 || p.end < p.tiles;
+            now.join = !p.paired && it.jobs > 1;
+            now.rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
+            now.row_at = now.live ? ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D : 0;
+            if (now.live) bound = it.L - it.n + token;  // last position that the row sees
+            if (my_jobs > 0) {
+                // the stream's last scores were waited for, so its query tile is free
+                const float undo =
+                    stage_query<T, D>(static_cast<const T*>(a.query) + now.row_at, now.live, a.scale < 0.f, sm.q[t], r);
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.q_full[t]);
+                qf = fabsf(a.scale) * 1.4426950408889634f * undo;
+            }
+        }
+
+        if (pending) {  // the previous piece's result
+            if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+            tc_fence_after();
+            ++pieces;
+            float f0 = vref, f1 = 0.f;  // factors of this stream's output and of the other's
+            uint32_t nan_from = has_nan ? 1u << t : 0u;
+            if (res.join) {  // both streams have a part of the same rows, in the same lanes of tensor memory
+                sm.state[t][r] = make_float4(m, l, vref, has_nan ? 1.f : 0.f);
+                tc_fence_before();
+                mbar_arrive(&sm.join_full);
+                if (!warp_wait(&sm.join_full, joins & 1, a.err, abort)) return;
+                tc_fence_after();
+                const float4 o = sm.state[t ^ 1][r];
+                const float mn = fmaxf(m, o.x);
+                // a state without a maximum is empty, unless its sum is NaN
+                const float w0 = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2_approx(m - mn);
+                const float w1 = o.x == -INFINITY ? (o.y != o.y ? 1.f : 0.f) : exp2_approx(o.x - mn);
+                f0 = vref * w0;
+                f1 = o.z * w1;
+                l = l * w0 + o.y * w1;
+                m = mn;
+                if (o.w != 0.f) nan_from |= 2u >> t;
+            }
+            if (res.warp_live) {
+                const float inv = res.cut ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                const int c0 = res.join ? t * (D / 2) : 0, c1 = res.join ? c0 + D / 2 : D;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    uint32_t s[32];
+                    tmem_ld32(o_at + c, s);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
+                    if (res.join) {
+                        uint32_t o[32];
+                        tmem_ld32(other_o_at + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k])));
+                    }
+                    if (nan_from) {
+                        const uint32_t nan = (nan_from & 1 ? sm.nan_row[0][r][c / 32] : 0u) | (nan_from & 2 ? sm.nan_row[1][r][c / 32] : 0u);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (nan >> k & 1) s[k] = 0x7fc00000u;
+                    }
+                    if (res.live && res.cut) {
+                        uint4* d = reinterpret_cast<uint4*>(res.rec + 2 * kTile + (size_t)r * D + c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[k] = make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
+                    } else if (res.live) {
+                        uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + res.row_at + c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            T y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = from_float<T>(__uint_as_float(s[8 * k + i]) * inv);
+                            d[k] = *reinterpret_cast<const uint4*>(y);
+                        }
+                    }
+                }
+                if (res.cut && res.live && c0 == 0) {
+                    res.rec[r] = m;
+                    res.rec[kTile + r] = l;
+                }
+            }
+            tc_fence_before();
+            if (res.join) {  // neither stream's output is written again before both have read it
+                mbar_arrive(&sm.join_done);
+                if (!warp_wait(&sm.join_done, joins & 1, a.err, abort)) return;
+                ++joins;
+            }
+            pending = false;
+        }
+        if (!have) return;
+        if (my_jobs == 0) {
             tiles_before += n;
             continue;
         }
-        const float undo = stage_query<T, D>(static_cast<const T*>(a.query) + (live ? row_at : 0), live, a.scale < 0.f, sm.q[t], r);
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.q_full[t]);
-        const float qf = fabsf(a.scale) * 1.4426950408889634f * undo;
 
-        float m = -INFINITY, l = 0.f, vref = 0.f;
-        bool has_nan = false;
+        res = now;
+        pending = true;
+        m = -INFINITY;
+        l = vref = 0.f;
+        has_nan = false;
+#pragma unroll 1
         for (int step = 0; step < my_jobs; ++step, ++steps) {
             const int local = p.paired ? step : 2 * step + t;
             const unsigned count = tiles_before + local;
             const int p0 = (p.begin + local) * kTile, slot = count % kRing;
             if (!warp_wait(&sm.s_full[t], steps & 1, a.err, abort)) return;
             tc_fence_after();
-            if (warp_live) {
+            if (now.warp_live) {
                 const unsigned masked = sm.masked[slot];
                 const int cols = min(kTile, bound - p0 + 1);  // columns of the tile that the row sees
-                const bool whole = __all_sync(0xffffffffu, !live || cols == kTile) && masked == 0;
-                float top = whole ? row_max<BS, true>(s_at, sm.ks[slot], qf, cols, masked)
-                                  : row_max<BS, false>(s_at, sm.ks[slot], qf, cols, masked);
+                const bool whole = __all_sync(0xffffffffu, !now.live || cols == kTile) && masked == 0;
+                const float top = whole ? row_max<BS, true>(s_at, sm.ks[slot], qf, cols, masked)
+                                        : row_max<BS, false>(s_at, sm.ks[slot], qf, cols, masked);
                 // the power of two that P's V scales are relative to
                 float vmax = 0.f;
 #pragma unroll
@@ -801,13 +945,13 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                     m = mn;
                     vref = vnew;
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
+                    for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
-                        tmem_ld16(o_at + 16 * c, o);
+                        tmem_ld16(o_at + c, o);
                         tc_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * of);
-                        tmem_st16(o_at + 16 * c, o);
+                        tmem_st16(o_at + c, o);
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
@@ -837,87 +981,6 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[t]);
         }
-
-        // The piece's result.  In a split piece both streams have a part of the same rows: stream 1 leaves its own in the query
-        // tiles, once stream 0's scores are done with them too, and stream 0 joins the two.
-        if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
-        tc_fence_after();
-        ++pieces;
-        const bool join = !p.paired && it.jobs > 1, give = join && t == 1, take = join && t == 0;
-        const bool cut = p.begin > 0 || p.end < p.tiles;
-        float* rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
-        float4* exchange = reinterpret_cast<float4*>(&sm.q[0][0]);
-        float f0 = vref, f1 = 0.f;  // factors of this stream's and of stream 1's output
-        if (give) {
-            if (!warp_wait(&sm.x_empty, splits & 1, a.err, abort)) return;
-            sm.m1[r] = m;
-            sm.l1[r] = l;
-        }
-        if (take) {
-            mbar_arrive(&sm.x_empty);
-            if (!warp_wait(&sm.x_full, (splits >> 1) & 1, a.err, abort)) return;
-            const float m1 = sm.m1[r], l1 = sm.l1[r], mn = fmaxf(m, m1);
-            // a state without a maximum is empty, unless its sum is NaN
-            const float a0 = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2_approx(m - mn);
-            f1 = m1 == -INFINITY ? (l1 != l1 ? 1.f : 0.f) : exp2_approx(m1 - mn);
-            f0 = vref * a0;
-            l = l * a0 + l1 * f1;
-            m = mn;
-        }
-        if (warp_live) {
-            const float inv = cut || give ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-            uint32_t s[32];
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(o_at + 32 * c, s);
-                tc_wait_ld();
-                const uint32_t nan = has_nan ? sm.nan_row[t][r][c] : 0u;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint((nan >> k & 1) ? quiet_nan() : __uint_as_float(s[k]) * f0);
-                if (take) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float4 y = exchange[(8 * c + k) * kTile + r];
-                        s[4 * k] = __float_as_uint(fmaf(y.x, f1, __uint_as_float(s[4 * k])));
-                        s[4 * k + 1] = __float_as_uint(fmaf(y.y, f1, __uint_as_float(s[4 * k + 1])));
-                        s[4 * k + 2] = __float_as_uint(fmaf(y.z, f1, __uint_as_float(s[4 * k + 2])));
-                        s[4 * k + 3] = __float_as_uint(fmaf(y.w, f1, __uint_as_float(s[4 * k + 3])));
-                    }
-                }
-                if (give || cut) {
-                    uint4* d = give ? reinterpret_cast<uint4*>(exchange + 8 * c * kTile + r)
-                                    : reinterpret_cast<uint4*>(rec + 2 * kTile + (size_t)r * D + 32 * c);
-                    const int step = give ? kTile : 1;
-                    if (give || live) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) d[k * step] = make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
-                    }
-                } else if (live) {
-                    uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row_at + 32 * c);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        T y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = from_float<T>(__uint_as_float(s[8 * k + i]) * inv);
-                        d[k] = *reinterpret_cast<const uint4*>(y);
-                    }
-                }
-            }
-            if (cut && live && !give) {
-                rec[r] = m;
-                rec[kTile + r] = l;
-            }
-        }
-        tc_fence_before();
-        if (join) {
-            // nobody writes query tiles before all of stream 0 has read the output that lies there
-            if (give)
-                mbar_arrive(&sm.x_full);
-            else
-                mbar_arrive(&sm.x_empty);
-            if (!warp_wait(&sm.x_empty, 1, a.err, abort)) return;
-            splits += 2;
-        }
         tiles_before += n;
     }
 }
@@ -940,11 +1003,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
         }
         for (int i = 0; i < kBuffers; ++i) {
             mbar_init(&sm.kv_full[i], kWidenWarps);
-            mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.kv_empty[i], 2);
         }
-        mbar_init(&sm.x_full, 128);
-        mbar_init(&sm.x_empty, 128);
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.join_full, kSoftmaxWarps * 32);
+        mbar_init(&sm.join_done, kSoftmaxWarps * 32);
+        mbar_init(&sm.drain[0], 1);
+        mbar_init(&sm.drain[1], 1);
         sm.abort = 0;
         fence_barrier_init();
     }
@@ -960,12 +1024,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
         widen_tiles<D, BS>(a, ws, sm);
     } else if (warp == kCopyWarp) {
         copy_tiles<D, BS>(a, ws, sm);
-    } else if (warp == kIssueWarp && (threadIdx.x & 31) == 0) {
-        issue_products<D>(a, ws, sm);
+    } else if ((threadIdx.x & 31) == 0) {
+        const int t = warp - kIssueWarp;
+        issue_products<D>(a, ws, sm, t);
         if (sm.abort) {  // products still in flight read shared and tensor memory
             int never = 0;
-            tc_commit(&sm.drain);
-            mbar_wait_bounded(&sm.drain, 0, a.err, &never);
+            tc_commit(&sm.drain[t]);
+            mbar_wait_bounded(&sm.drain[t], 0, a.err, &never);
         }
     }
     __syncwarp();
@@ -996,7 +1061,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     // pieces: CTA c has tiles [cut(c), cut(c + 1))
     auto cut = [&](int c) {
         const long long from = share * c - unit;
-        return from <= 0 ? 0 : (int)min((long long)en.tiles, (from + w - 1) / w);
+        return from <= 0 ? 0 : tiles_in(from, en.tiles, en.paired != 0);
     };
     const int first = c1 - 1, last = (int)((end - 1) / share);
     if (cut(first + 1) >= en.tiles) return;  // one piece after all
