@@ -83,25 +83,37 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, int columns) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Products and commits are issued by whole warps, in which one lane is elected each time: control flow and operands are then
+// uniform for the compiler too.  In a branch of one lane every descriptor has to be moved to uniform registers before
+// each product: 70 to 125 cycles apart instead of the 64 that one takes.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this warp's loads; r are registers that they fill (so that nothing reads them earlier).
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[smem] B[smem]
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
@@ -446,7 +458,7 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
     while (ok && walk.next(&p)) {
         const int n = p.end - p.begin, L = clamped_length(a, p.seq), used = (L + BS - 1) / BS;
         const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
-        // Lane j < BLOCKS has block j of a tile: its id, one tile ahead of its use, then scales and record.
+        // Lane j < BLOCKS has block j of a tile.
         auto wanted = [&](int tile) { return lane < BLOCKS && tile < n && (p.begin + tile) * BLOCKS + lane < used; };
         auto fetch = [&](int tile) { return wanted(tile) ? table[(p.begin + tile) * BLOCKS + lane] : -1; };
         auto prefetch = [&](int id) {
@@ -455,7 +467,11 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
             bulk_prefetch(a.key_cache + r * stride, (both ? 2 : 1) * BS * D);
             if (!both) bulk_prefetch(a.value_cache + r * stride, BS * D);
         };
-        int next_id = fetch(0), ahead_id = fetch(kAhead);
+        auto inside = [&](int id) { return id >= 0 && id < a.num_blocks; };
+        auto record = [&](int id) { return (size_t)(inside(id) ? id : 0) * a.num_kv_heads + p.kvh; };
+        // ids are read two tiles ahead of their copy, scales one
+        int id1 = fetch(0), id2 = fetch(1), ahead_id = fetch(kAhead);
+        float ks1 = inside(id1) ? a.k_scale[record(id1)] : 0.f, vs1 = inside(id1) ? a.v_scale[record(id1)] : 0.f;
 #pragma unroll 1
         for (int i = 1; i < kAhead; ++i) prefetch(fetch(i));
         size_t rec[2] = {0, 0};  // of even and odd tiles: V of a tile is copied after K of the next one
@@ -466,21 +482,20 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
             float ks = 0.f, vs = 0.f;
             bool bad = false;
             if (!f.value) {
-                const int id = next_id;
-                next_id = fetch(f.tile + 1);
+                const int id = id1;
+                ks = ks1;
+                vs = vs1;
+                id1 = id2;
+                ks1 = inside(id1) ? a.k_scale[record(id1)] : 0.f;
+                vs1 = inside(id1) ? a.v_scale[record(id1)] : 0.f;
+                id2 = fetch(f.tile + 2);
                 prefetch(ahead_id);
                 ahead_id = fetch(f.tile + 1 + kAhead);
-                const bool in = id >= 0 && id < a.num_blocks && wanted(f.tile);
-                bad = wanted(f.tile) && !in;
-                const size_t r = (size_t)(in ? id : 0) * a.num_kv_heads + p.kvh;
+                bad = wanted(f.tile) && !inside(id);
                 if (odd)
-                    rec[1] = r, have[1] = in;
+                    rec[1] = record(id), have[1] = inside(id);
                 else
-                    rec[0] = r, have[0] = in;
-                if (in) {
-                    ks = a.k_scale[r];
-                    vs = a.v_scale[r];
-                }
+                    rec[0] = record(id), have[0] = inside(id);
                 if (bad) atomicOr(a.err, kErrBadTable);
             }
             const bool in = odd ? have[1] : have[0];
@@ -594,13 +609,13 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
     }
 }
 
-// One thread per stream issues its products; while one waits, the other's keep the tensor cores busy.  Job j of a piece is a
+// One warp per stream issues its products; while one waits, the other's keep the tensor cores busy.  Job j of a piece is a
 // score tile of stream j % 2; its scores are issued right behind the output of the stream's previous job, which has then read
 // the P that they overwrite.
 template <int D>
 __device__ __forceinline__ void issue_products(const AttendArgs& a, const Workspace& ws, Smem<D>& sm, int t) {
     volatile int* abort = &sm.abort;
-    const uint32_t s_at = sm.tmem + t * kTile, o_at = sm.tmem + 2 * kTile + t * D;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
     const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024);
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
@@ -618,19 +633,19 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
         };
         if (jobs <= t) {
             for (unsigned f = fills; f < fills + 2; ++f) {
-                if (!wait_for(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
-                mbar_arrive(&sm.kv_empty[f % kBuffers]);
+                if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
+                if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.kv_empty[f % kBuffers]);
             }
         }
 #pragma unroll 1
         for (int j = t - 2; j < jobs; j += 2) {
             if (j >= 0) {
                 const unsigned f = fills + value_fill(p.paired, n, p.paired ? j >> 1 : j), buf = f % kBuffers;
-                if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-                if (!wait_for(&sm.p_full[t], steps++ & 1, a.err, abort)) return;
+                if (!warp_wait(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+                if (!warp_wait(&sm.p_full[t], steps++ & 1, a.err, abort)) return;
                 tc_fence_after();
                 const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
-#pragma unroll 2
+#pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
                     mma_ts(o_at, s_at + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
                 release(buf);
@@ -639,11 +654,11 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
             const int next = j + 2;
             if (next < jobs) {
                 const unsigned f = fills + key_fill(p.paired, p.paired ? next >> 1 : next), buf = f % kBuffers;
-                if (!wait_for(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-                if (next < 2 && !wait_for(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
+                if (!warp_wait(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+                if (next < 2 && !warp_wait(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
                 tc_fence_after();
                 const uint64_t kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
-#pragma unroll 2
+#pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
                     mma_ss(s_at, qd + off, kd + off, idesc_of(kTile, false), k > 0);
@@ -724,7 +739,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float q
         float kf[32 / BS];
 #pragma unroll
         for (int h = 0; h < 32 / BS; ++h) kf[h] = ks[c / BS + h] * qf;
-        tc_wait_ld();
+        tc_wait_ld(s);
 #pragma unroll
         for (int h = 0; h < 32 / BS; ++h) {
             float x = -INFINITY, y = -INFINITY;  // two chains
@@ -759,7 +774,7 @@ __device__ __forceinline__ float row_exp(uint32_t s_at, const float* ks, const f
             kf[h] = ks[c / BS + h] * qf;
             vf[h] = vs[c / BS + h] * vinv;
         }
-        tc_wait_ld();
+        tc_wait_ld(s);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
             const int h = i / BS;
@@ -861,13 +876,13 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                 for (int c = c0; c < c1; c += 32) {
                     uint32_t s[32];
                     tmem_ld32(o_at + c, s);
-                    tc_wait_ld();
+                    tc_wait_ld(s);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
                     if (res.join) {
                         uint32_t o[32];
                         tmem_ld32(other_o_at + c, o);
-                        tc_wait_ld();
+                        tc_wait_ld(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k])));
                     }
@@ -948,7 +963,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
                         tmem_ld16(o_at + c, o);
-                        tc_wait_ld();
+                        tc_wait_ld(o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * of);
                         tmem_st16(o_at + c, o);
@@ -1024,10 +1039,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
         widen_tiles<D, BS>(a, ws, sm);
     } else if (warp == kCopyWarp) {
         copy_tiles<D, BS>(a, ws, sm);
-    } else if ((threadIdx.x & 31) == 0) {
-        const int t = warp - kIssueWarp;
+    } else {
+        const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
         issue_products<D>(a, ws, sm, t);
-        if (sm.abort) {  // products still in flight read shared and tensor memory
+        if (__any_sync(0xffffffffu, sm.abort)) {  // products still in flight read shared and tensor memory
             int never = 0;
             tc_commit(&sm.drain[t]);
             mbar_wait_bounded(&sm.drain[t], 0, a.err, &never);
