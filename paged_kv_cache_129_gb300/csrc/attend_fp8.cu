@@ -4,8 +4,9 @@
 // position p attends positions 0 .. p:  out = sum softmax(scale q k_j) v_j, with k_j, v_j = code * scale(block, head).
 //
 // Rows.  The g query heads of a kv head and the request's tokens form R = n_b * g rows (row v: token v / g, head
-// v % g), cut into tiles of 128, the M of the products; keys come in tiles of 128 tokens.  A CTA has two streams of
-// softmax warps, so that one's exponentials run under the other's products:
+// v % g), cut into tiles of 128, the M of the products; keys come in tiles of 128 tokens, whose scores are made and
+// used in halves of 64 columns: while the softmax warps work on one half, the other half's products run.
+// A CTA has two streams of softmax warps:
 //   paired  two row tiles share every key tile (it is widened once for both);
 //   split   a single row tile (few rows: verification, decode, the rest of a run): the streams take alternate key
 //           tiles, and join their results at the end.
@@ -154,15 +155,22 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// size bytes (a multiple of 16, both addresses 16-byte aligned) into shared memory, completion on bar.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned size, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
-                 "l"(src), "r"(size), "r"(smem_addr(bar))
-                 : "memory");
+// Four rows y of a tensor map whose box is one row, into shared memory one after the other; x in elements.  One elected lane.
+__device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int x, int4 y, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_addr(bar))
+        : "memory");
 }
-
-__device__ __forceinline__ void bulk_prefetch(const void* src, unsigned size) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(size) : "memory");
+__device__ __forceinline__ void gather4_to_l2(const CUtensorMap* map, int x, int4 y) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.2d.L2.global.tile::gather4 [%0, {%1, %2, %3, %4, %5}];\n\t}" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+        : "memory");
 }
 
 // Operand tiles in shared memory: panels of 64 elements (128 bytes) by 128 rows, 128-byte swizzle (16-byte unit u of row r
@@ -369,7 +377,7 @@ struct Smem {
     uint32_t nan_row[2][kTile][D / 32];                 // per row: elements of the output that are NaN, if its thread says so
     float4 state[2][kTile];                             // at the end of a split piece: both streams' m, l, vref, has_nan
     uint64_t q_full[2], raw_full[kRaw], raw_empty[kRaw], kv_full[kBuffers], kv_empty[kBuffers];
-    uint64_t s_full[2], p_full[2], o_full[2], join_full, join_done, drain[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -438,19 +446,21 @@ __device__ __forceinline__ void widen_store(unsigned char* unit0, unsigned char*
 // Per byte of w: 0x80 where the code is NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// The copy warp: every block's K or V rows (contiguous) into the raw ring by one bulk copy per block, a lane each, and the tile's
-// scales into the side ring.  Registers and L1 could not hold what has to be in flight: with 206 KB of shared memory taken, L1
-// has room for about 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.  Three tiles of the ring do not cover the latency of
-// HBM either: tiles further ahead are prefetched into L2, and the copies take L2's latency.
+// The copy warp: K or V of four blocks by one gather (a block's rows of a head are one row of the tensor map), into the raw ring,
+// and the tile's scales into the side ring.  Registers and L1 could not hold what has to be in flight: with 200 KB of shared memory
+// taken, L1 has room for about 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.  Three tiles of the ring do not cover
+// the latency of HBM either: tiles further ahead are prefetched into L2, and the copies take L2's latency.  One copy per block,
+// from a lane each, took 1900 cycles a tile to issue.
 // Side data of tile i sits in slot i % 8.  When K of tile i is copied, the raw slot that it takes was widened, so the f16 buffer
 // three fills before that one was free: scores of tile i - 3 at least are done, so the softmax of tile i - 5, and slot i % 8 is
 // tile i - 8's.
 template <int D, int BS>
-__device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+__device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm, const CUtensorMap* kmap,
+                                           const CUtensorMap* vmap) {
     constexpr int BLOCKS = kTile / BS, RAW = Smem<D>::kRaw;
+    constexpr int kRowBytes = BS * D, kBox = kRowBytes < 2048 ? kRowBytes : 2048, PARTS = kRowBytes / kBox;  // 8-byte elements
     const int lane = threadIdx.x & 31;
     const bool both = a.value_cache == nullptr;
-    const size_t stride = (size_t)(both ? 2 : 1) * BS * D;  // K of a (block, head) begins at record * stride
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
     unsigned fills = 0, tiles = 0;
@@ -461,52 +471,59 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
         // Lane j < BLOCKS has block j of a tile.
         auto wanted = [&](int tile) { return lane < BLOCKS && tile < n && (p.begin + tile) * BLOCKS + lane < used; };
         auto fetch = [&](int tile) { return wanted(tile) ? table[(p.begin + tile) * BLOCKS + lane] : -1; };
-        auto prefetch = [&](int id) {
-            if (id < 0 || id >= a.num_blocks) return;
-            const size_t r = (size_t)id * a.num_kv_heads + p.kvh;
-            bulk_prefetch(a.key_cache + r * stride, (both ? 2 : 1) * BS * D);
-            if (!both) bulk_prefetch(a.value_cache + r * stride, BS * D);
-        };
         auto inside = [&](int id) { return id >= 0 && id < a.num_blocks; };
-        auto record = [&](int id) { return (size_t)(inside(id) ? id : 0) * a.num_kv_heads + p.kvh; };
+        // (blocks that are not there take row 0's place: whatever they bring is not used)
+        auto record = [&](int id) { return (inside(id) ? id : 0) * a.num_kv_heads + p.kvh; };
+        auto row4 = [&](int row, int g) {
+            return make_int4(__shfl_sync(0xffffffffu, row, 4 * g), __shfl_sync(0xffffffffu, row, 4 * g + 1),
+                             __shfl_sync(0xffffffffu, row, 4 * g + 2), __shfl_sync(0xffffffffu, row, 4 * g + 3));
+        };
+        auto prefetch = [&](int id) {
+            const int r = record(id);
+            if (!__any_sync(0xffffffffu, inside(id))) return;
+#pragma unroll
+            for (int g = 0; g < BLOCKS / 4; ++g) {
+                const int4 k = row4(both ? 2 * r : r, g), v = row4(both ? 2 * r + 1 : r, g);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    gather4_to_l2(kmap, part * (kBox / 8), k);
+                    gather4_to_l2(vmap, part * (kBox / 8), v);
+                }
+            }
+        };
         // ids are read two tiles ahead of their copy, scales one
         int id1 = fetch(0), id2 = fetch(1), ahead_id = fetch(kAhead);
         float ks1 = inside(id1) ? a.k_scale[record(id1)] : 0.f, vs1 = inside(id1) ? a.v_scale[record(id1)] : 0.f;
 #pragma unroll 1
         for (int i = 1; i < kAhead; ++i) prefetch(fetch(i));
-        size_t rec[2] = {0, 0};  // of even and odd tiles: V of a tile is copied after K of the next one
-        bool have[2] = {false, false};
+        int rec0 = 0, rec1 = 0;  // of even and odd tiles: V of a tile may be copied after K of the next one
+#pragma unroll 1
         for (int i = 0; i < 2 * n; ++i, ++fills) {
             const Fill f = fill_of(p.paired, n, i);
-            const int odd = f.tile & 1, slot = fills % RAW;
-            float ks = 0.f, vs = 0.f;
-            bool bad = false;
+            const int slot = fills % RAW, side = (tiles + f.tile) % kRing;
+            float ks = ks1, vs = vs1;
+            unsigned present = 0, masked = 0;
             if (!f.value) {
-                const int id = id1;
-                ks = ks1;
-                vs = vs1;
+                present = __ballot_sync(0xffffffffu, inside(id1) && wanted(f.tile));
+                const bool bad = wanted(f.tile) && !inside(id1);
+                masked = __ballot_sync(0xffffffffu, bad);
+                if (bad) atomicOr(a.err, kErrBadTable);
+                if (f.tile & 1)
+                    rec1 = record(id1);
+                else
+                    rec0 = record(id1);
                 id1 = id2;
                 ks1 = inside(id1) ? a.k_scale[record(id1)] : 0.f;
                 vs1 = inside(id1) ? a.v_scale[record(id1)] : 0.f;
                 id2 = fetch(f.tile + 2);
                 prefetch(ahead_id);
                 ahead_id = fetch(f.tile + 1 + kAhead);
-                bad = wanted(f.tile) && !inside(id);
-                if (odd)
-                    rec[1] = record(id), have[1] = inside(id);
-                else
-                    rec[0] = record(id), have[0] = inside(id);
-                if (bad) atomicOr(a.err, kErrBadTable);
             }
-            const bool in = odd ? have[1] : have[0];
-            const size_t r = odd ? rec[1] : rec[0];
-            const unsigned present = __ballot_sync(0xffffffffu, in), masked = __ballot_sync(0xffffffffu, bad);
             if (!warp_wait(&sm.raw_empty[slot], ((fills / RAW) & 1) ^ 1, a.err, &sm.abort)) {
                 ok = false;
                 break;
             }
             if (!f.value) {
-                const int side = (tiles + f.tile) % kRing;
                 if (lane < 8) {
                     sm.ks[side][lane] = ks;
                     sm.vs[side][lane] = vs;
@@ -517,13 +534,15 @@ __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace&
                 }
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[slot], __popc(present) * BS * D);
+            if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[slot], kTile * D);
             __syncwarp();
-            if (in) {
-                const uint8_t* src = f.value ? (both ? a.key_cache + r * stride + BS * D : a.value_cache + r * stride)
-                                             : a.key_cache + r * stride;
-                bulk_load(sm.raw[slot] + lane * BS * D, src, BS * D, &sm.raw_full[slot]);
-            }
+            const int r = f.tile & 1 ? rec1 : rec0, row = both ? 2 * r + (f.value ? 1 : 0) : r;
+            const CUtensorMap* map = f.value ? vmap : kmap;
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                for (int g = 0; g < BLOCKS / 4; ++g)
+                    gather4(sm.raw[slot] + (part * BLOCKS + 4 * g) * kBox, map, part * (kBox / 8), row4(row, g), &sm.raw_full[slot]);
         }
         tiles += n;
     }
@@ -560,7 +579,9 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
             const unsigned present = sm.present[(tiles + f.tile) % kRing];
             const int left = it.L - p0;  // rows of the tile inside the context; the others' codes may be anything
             if (!warp_wait(&sm.kv_empty[buf], ((fills / kBuffers) & 1) ^ 1, a.err, &sm.abort)) return;
+            // rows row0 + 16 k (32 k); a block of 4 KB came as two halves, all first halves before all second ones
             const unsigned char* from = sm.raw[slot] + row0 * D + chunk * 16;
+            auto pass = [&](int k) { return BS * D > 2048 ? ((k & 1) * 4 + (k >> 1)) * 2048 : k * RPP * D; };
             unsigned char *to0 = sm.kv[buf] + unit0, *to1 = sm.kv[buf] + unit1;
             const bool seen_in_part = p0 + kTile - 1 > seen_by_all;
             if (left >= kTile && present == (1u << (kTile / BS)) - 1 && !(f.value && seen_in_part)) {
@@ -568,7 +589,7 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
                 for (int k = 0; k < N; k += 4) {
                     uint4 c[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(from + (k + j) * RPP * D);
+                    for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(from + pass(k + j));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) widen_store(to0 + (k + j) * RPP * 128, to1 + (k + j) * RPP * 128, c[j]);
                 }
@@ -581,7 +602,7 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
 #pragma unroll 1
                 for (int k = 0; k < N; ++k) {
                     const int r = row0 + k * RPP;
-                    uint4 c = *reinterpret_cast<const uint4*>(from + k * RPP * D);
+                    uint4 c = *reinterpret_cast<const uint4*>(from + pass(k));
                     if (r >= left || !(present >> (r / BS) & 1)) c = make_uint4(0u, 0u, 0u, 0u);
                     if (f.value && seen_in_part) {
                         unsigned at = 0;
@@ -610,13 +631,15 @@ __device__ __forceinline__ void widen_tiles(const AttendArgs& a, const Workspace
 }
 
 // One warp per stream issues its products; while one waits, the other's keep the tensor cores busy.  Job j of a piece is a
-// score tile of stream j % 2; its scores are issued right behind the output of the stream's previous job, which has then read
-// the P that they overwrite.
+// score tile of stream j % 2, in two halves of 64 columns (64 tokens): a half's scores are issued right behind the output of the
+// same half of the stream's previous job, which has then read the P that they overwrite, and are ready while the softmax warps are
+// still at the other half.  (Scores of 64 columns cost 768 cycles a tile instead of 512: the query rows are read twice.)
 template <int D>
 __device__ __forceinline__ void issue_products(const AttendArgs& a, const Workspace& ws, Smem<D>& sm, int t) {
     volatile int* abort = &sm.abort;
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
-    const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024);
+    const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), k0 = desc_of(smem_addr(sm.kv[0]), 16, 1024),
+                   v0 = desc_of(smem_addr(sm.kv[0]), kPanel, 1024);
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
     unsigned fills = 0, pieces = 0, steps = 0;
@@ -637,34 +660,43 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
                 if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.kv_empty[f % kBuffers]);
             }
         }
+        // unit u: half u % 2 of the stream's job u / 2
+        const int units = 2 * ((jobs + 1 - t) / 2);
 #pragma unroll 1
-        for (int j = t - 2; j < jobs; j += 2) {
-            if (j >= 0) {
-                const unsigned f = fills + value_fill(p.paired, n, p.paired ? j >> 1 : j), buf = f % kBuffers;
-                if (!warp_wait(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-                if (!warp_wait(&sm.p_full[t], steps++ & 1, a.err, abort)) return;
+        for (int u = -2; u < units; ++u) {
+            const int half = u & 1;
+            if (u >= 0) {
+                const int tile = p.paired ? u >> 1 : u - half + t;
+                const unsigned f = fills + value_fill(p.paired, n, tile), buf = f % kBuffers;
+                if (half == 0 && !warp_wait(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+                if (!warp_wait(&sm.p_full[t][half], steps & 1, a.err, abort)) return;
                 tc_fence_after();
-                const uint64_t vd = desc_of(smem_addr(sm.kv[buf]), kPanel, 1024);
+                const uint64_t vd = v0 + buf * (Smem<D>::kOperand >> 4) + half * (kTile * 64 >> 4);
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_ts(o_at, s_at + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), j >= 2 || k > 0);
-                release(buf);
-                if (j + 2 >= jobs) tc_commit(&sm.o_full[t]);
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ts(o_at, s_at + 64 * half + 8 * k, vd + (k * 2048 >> 4), idesc_of(D, true), u > 0 || k > 0);
+                tc_commit(&sm.pv_done[t][half]);
+                if (half == 1) {
+                    release(buf);
+                    ++steps;
+                }
+                if (u == units - 1) tc_commit(&sm.o_full[t]);
             }
-            const int next = j + 2;
-            if (next < jobs) {
-                const unsigned f = fills + key_fill(p.paired, p.paired ? next >> 1 : next), buf = f % kBuffers;
-                if (!warp_wait(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
-                if (next < 2 && !warp_wait(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
+            const int next = u + 2;
+            if (next < units) {
+                const int tile = p.paired ? next >> 1 : next - half + t;
+                const unsigned f = fills + key_fill(p.paired, tile), buf = f % kBuffers;
+                if (half == 0 && !warp_wait(&sm.kv_full[buf], (f / kBuffers) & 1, a.err, abort)) return;
+                if (next == 0 && !warp_wait(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
                 tc_fence_after();
-                const uint64_t kd = desc_of(smem_addr(sm.kv[buf]), 16, 1024);
+                const uint64_t kd = k0 + buf * (Smem<D>::kOperand >> 4) + half * (kTile * 64 >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = ((k / 4) * kPanel + (k % 4) * 32) >> 4;
-                    mma_ss(s_at, qd + off, kd + off, idesc_of(kTile, false), k > 0);
+                    mma_ss(s_at + 64 * half, qd + off, kd + off, idesc_of(kTile / 2, false), k > 0);
                 }
-                release(buf);
-                tc_commit(&sm.s_full[t]);
+                if (half == 1) release(buf);
+                tc_commit(&sm.s_full[t][half]);
             }
         }
         fills += 2 * n;
@@ -690,105 +722,108 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// A query row to f16 in the swizzled tile; returns what undoes its power of two.
+// A warp's 32 query rows to f16, into the swizzled tile; row_at: where this lane's row begins (live: if it exists).  D / 8 lanes load a
+// row together.  Returns what undoes the power of two that this lane's row was moved by.
 template <typename T, int D>
-__device__ __forceinline__ float stage_query(const T* src, bool live, bool negate, unsigned char* tile, int r) {
-    float mul = negate ? -1.f : 1.f;
-    int e = 0;
-    if (!std::is_same<T, __half>::value) {
-        float most = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
+__device__ __forceinline__ float stage_query(const T* query, size_t row_at, bool live, bool negate, unsigned char* tile, int row0) {
+    constexpr int LPR = D / 8, RPS = 32 / LPR, BATCH = 8;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, i = lane % LPR;
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
+    float undo = 1.f;
+#pragma unroll 1
+    for (int b = 0; b < 32; b += BATCH * RPS) {
+        uint4 raw[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int r = b + k * RPS + sub;
+            const size_t at = __shfl_sync(0xffffffffu, row_at, r);
+            raw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (alive >> r & 1) raw[k] = *reinterpret_cast<const uint4*>(query + at + 8 * i);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int r = b + k * RPS + sub;
             float x[8];
-            unpack16<T>(live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), x);
+            unpack16<T>(raw[k], x);
+            float mul = negate ? -1.f : 1.f;
+            if (!std::is_same<T, __half>::value) {
+                float most = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[k]));
-        }
-        if (most > 0.f && most <= 3.402823466e38f) {
-            int ex;
-            frexpf(most, &ex);  // most = f * 2^ex, f in [0.5, 1): the row's largest goes to [2^14, 2^15)
-            e = min(max(15 - ex, -126), 126);
-        }
-        mul *= __int_as_float((e + 127) << 23);
-    }
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-        float x[8];
-        unpack16<T>(live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), x);
-        uint32_t h[4];
+                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __half2 y = __floats2half2_rn(x[2 * k] * mul, x[2 * k + 1] * mul);
-            h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                int e = 0;
+                if (most > 0.f && most <= 3.402823466e38f) {
+                    int ex;
+                    frexpf(most, &ex);  // most = f * 2^ex, f in [0.5, 1): the row's largest goes to [2^14, 2^15)
+                    e = min(max(15 - ex, -126), 126);
+                }
+                mul *= __int_as_float((e + 127) << 23);
+                const float back = __int_as_float((127 - e) << 23);
+#pragma unroll
+                for (int o = 0; o < RPS; ++o) {
+                    const float y = __shfl_sync(0xffffffffu, back, o * LPR);
+                    if (lane == b + k * RPS + o) undo = y;
+                }
+            }
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 y = __floats2half2_rn(x[2 * j] * mul, x[2 * j + 1] * mul);
+                h[j] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            const int row = row0 + r;
+            *reinterpret_cast<uint4*>(tile + row * 128 + (i / 8) * kPanel + (((i & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        *reinterpret_cast<uint4*>(tile + r * 128 + (i / 8) * kPanel + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    return __int_as_float((127 - e) << 23);
+    return undo;
 }
 
-// The largest score of a lane's row in one key tile, scales applied.  WHOLE: the row sees all of it.
-// This loop, row_exp() and the one in widen_tiles() run all the time, on every scheduler next to one another: they are short, so
-// that they stay in the instruction caches together.  Straight code over the 128 columns took five times its issue time.
-template <int BS, bool WHOLE>
-__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float qf, int cols, unsigned masked) {
+// 64 scores of a lane's row that it does not see become -inf: cols of them are seen, less the blocks in masked.
+template <int BS>
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[64], int cols, unsigned masked) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        if (i >= cols || (masked >> (i / BS) & 1)) s[i] = 0xff800000u;
+}
+
+// Largest of 64 scores, times the factors of their blocks.
+template <int BS>
+__device__ __forceinline__ float row_max(const uint32_t (&s)[64], const float (&kf)[64 / BS]) {
     float top = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
-        uint32_t s[32];
-        tmem_ld32(s_at + c, s);
-        float kf[32 / BS];
 #pragma unroll
-        for (int h = 0; h < 32 / BS; ++h) kf[h] = ks[c / BS + h] * qf;
-        tc_wait_ld(s);
+    for (int h = 0; h < 64 / BS; ++h) {
+        float x = -INFINITY, y = -INFINITY;  // two chains
 #pragma unroll
-        for (int h = 0; h < 32 / BS; ++h) {
-            float x = -INFINITY, y = -INFINITY;  // two chains
-#pragma unroll
-            for (int k = 0; k < BS; k += 2) {
-                const int i = BS * h + k;
-                if (!WHOLE && (c + i >= cols || (masked >> (c / BS + h) & 1))) s[i] = 0xff800000u;  // -inf
-                if (!WHOLE && (c + i + 1 >= cols || (masked >> (c / BS + h) & 1))) s[i + 1] = 0xff800000u;
-                x = fmaxf(x, __uint_as_float(s[i]));
-                y = fmaxf(y, __uint_as_float(s[i + 1]));
-            }
-            x = fmaxf(x, y);
-            top = fmaxf(top, x == -INFINITY ? x : x * kf[h]);
+        for (int k = 0; k < BS; k += 4) {
+            x = fmaxf(x, fmaxf(__uint_as_float(s[BS * h + k]), __uint_as_float(s[BS * h + k + 1])));
+            y = fmaxf(y, fmaxf(__uint_as_float(s[BS * h + k + 2]), __uint_as_float(s[BS * h + k + 3])));
         }
+        top = fmaxf(top, fmaxf(x, y) * kf[h]);
     }
     return top;
 }
 
-// P of a lane's row in one key tile: exp2(score - mu) times the block's V scale, as f16 over the scores that it comes from; returns
-// the sum of the exponentials.
-template <int BS, bool WHOLE>
-__device__ __forceinline__ float row_exp(uint32_t s_at, const float* ks, const float* vs, float qf, float mu, float vinv, int cols,
-                                         unsigned masked) {
+// P of 64 scores: exp2(score - mu) times the block's V scale, as f16, over the scores in tensor memory; returns the sum of the
+// exponentials.
+template <int BS>
+__device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, const float (&kf)[64 / BS], const float* vs, float vinv, float mu) {
     float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
-        uint32_t s[32], out[16];
-        tmem_ld32(s_at + c, s);
-        float kf[32 / BS], vf[32 / BS];
 #pragma unroll
-        for (int h = 0; h < 32 / BS; ++h) {
-            kf[h] = ks[c / BS + h] * qf;
-            vf[h] = vs[c / BS + h] * vinv;
-        }
-        tc_wait_ld(s);
+    for (int c = 0; c < 64; c += 32) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
+        for (int i = c; i < c + 32; i += 2) {
             const int h = i / BS;
-            float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf[h], kf[h]),
-                            make_float2(-mu, -mu));
-            if (!WHOLE && (c + i >= cols || (masked >> (c / BS + h) & 1))) x.x = -INFINITY;
-            if (!WHOLE && (c + i + 1 >= cols || (masked >> (c / BS + h) & 1))) x.y = -INFINITY;
+            const float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf[h], kf[h]),
+                                  make_float2(-mu, -mu));
             const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
             sum = add2(sum, e);
-            const float2 w = mul2(e, make_float2(vf[h], vf[h]));
+            const float vf = vs[h] * vinv;
+            const float2 w = mul2(e, make_float2(vf, vf));
             const __half2 p = __floats2half2_rn(w.x, w.y);
-            out[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
+            s[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
         }
-        tmem_st16(s_at + c / 2, out);
+        tmem_st16(s_at + c / 2, *reinterpret_cast<uint32_t(*)[16]>(&s[c / 2]));
     }
     return sum.x + sum.y;
 }
@@ -815,7 +850,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
     for (;;) {
         Piece p;
         Item it{};
-        int n = 0, my_jobs = 0, bound = -1;
+        int n = 0, my_jobs = 0, bound = -1, seen_by_all = 0;
         float qf = 0.f;
         Result now{};
         const bool have = walk.next(&p);
@@ -836,10 +871,11 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
             now.rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
             now.row_at = now.live ? ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D : 0;
             if (now.live) bound = it.L - it.n + token;  // last position that the row sees
+            seen_by_all = it.L - it.n + p.row0 / it.group;
             if (my_jobs > 0) {
                 // the stream's last scores were waited for, so its query tile is free
                 const float undo =
-                    stage_query<T, D>(static_cast<const T*>(a.query) + now.row_at, now.live, a.scale < 0.f, sm.q[t], r);
+                    stage_query<T, D>(static_cast<const T*>(a.query), now.row_at, now.live, a.scale < 0.f, sm.q[t], (warp & 3) * 32);
                 fence_proxy_async_smem();
                 mbar_arrive(&sm.q_full[t]);
                 qf = fabsf(a.scale) * 1.4426950408889634f * undo;
@@ -936,23 +972,44 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
             const int local = p.paired ? step : 2 * step + t;
             const unsigned count = tiles_before + local;
             const int p0 = (p.begin + local) * kTile, slot = count % kRing;
-            if (!warp_wait(&sm.s_full[t], steps & 1, a.err, abort)) return;
-            tc_fence_after();
-            if (now.warp_live) {
-                const unsigned masked = sm.masked[slot];
-                const int cols = min(kTile, bound - p0 + 1);  // columns of the tile that the row sees
-                const bool whole = __all_sync(0xffffffffu, !now.live || cols == kTile) && masked == 0;
-                const float top = whole ? row_max<BS, true>(s_at, sm.ks[slot], qf, cols, masked)
-                                        : row_max<BS, false>(s_at, sm.ks[slot], qf, cols, masked);
-                // the power of two that P's V scales are relative to
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (!warp_wait(&sm.s_full[t][half], steps & 1, a.err, abort)) return;
+                tc_fence_after();
+                if (!now.warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
+                    if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
+                    continue;
+                }
+                const uint32_t at = s_at + 64 * half;
+                uint32_t s[64];
+                tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                const float* vs = sm.vs[slot] + half * (64 / BS);
+                // factors of the scores; kept above zero, so that masked scores stay -inf
+                float kf[64 / BS];
                 float vmax = 0.f;
 #pragma unroll
-                for (int k = 0; k < kTile / BS; ++k) vmax = fmaxf(vmax, sm.vs[slot][k]);
+                for (int k = 0; k < 64 / BS; ++k) {
+                    kf[k] = fmaxf(sm.ks[slot][half * (64 / BS) + k] * qf, 1e-38f);
+                    vmax = fmaxf(vmax, vs[k]);
+                }
+                const unsigned masked = sm.masked[slot] >> (half * (64 / BS));
+                const int cols = bound - p0 - 64 * half + 1;  // columns that the row sees, if below 64
+                const bool whole = __all_sync(0xffffffffu, !now.live || cols >= 64) && (masked & ((1u << (64 / BS)) - 1)) == 0;
+                tc_wait_ld(s);
+                if (!whole) mask_scores<BS>(s, cols, masked);
+                const float top = row_max<BS>(s, kf);
+                // the power of two that P's V scales are relative to
                 const float vnew = fmaxf(vref, __int_as_float(__float_as_int(fmaxf(vmax, 7.888609052210118e-31f)) & 0x7f800000));
-                if (step == 0) {
+                if (step == 0 && half == 0) {
                     m = top;
                     vref = vnew;
                 } else if (__any_sync(0xffffffffu, vnew > vref || top > m + 8.f)) {
+                    // The output so far has to be there.  (Its barrier is waited for only here: the phase before the one that is
+                    // meant is over, because this half's scores were issued after the output of the half before the last.)
+                    const unsigned last = half ? steps : steps - 1;
+                    if (!warp_wait(&sm.pv_done[t][half ^ 1], last & 1, a.err, abort)) return;
+                    tc_fence_after();
                     const float mn = fmaxf(m, top);
                     const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
                     const float of = f * (vref / vnew);
@@ -969,21 +1026,19 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                         tmem_st16(o_at + c, o);
                     }
                 }
-                const float mu = m == -INFINITY ? 0.f : m;
                 const float vinv = __int_as_float(0x7f000000 - __float_as_int(vref));  // 1 / vref, a power of two
-                l += whole ? row_exp<BS, true>(s_at, sm.ks[slot], sm.vs[slot], qf, mu, vinv, cols, masked)
-                           : row_exp<BS, false>(s_at, sm.ks[slot], sm.vs[slot], qf, mu, vinv, cols, masked);
-                if (!whole) {
+                l += row_exp<BS>(s, at, kf, vs, vinv, m == -INFINITY ? 0.f : m);
+                if (half == 1 && p0 + kTile - 1 > seen_by_all) {  // a tile whose V was searched for NaN
                     const unsigned f = 2 * tiles_before + value_fill(p.paired, n, local);
                     if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
-                    const int at_slot = count % kNanRing;
+                    const int at_slot = count % kNanRing, all = min(kTile, bound - p0 + 1);
                     if (sm.nan_any[at_slot][0] | sm.nan_any[at_slot][1] | sm.nan_any[at_slot][2] | sm.nan_any[at_slot][3]) {
 #pragma unroll 1
                         for (int i = 0; i < D / 32; ++i) {
                             uint32_t bits = has_nan ? sm.nan_row[t][r][i] : 0u;
 #pragma unroll 1
-                            for (int k = 0; k < cols; ++k)
-                                if (!(masked >> (k / BS) & 1))
+                            for (int k = 0; k < all; ++k)
+                                if (!(sm.masked[slot] >> (k / BS) & 1))
                                     bits |= (uint32_t)sm.nan_at[at_slot][k][2 * i] | ((uint32_t)sm.nan_at[at_slot][k][2 * i + 1] << 16);
                             sm.nan_row[t][r][i] = bits;
                         }
@@ -991,25 +1046,30 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                     }
                 }
                 tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[t]);
         }
         tiles_before += n;
     }
 }
 
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArgs a, const Workspace ws) {
+__global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArgs a, const Workspace ws,
+                                                                 const __grid_constant__ CUtensorMap kmap,
+                                                                 const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ unsigned char raw_smem[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(((uintptr_t)raw_smem + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 128);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm.s_full[i][h], 1);
+                mbar_init(&sm.p_full[i][h], 4);
+                mbar_init(&sm.pv_done[i][h], 1);
+            }
             mbar_init(&sm.o_full[i], 1);
         }
         for (int i = 0; i < Smem<D>::kRaw; ++i) {
@@ -1038,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
     } else if (warp < kSoftmaxWarps + kWidenWarps) {
         widen_tiles<D, BS>(a, ws, sm);
     } else if (warp == kCopyWarp) {
-        copy_tiles<D, BS>(a, ws, sm);
+        copy_tiles<D, BS>(a, ws, sm, &kmap, &vmap);
     } else {
         const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
         issue_products<D>(a, ws, sm, t);
@@ -1113,7 +1173,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 }
 
 template <typename T, int D, int BS>
-cudaError_t attend_typed(const AttendArgs& a, cudaStream_t stream) {
+cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
     const int group = a.num_heads / a.num_kv_heads, ctas = a.num_sms;
     const size_t cap = max_entries(a.num_seqs, a.num_tokens, group);
     char* base = static_cast<char*>(a.workspace);
@@ -1127,7 +1187,7 @@ cudaError_t attend_typed(const AttendArgs& a, cudaStream_t stream) {
     const size_t smem = sizeof(Smem<D>) + 1024;
     e = cudaFuncSetAttribute(attend_fp8_kernel<T, D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws);
+    e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, kmap, vmap);
     if (e != cudaSuccess || ctas < 2) return e;
     return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 4), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
@@ -1140,17 +1200,17 @@ size_t attend_fp8_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int
     return 256 + align256((cap + 1) * sizeof(Entry)) + (size_t)num_sms * 4 * record_floats(head_dim) * sizeof(float);
 }
 
-cudaError_t attend_fp8_launch(const AttendArgs& a, cudaStream_t stream) {
+cudaError_t attend_fp8_launch(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
     const int pick = (a.dtype == 1 ? 4 : 0) + (a.head_dim == 64 ? 2 : 0) + (a.block_size == 32 ? 1 : 0);
     switch (pick) {
-        case 0: return attend_typed<__nv_bfloat16, 128, 16>(a, stream);
-        case 1: return attend_typed<__nv_bfloat16, 128, 32>(a, stream);
-        case 2: return attend_typed<__nv_bfloat16, 64, 16>(a, stream);
-        case 3: return attend_typed<__nv_bfloat16, 64, 32>(a, stream);
-        case 4: return attend_typed<__half, 128, 16>(a, stream);
-        case 5: return attend_typed<__half, 128, 32>(a, stream);
-        case 6: return attend_typed<__half, 64, 16>(a, stream);
-        default: return attend_typed<__half, 64, 32>(a, stream);
+        case 0: return attend_typed<__nv_bfloat16, 128, 16>(a, kmap, vmap, stream);
+        case 1: return attend_typed<__nv_bfloat16, 128, 32>(a, kmap, vmap, stream);
+        case 2: return attend_typed<__nv_bfloat16, 64, 16>(a, kmap, vmap, stream);
+        case 3: return attend_typed<__nv_bfloat16, 64, 32>(a, kmap, vmap, stream);
+        case 4: return attend_typed<__half, 128, 16>(a, kmap, vmap, stream);
+        case 5: return attend_typed<__half, 128, 32>(a, kmap, vmap, stream);
+        case 6: return attend_typed<__half, 64, 16>(a, kmap, vmap, stream);
+        default: return attend_typed<__half, 64, 32>(a, kmap, vmap, stream);
     }
 }
 

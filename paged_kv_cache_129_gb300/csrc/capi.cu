@@ -18,6 +18,7 @@
 #include "pa.h"
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "step_ops.h"
 
 // One error word per device, set by kernels with atomicOr (see pa_common.cuh).
 __device__ unsigned int g_pa_device_error_word;
@@ -411,6 +412,37 @@ int make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int b
 }
 
 }  // namespace
+
+int record_map(CUtensorMap* map, const void* base, long long records, int record_bytes) {
+    struct Entry {
+        const void* base;
+        long long records;
+        int record_bytes;
+        CUtensorMap map;
+    };
+    constexpr int kEntries = 8;  // the last few of this thread, as encode_cache_map()
+    thread_local Entry entries[kEntries] = {};
+    thread_local int next = 0;
+    for (const Entry& e : entries)
+        if (e.base == base && e.base && e.records == records && e.record_bytes == record_bytes) {
+            *map = e.map;
+            return PA_OK;
+        }
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const int part = record_bytes < 2048 ? record_bytes : 2048;
+    cuuint64_t dims[2] = {(cuuint64_t)record_bytes / 8, (cuuint64_t)records};
+    cuuint64_t strides[1] = {(cuuint64_t)record_bytes};
+    cuuint32_t box[2] = {(cuuint32_t)part / 8, 1};
+    cuuint32_t estrides[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(base), dims, strides, box, estrides,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    entries[next] = Entry{base, records, record_bytes, *map};
+    next = (next + 1) % kEntries;
+    return PA_OK;
+}
 
 int device_state(unsigned** error_word, int* num_sms) {
     DeviceState* dev = nullptr;

@@ -245,7 +245,13 @@ int pa_attend_fp8(void* out, const void* query, const void* key_cache, const voi
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return fail(PA_ERR_INVALID_ARG, "pa_attend_fp8: needs a 256-byte aligned workspace of %zu bytes (%zu given)", need,
                     workspace ? workspace_bytes : (size_t)0);
-    const cudaError_t e = attend_fp8_launch(a, static_cast<cudaStream_t>(stream));
+    // rows of K and V of a (block, head); in the layout of records K and V alternate
+    const long long records = (long long)num_blocks * num_kv_heads * (value_cache ? 1 : 2);
+    CUtensorMap kmap, vmap;
+    int ms = record_map(&kmap, key_cache, records, block_size * head_dim);
+    if (ms == PA_OK && value_cache) ms = record_map(&vmap, value_cache, records, block_size * head_dim);
+    if (ms != PA_OK) return ms;
+    const cudaError_t e = attend_fp8_launch(a, kmap, value_cache ? vmap : kmap, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : launch_failed(e, "pa_attend_fp8");
 }
 

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace pa {
@@ -83,6 +84,11 @@ cudaError_t rope_append_fp8_launch(const RopeAppendArgs& a, cudaStream_t stream)
 // Scratch of one attend_fp8 call.
 size_t attend_fp8_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
                                   int block_size, int max_blocks);
-cudaError_t attend_fp8_launch(const AttendArgs& a, cudaStream_t stream);
+// kmap, vmap: record_map()s of K and V.
+cudaError_t attend_fp8_launch(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream);
+
+// A cache as rows of record_bytes (K or V of one block and kv head), for gathers of rows in parts of at most 2 KB.  PA_OK or a failure
+// with its message.
+int record_map(CUtensorMap* map, const void* base, long long records, int record_bytes);
 
 }  // namespace pa
