@@ -35,15 +35,18 @@ constexpr int kTile = 128;             // rows of a row tile, tokens of a key ti
 constexpr int kSoftmaxWarps = 8;       // four per stream
 constexpr int kWidenWarps = 4;
 constexpr int kIssueWarp = kSoftmaxWarps + kWidenWarps;  // two, one per stream
-constexpr int kCopyWarp = kIssueWarp + 2;
-constexpr int kThreads = (kCopyWarp + 1) * 32;
-constexpr int kAhead = 4;              // key tiles whose codes are on their way into L2 before they are copied
+constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1;
+constexpr int kThreads = (kLookWarp + 1) * 32;
 constexpr int kBuffers = 3;            // f16 operand tiles (K or V) in shared memory
-constexpr int kRing = 8;               // slots of per-tile side data (scales), see copy_tiles()
-constexpr int kNanRing = 4;
-// Cost of a key tile in shares: a pair does twice the products and exponentials of a split tile, but loads and widens it once.
-constexpr int kPairedCost = 4, kSplitCost = 3;
-constexpr int kMinShare = 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
+constexpr int kRing = 16;              // slots of per-tile side data (block ids, scales), see look_ahead()
+constexpr int kAhead = kRing - 6;      // key tiles that look_ahead() may be ahead of the copies
+constexpr int kNanRing = 2;            // V of tile i is widened once the scores of tile i (i - 1) are done: the softmax of i - 2 too
+// Cost of work in shares: of a key tile of a pair, of a split tile (half the products and exponentials, but the same loads and
+// widening), and of a unit besides its tiles (queries staged, streams joined, output written: about six split tiles).  Measured
+// (verification / prompt chunks / long contexts / short mixed D = 64, us): 6, 4, 24: 115 / 625 / 387 / 95; 4, 3, 8: 135 / 656 / 412 /
+// 98.  With prefetches as in look_ahead()'s note, 4, 3, 0 (no cost of a unit) took 175 / 694 / 430 / 125, 4, 3, 8 143 / 675 / 439 / 99.
+constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 24;
+constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
 
 // ---- work list (made by plan_kernel) ------------------------------------------------------------
 
@@ -164,15 +167,6 @@ __device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int x
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_addr(bar))
         : "memory");
 }
-__device__ __forceinline__ void gather4_to_l2(const CUtensorMap* map, int x, int4 y) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q cp.async.bulk.prefetch.tensor.2d.L2.global.tile::gather4 [%0, {%1, %2, %3, %4, %5}];\n\t}" ::"l"(
-            reinterpret_cast<uint64_t>(map)),
-        "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-        : "memory");
-}
-
 // Operand tiles in shared memory: panels of 64 elements (128 bytes) by 128 rows, 128-byte swizzle (16-byte unit u of row r
 // at u ^ (r % 8)), 16 KB apart.  Descriptors: bits 0-13 address / 16, 16-29 and 32-45 byte offsets / 16, 46 version 1,
 // 61-63 the 128-byte swizzle (2).
@@ -201,6 +195,10 @@ __device__ __forceinline__ int tiles_of(int L, int n, int group, int row0) {
     const int last = min(n * group, row0 + 2 * kTile) - 1;
     const int bound = L - n + last / group;
     return max(1, (bound + kTile) / kTile);
+}
+
+__device__ __forceinline__ long long unit_cost(int tiles, int paired) {
+    return kUnitCost + (long long)tiles * (paired ? kPairedCost : kSplitCost);
 }
 
 constexpr int kPlanThreads = 1024;
@@ -277,7 +275,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendA
             x.row0 = (e - first_entry[lo]) * 2 * kTile;
             x.paired = n * group - x.row0 > kTile;
             x.tiles = tiles_of(clamped_length(a, lo), n, group, x.row0);
-            c = (long long)x.tiles * (x.paired ? kPairedCost : kSplitCost) * a.num_kv_heads;
+            c = unit_cost(x.tiles, x.paired) * a.num_kv_heads;
         }
         x.first = cost + block_scan(c, scratch, &total);
         cost += total;
@@ -310,7 +308,7 @@ __device__ __forceinline__ int find_entry(const Entry* e, int n, long long x) {
 
 // Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).
 __device__ __forceinline__ int tiles_in(long long x, int tiles, bool paired) {
-    const unsigned cost = (unsigned)min(x, (long long)tiles * (paired ? kPairedCost : kSplitCost));
+    const unsigned cost = (unsigned)max(0ll, min(x - kUnitCost, (long long)tiles * (paired ? kPairedCost : kSplitCost)));
     return (int)(paired ? (cost + kPairedCost - 1) / kPairedCost : (cost + kSplitCost - 1) / kSplitCost);
 }
 
@@ -334,14 +332,13 @@ struct Walk {
         if (pos < stop) {
             e = find_entry(entries, count, pos);
             const Entry x = entries[e];
-            kvh = (int)((pos - x.first) / ((long long)x.tiles * (x.paired ? kPairedCost : kSplitCost)));
+            kvh = (int)((pos - x.first) / unit_cost(x.tiles, x.paired));
         }
     }
     __device__ __forceinline__ bool next(Piece* p) {
         while (pos < stop) {
             const Entry x = entries[e];
-            const int w = x.paired ? kPairedCost : kSplitCost;
-            const long long unit = x.first + (long long)kvh * x.tiles * w;
+            const long long cost = unit_cost(x.tiles, x.paired), unit = x.first + kvh * cost;
             const long long from = pos > unit ? pos - unit : 0, to = stop - unit;
             p->seq = x.seq;
             p->row0 = x.row0;
@@ -350,7 +347,7 @@ struct Walk {
             p->paired = x.paired != 0;
             p->begin = tiles_in(from, x.tiles, p->paired);
             p->end = tiles_in(to, x.tiles, p->paired);
-            pos = unit + (long long)x.tiles * w;
+            pos = unit + cost;
             if (++kvh == heads) {
                 kvh = 0;
                 ++e;
@@ -371,12 +368,13 @@ struct Smem {
     unsigned char kv[kBuffers][kOperand];
     unsigned char raw[kRaw][kTile * D];
     float ks[kRing][8], vs[kRing][8];                   // scales of the tile's blocks
-    unsigned present[kRing], masked[kRing];             // blocks of the tile: copied; with an id outside the pool
+    int rows[kRing][8];                                 // and their rows of the K map (of the V map: the next)
+    unsigned present[kRing], masked[kRing];             // blocks of the tile: there; with an id outside the pool
     unsigned nan_any[kNanRing][kWidenWarps];            // whether a warp found NaN in V of a tile that some row sees in part,
     uint16_t nan_at[kNanRing][kTile][D / 16];           // and where: per token and 16 elements
     uint32_t nan_row[2][kTile][D / 32];                 // per row: elements of the output that are NaN, if its thread says so
     float4 state[2][kTile];                             // at the end of a split piece: both streams' m, l, vref, has_nan
-    uint64_t q_full[2], raw_full[kRaw], raw_empty[kRaw], kv_full[kBuffers], kv_empty[kBuffers];
+    uint64_t side_full[kRing], copied[kRing], q_full[2], raw_full[kRaw], raw_empty[kRaw], kv_full[kBuffers], kv_empty[kBuffers];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
     uint32_t tmem;
     volatile int abort;
@@ -398,6 +396,8 @@ __device__ __forceinline__ int key_fill(bool paired, int tile) { return paired ?
 __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
     return paired ? 2 * tile + 1 : tile == n - 1 ? 2 * n - 1 : 2 * tile + 2;
 }
+
+static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "fits an SM");
 
 // mbar_wait_bounded, with the clock and the abort flag read only now and then: waiting warps share their scheduler with warps
 // that work.
@@ -446,103 +446,93 @@ __device__ __forceinline__ void widen_store(unsigned char* unit0, unsigned char*
 // Per byte of w: 0x80 where the code is NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// The copy warp: K or V of four blocks by one gather (a block's rows of a head are one row of the tensor map), into the raw ring,
-// and the tile's scales into the side ring.  Registers and L1 could not hold what has to be in flight: with 200 KB of shared memory
-// taken, L1 has room for about 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.  Three tiles of the ring do not cover
-// the latency of HBM either: tiles further ahead are prefetched into L2, and the copies take L2's latency.  One copy per block,
-// from a lane each, took 1900 cycles a tile to issue.
-// Side data of tile i sits in slot i % 8.  When K of tile i is copied, the raw slot that it takes was widened, so the f16 buffer
-// three fills before that one was free: scores of tile i - 3 at least are done, so the softmax of tile i - 5, and slot i % 8 is
-// tile i - 8's.
+// The look-ahead warp: block ids and scales of tile after tile into the side ring, up to kAhead tiles before they are copied and
+// across the ends of pieces, so that the tables' and scales' latencies are not waited for.  (It also prefetched the codes into L2 at
+// first, line by line: 144 / 676 / 439 us on verification, chunks, long contexts with, 134 / 656 / 412 without; the raw ring's
+// 48 KB in flight per SM cover HBM's latency.)
+// Side data of tile i sits in slot i % 16, which was tile i - 16's.  When K of tile j is copied, the raw slot that it takes was widened,
+// so the f16 buffer three fills before that one was free: scores of tile j - 3 at least are done, so the softmax of tile j - 5.
+// Tile i is looked at once K of tile i - 10 is copied.
+template <int D, int BS>
+__device__ __forceinline__ void look_ahead(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    constexpr int BLOCKS = kTile / BS;
+    const int lane = threadIdx.x & 31;
+    const bool both = a.value_cache == nullptr;
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned tiles = 0;
+    while (walk.next(&p)) {
+        const int used = (clamped_length(a, p.seq) + BS - 1) / BS;
+        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
+        // lane j < BLOCKS has block j of a tile
+        auto wanted = [&](int tile) { return lane < BLOCKS && tile < p.end && tile * BLOCKS + lane < used; };
+        int id = wanted(p.begin) ? table[p.begin * BLOCKS + lane] : -1;
+        for (int tile = p.begin; tile < p.end; ++tile, ++tiles) {
+            const bool mine = wanted(tile), in = mine && id >= 0 && id < a.num_blocks;
+            if (mine && !in) atomicOr(a.err, kErrBadTable);
+            // (blocks that are not there take record 0's place: whatever it brings is not used)
+            const int record = (in ? id : 0) * a.num_kv_heads + p.kvh;
+            const float ks = in ? a.k_scale[record] : 0.f, vs = in ? a.v_scale[record] : 0.f;
+            id = wanted(tile + 1) ? table[(tile + 1) * BLOCKS + lane] : -1;
+            const unsigned present = __ballot_sync(0xffffffffu, in), masked = __ballot_sync(0xffffffffu, mine && !in);
+            if (tiles >= kAhead) {
+                const unsigned before = tiles - kAhead;
+                if (!warp_wait(&sm.copied[before % kRing], (before / kRing) & 1, a.err, &sm.abort)) return;
+            }
+            const int slot = tiles % kRing;
+            if (lane < 8) {
+                sm.ks[slot][lane] = ks;
+                sm.vs[slot][lane] = vs;
+                sm.rows[slot][lane] = both ? 2 * record : record;
+            }
+            if (lane == 0) {
+                sm.present[slot] = present;
+                sm.masked[slot] = masked;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.side_full[slot]);
+        }
+    }
+}
+
+// The copy warp: K or V of four blocks by one gather (a block's rows of a head are one row of the tensor map), into the raw ring.
+// Registers and L1 could not hold what has to be in flight: with 200 KB of shared memory taken, L1 has room for about
+// 14 KB, and plain loads stalled at 2.2 TB/s over all SMs.  One copy per block, from a lane each, took 1900 cycles a tile to issue.
 template <int D, int BS>
 __device__ __forceinline__ void copy_tiles(const AttendArgs& a, const Workspace& ws, Smem<D>& sm, const CUtensorMap* kmap,
                                            const CUtensorMap* vmap) {
     constexpr int BLOCKS = kTile / BS, RAW = Smem<D>::kRaw;
     constexpr int kRowBytes = BS * D, kBox = kRowBytes < 2048 ? kRowBytes : 2048, PARTS = kRowBytes / kBox;  // 8-byte elements
     const int lane = threadIdx.x & 31;
-    const bool both = a.value_cache == nullptr;
+    const int next_row = a.value_cache == nullptr ? 1 : 0;
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
     Piece p;
     unsigned fills = 0, tiles = 0;
     bool ok = true;
     while (ok && walk.next(&p)) {
-        const int n = p.end - p.begin, L = clamped_length(a, p.seq), used = (L + BS - 1) / BS;
-        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
-        // Lane j < BLOCKS has block j of a tile.
-        auto wanted = [&](int tile) { return lane < BLOCKS && tile < n && (p.begin + tile) * BLOCKS + lane < used; };
-        auto fetch = [&](int tile) { return wanted(tile) ? table[(p.begin + tile) * BLOCKS + lane] : -1; };
-        auto inside = [&](int id) { return id >= 0 && id < a.num_blocks; };
-        // (blocks that are not there take row 0's place: whatever they bring is not used)
-        auto record = [&](int id) { return (inside(id) ? id : 0) * a.num_kv_heads + p.kvh; };
-        auto row4 = [&](int row, int g) {
-            return make_int4(__shfl_sync(0xffffffffu, row, 4 * g), __shfl_sync(0xffffffffu, row, 4 * g + 1),
-                             __shfl_sync(0xffffffffu, row, 4 * g + 2), __shfl_sync(0xffffffffu, row, 4 * g + 3));
-        };
-        auto prefetch = [&](int id) {
-            const int r = record(id);
-            if (!__any_sync(0xffffffffu, inside(id))) return;
-#pragma unroll
-            for (int g = 0; g < BLOCKS / 4; ++g) {
-                const int4 k = row4(both ? 2 * r : r, g), v = row4(both ? 2 * r + 1 : r, g);
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    gather4_to_l2(kmap, part * (kBox / 8), k);
-                    gather4_to_l2(vmap, part * (kBox / 8), v);
-                }
-            }
-        };
-        // ids are read two tiles ahead of their copy, scales one
-        int id1 = fetch(0), id2 = fetch(1), ahead_id = fetch(kAhead);
-        float ks1 = inside(id1) ? a.k_scale[record(id1)] : 0.f, vs1 = inside(id1) ? a.v_scale[record(id1)] : 0.f;
-#pragma unroll 1
-        for (int i = 1; i < kAhead; ++i) prefetch(fetch(i));
-        int rec0 = 0, rec1 = 0;  // of even and odd tiles: V of a tile may be copied after K of the next one
+        const int n = p.end - p.begin;
 #pragma unroll 1
         for (int i = 0; i < 2 * n; ++i, ++fills) {
             const Fill f = fill_of(p.paired, n, i);
-            const int slot = fills % RAW, side = (tiles + f.tile) % kRing;
-            float ks = ks1, vs = vs1;
-            unsigned present = 0, masked = 0;
-            if (!f.value) {
-                present = __ballot_sync(0xffffffffu, inside(id1) && wanted(f.tile));
-                const bool bad = wanted(f.tile) && !inside(id1);
-                masked = __ballot_sync(0xffffffffu, bad);
-                if (bad) atomicOr(a.err, kErrBadTable);
-                if (f.tile & 1)
-                    rec1 = record(id1);
-                else
-                    rec0 = record(id1);
-                id1 = id2;
-                ks1 = inside(id1) ? a.k_scale[record(id1)] : 0.f;
-                vs1 = inside(id1) ? a.v_scale[record(id1)] : 0.f;
-                id2 = fetch(f.tile + 2);
-                prefetch(ahead_id);
-                ahead_id = fetch(f.tile + 1 + kAhead);
+            const int slot = fills % RAW;
+            const unsigned tile = tiles + f.tile, side = tile % kRing;
+            ok = f.value || warp_wait(&sm.side_full[side], (tile / kRing) & 1, a.err, &sm.abort);
+            ok = ok && warp_wait(&sm.raw_empty[slot], ((fills / RAW) & 1) ^ 1, a.err, &sm.abort);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.raw_full[slot], kTile * D);
+                if (!f.value) mbar_arrive(&sm.copied[side]);
             }
-            if (!warp_wait(&sm.raw_empty[slot], ((fills / RAW) & 1) ^ 1, a.err, &sm.abort)) {
-                ok = false;
-                break;
-            }
-            if (!f.value) {
-                if (lane < 8) {
-                    sm.ks[side][lane] = ks;
-                    sm.vs[side][lane] = vs;
-                }
-                if (lane == 0) {
-                    sm.present[side] = present;
-                    sm.masked[side] = masked;
-                }
-                __syncwarp();
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[slot], kTile * D);
             __syncwarp();
-            const int r = f.tile & 1 ? rec1 : rec0, row = both ? 2 * r + (f.value ? 1 : 0) : r;
             const CUtensorMap* map = f.value ? vmap : kmap;
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
+            for (int g = 0; g < BLOCKS / 4; ++g) {
+                int4 y = *reinterpret_cast<const int4*>(&sm.rows[side][4 * g]);
+                if (f.value) y = make_int4(y.x + next_row, y.y + next_row, y.z + next_row, y.w + next_row);
 #pragma unroll
-                for (int g = 0; g < BLOCKS / 4; ++g)
-                    gather4(sm.raw[slot] + (part * BLOCKS + 4 * g) * kBox, map, part * (kBox / 8), row4(row, g), &sm.raw_full[slot]);
+                for (int part = 0; part < PARTS; ++part)
+                    gather4(sm.raw[slot] + (part * BLOCKS + 4 * g) * kBox, map, part * (kBox / 8), y, &sm.raw_full[slot]);
+            }
         }
         tiles += n;
     }
@@ -734,15 +724,12 @@ __device__ __forceinline__ float stage_query(const T* query, size_t row_at, bool
     for (int b = 0; b < 32; b += BATCH * RPS) {
         uint4 raw[BATCH];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int r = b + k * RPS + sub;
-            const size_t at = __shfl_sync(0xffffffffu, row_at, r);
-            raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (alive >> r & 1) raw[k] = *reinterpret_cast<const uint4*>(query + at + 8 * i);
-        }
+        for (int k = 0; k < BATCH; ++k)  // (rows that do not exist read the first one: a branch would wait for each load)
+            raw[k] = *reinterpret_cast<const uint4*>(query + __shfl_sync(0xffffffffu, row_at, b + k * RPS + sub) + 8 * i);
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int r = b + k * RPS + sub;
+            const int r = b + k * RPS + sub, row = row0 + r;
+            if (!(alive >> r & 1)) raw[k] = make_uint4(0u, 0u, 0u, 0u);
             float x[8];
             unpack16<T>(raw[k], x);
             float mul = negate ? -1.f : 1.f;
@@ -752,12 +739,9 @@ __device__ __forceinline__ float stage_query(const T* query, size_t row_at, bool
                 for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                int e = 0;
-                if (most > 0.f && most <= 3.402823466e38f) {
-                    int ex;
-                    frexpf(most, &ex);  // most = f * 2^ex, f in [0.5, 1): the row's largest goes to [2^14, 2^15)
-                    e = min(max(15 - ex, -126), 126);
-                }
+                // most = f * 2^ex, f in [1, 2): the row's largest goes to [2^14, 2^15)
+                const int ex = (int)(__float_as_uint(most) >> 23) - 127;
+                const int e = most > 0.f && ex < 128 ? min(14 - ex, 126) : 0;
                 mul *= __int_as_float((e + 127) << 23);
                 const float back = __int_as_float((127 - e) << 23);
 #pragma unroll
@@ -772,7 +756,6 @@ __device__ __forceinline__ float stage_query(const T* query, size_t row_at, bool
                 const __half2 y = __floats2half2_rn(x[2 * j] * mul, x[2 * j + 1] * mul);
                 h[j] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            const int row = row0 + r;
             *reinterpret_cast<uint4*>(tile + row * 128 + (i / 8) * kPanel + (((i & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
     }
@@ -1072,6 +1055,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
             }
             mbar_init(&sm.o_full[i], 1);
         }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sm.side_full[i], 1);
+            mbar_init(&sm.copied[i], 1);
+        }
         for (int i = 0; i < Smem<D>::kRaw; ++i) {
             mbar_init(&sm.raw_full[i], 1);
             mbar_init(&sm.raw_empty[i], kWidenWarps);
@@ -1099,6 +1086,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
         widen_tiles<D, BS>(a, ws, sm);
     } else if (warp == kCopyWarp) {
         copy_tiles<D, BS>(a, ws, sm, &kmap, &vmap);
+    } else if (warp == kLookWarp) {
+        look_ahead<D, BS>(a, ws, sm);
     } else {
         const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
         issue_products<D>(a, ws, sm, t);
@@ -1128,18 +1117,19 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     const long long x = share * c1;
     if (x >= cost) return;
     const Entry en = ws.entries[find_entry(ws.entries, ws.head->entries, x)];
-    const int w = en.paired ? kPairedCost : kSplitCost;
-    const long long unit_cost = (long long)en.tiles * w;
-    const int kvh = (int)((x - en.first) / unit_cost);
-    const long long unit = en.first + kvh * unit_cost, end = unit + unit_cost;
+    const long long each = unit_cost(en.tiles, en.paired);
+    const int kvh = (int)((x - en.first) / each);
+    const long long unit = en.first + kvh * each, end = unit + each;
     if (x == unit || share * (c1 - 1) > unit) return;  // not inside, or not the first inside
     // pieces: CTA c has tiles [cut(c), cut(c + 1))
     auto cut = [&](int c) {
         const long long from = share * c - unit;
-        return from <= 0 ? 0 : tiles_in(from, en.tiles, en.paired != 0);
+        return tiles_in(from, en.tiles, en.paired != 0);
     };
     const int first = c1 - 1, last = (int)((end - 1) / share);
-    if (cut(first + 1) >= en.tiles) return;  // one piece after all
+    bool parts = false;  // (a boundary inside the cost may still fall before the first tile or behind the last)
+    for (int c = first + 1; c <= last; ++c) parts |= cut(c) > 0 && cut(c) < en.tiles;
+    if (!parts) return;
     const int n = rows_of(a, en.seq), group = a.num_heads / a.num_kv_heads;
     const int rows = min(n * group - en.row0, 2 * kTile);
     const int lane = threadIdx.x & 31;
