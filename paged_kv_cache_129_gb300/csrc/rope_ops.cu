@@ -10,6 +10,7 @@
 // sincospi(that / 2^31) is as exact as float32 gives.  One integer product per angle, no reduction.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -33,24 +34,66 @@ __device__ __forceinline__ float2 turn(uint64_t step, int pos, float factor) {
     return make_float2(c * factor, s * factor);
 }
 
-template <int BYTES>
-struct VecOf;
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
 template <>
-struct VecOf<16> { using type = uint4; };
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 template <>
-struct VecOf<4> { using type = uint32_t; };
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float2 x);
 template <>
-struct VecOf<2> { using type = uint16_t; };
+__device__ __forceinline__ uint32_t pack2<__half>(float2 x) {
+    const __half2 h = __float22half2_rn(x);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float2 x) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(x);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 
-// VB bytes = V elements of type T.
+// VB bytes = V elements of type T, taken two at a time where there are two: elements of 16 bits one at a time would occupy a
+// register each.
 template <typename T, int VB>
 struct Chunk {
-    static constexpr int V = VB / (int)sizeof(T);
-    typename VecOf<VB>::type raw;
-    __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const typename VecOf<VB>::type*>(p); }
-    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<typename VecOf<VB>::type*>(p) = raw; }
-    __device__ __forceinline__ float get(int i) const { return to_float(reinterpret_cast<const T*>(&raw)[i]); }
-    __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<T*>(&raw)[i] = from_float<T>(x); }
+    static constexpr int V = VB / (int)sizeof(T), W = VB < 4 ? 1 : VB / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VB == 16) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else if constexpr (VB == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (VB == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (VB == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+        else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+    }
+    // elements 2i and 2i + 1
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return unpack2<T>(w[i]);
+    }
+    __device__ __forceinline__ void put(int i, float2 x) {
+        if constexpr (sizeof(T) == 4) w[2 * i] = __float_as_uint(x.x), w[2 * i + 1] = __float_as_uint(x.y);
+        else w[i] = pack2<T>(x);
+    }
+    // the element of a chunk of one
+    __device__ __forceinline__ float one() const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[0]);
+        else return unpack2<T>(w[0]).x;
+    }
+    __device__ __forceinline__ void put_one(float x) {
+        if constexpr (sizeof(T) == 4) w[0] = __float_as_uint(x);
+        else w[0] = pack2<T>(make_float2(x, 0.f));
+    }
 };
 
 constexpr int kRopeThreads = 256;
@@ -62,19 +105,23 @@ constexpr int kRopeBatch = 4;   // rows that a thread has in flight
 template <typename T, int VB, bool INTERLEAVED>
 __device__ __forceinline__ void rotate(Chunk<T, VB>& x0, Chunk<T, VB>& x1, const float2* cs) {
     constexpr int V = Chunk<T, VB>::V;
+    if constexpr (V == 1) {
+        const float p = x0.one(), q = x1.one();
+        x0.put_one(p * cs[0].x - q * cs[0].y);
+        x1.put_one(p * cs[0].y + q * cs[0].x);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float2 t = cs[i];
-        if (INTERLEAVED && V > 1) {
-            Chunk<T, VB>& x = 2 * i < V ? x0 : x1;
-            const int e = (2 * i) % V;
-            const float p = x.get(e), q = x.get(e + 1);
-            x.set(e, p * t.x - q * t.y);
-            x.set(e + 1, p * t.y + q * t.x);
-        } else {
-            const float p = x0.get(i), q = x1.get(i);
-            x0.set(i, p * t.x - q * t.y);
-            x1.set(i, p * t.y + q * t.x);
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 a = x0.pair(i), b = x1.pair(i);
+            if (INTERLEAVED) {
+                const float2 t = cs[i], u = cs[V / 2 + i];
+                x0.put(i, make_float2(a.x * t.x - a.y * t.y, a.x * t.y + a.y * t.x));
+                x1.put(i, make_float2(b.x * u.x - b.y * u.y, b.x * u.y + b.y * u.x));
+            } else {
+                const float2 t = cs[2 * i], u = cs[2 * i + 1];
+                x0.put(i, make_float2(a.x * t.x - b.x * t.y, a.y * u.x - b.y * u.y));
+                x1.put(i, make_float2(a.x * t.y + b.x * t.x, a.y * u.y + b.y * u.x));
+            }
         }
     }
 }
@@ -176,184 +223,297 @@ __device__ __forceinline__ int warp_find(const int32_t* off, int n, int x, int l
     return lo;
 }
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a block of zeros
 
-__device__ __forceinline__ uint16_t to_codes(float a, float b) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+// e4m3 of four quotients y / scale, inv = 1 / scale rounded.  y * inv is within 2 steps of float32 of the quotient, and codes change
+// at values whose lower 19 bits of mantissa are zero (four bits are kept, one decides; fewer below 2^-6): next to
+// those alone the division is made.  (16 divisions a slot took more registers than there are for two CTAs per SM.)
+__device__ __forceinline__ uint32_t codes_of(float y0, float y1, float y2, float y3, float scale, float inv) {
+    float q[4] = {y0 * inv, y1 * inv, y2 * inv, y3 * inv};
+    unsigned near = ~0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) near = min(near, (__float_as_uint(q[i]) + 4) & 0x7ffffu);
+    if (near < 9) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // (one division in the code, not sixteen)
+            const float x = y0 / scale;
+            y0 = y1, y1 = y2, y2 = y3;
+            q[0] = q[1], q[1] = q[2], q[2] = q[3], q[3] = x;
+        }
+    }
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3) |
+           ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3) << 16);
 }
 
-// One unit: the rows of the call that fall into one block of one request, one kv head, K or V.  A warp holds them
-// in float32, D / 4 lanes to a row: (2p, 2p + 1) and their partners of two pairs (half layout), or four neighbours.
-template <typename T, int D, int BS>
-__device__ __forceinline__ void append_unit(const RopeAppendArgs& a, int tok, int n, int off, int pos, long long blk, int h,
-                                            bool is_value, int lane) {
-    constexpr int LPR = D / 4, RPS = 32 / LPR, STEPS = BS / RPS;
-    const RopeArgs& r = a.r;
-    const int l = lane % LPR, sub = lane / LPR;
-    const int half = r.rotary_dim / 2;
-    const T* src = is_value ? static_cast<const T*>(r.value) + h * D + (long long)tok * r.v_stride
-                            : static_cast<const T*>(r.key) + h * D + (long long)tok * r.k_stride;
-    const long long stride = is_value ? r.v_stride : r.k_stride;
-    // element places of this lane: e, e + 1 and f, f + 1
-    int e = 4 * l, f = 4 * l + 2;
-    const bool turns = !is_value && 4 * l < r.rotary_dim;
-    if (turns && !r.interleaved) {
-        e = 2 * l;
-        f = 2 * l + half;
-    }
-    uint64_t s0 = 0, s1 = 0;
-    if (turns) {  // pairs 2l and 2l + 1 in either layout
-        s0 = turn_step(r.inv_freq[2 * l]);
-        s1 = turn_step(r.inv_freq[2 * l + 1]);
-    }
-    float x[STEPS][4];
-    float most = 0.f;
+// (cos, sin) of a token's pairs in shared memory, for slots of V pairs: two pairs to 16 bytes, those of neighbouring slots
+// next to each other, so that the lanes of a row read without bank conflicts.
+template <int V>
+__device__ __forceinline__ int turn_place(int pair, int slots) {
+    return V == 1 ? pair : (((pair % V) / 2) * slots + pair / V) * 2 + pair % 2;
+}
+template <int V>
+__device__ __forceinline__ void load_turns(float2 (&cs)[V], const float2* of_token, int slot, int slots) {
+    if constexpr (V == 1) {
+        cs[0] = of_token[slot];
+    } else {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int row = i * RPS + sub;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[i][k] = 0.f;
-        if (row < n) {
-            const T* p = src + row * stride;
-            x[i][0] = to_float(p[e]);
-            x[i][1] = to_float(p[e + 1]);
-            x[i][2] = to_float(p[f]);
-            x[i][3] = to_float(p[f + 1]);
+        for (int j = 0; j < V / 2; ++j) {
+            const float4 w = *reinterpret_cast<const float4*>(of_token + (j * slots + slot) * 2);
+            cs[2 * j] = make_float2(w.x, w.y);
+            cs[2 * j + 1] = make_float2(w.z, w.w);
         }
     }
-    const size_t si = (size_t)blk * r.num_kv_heads + h;
+}
+
+// The V pairs of one slot in float32: first[] and second[], rotated where TURNS is set.  Interleaved slots hold V pairs too.
+template <typename T, int VB>
+__device__ __forceinline__ void turned(const Chunk<T, VB>& x0, const Chunk<T, VB>& x1, const float2* cs, bool turns, bool interleaved,
+                                       float* y0, float* y1) {
+    constexpr int V = Chunk<T, VB>::V;
+    if constexpr (V == 1) {
+        y0[0] = x0.one();
+        y1[0] = x1.one();
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 a = x0.pair(i), b = x1.pair(i);
+            y0[2 * i] = a.x, y0[2 * i + 1] = a.y;
+            y1[2 * i] = b.x, y1[2 * i + 1] = b.y;
+        }
+    }
+    if (!turns) return;
+    if (V > 1 && interleaved) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float* y = 2 * i < V ? y0 : y1;
+            const int e = (2 * i) % V;
+            const float p = y[e], q = y[e + (V > 1 ? 1 : 0)];
+            y[e] = p * cs[i].x - q * cs[i].y;
+            y[e + (V > 1 ? 1 : 0)] = p * cs[i].y + q * cs[i].x;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float p = y0[i], q = y1[i];
+            y0[i] = p * cs[i].x - q * cs[i].y;
+            y1[i] = p * cs[i].y + q * cs[i].x;
+        }
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* y, float scale, float inv) {
+    if constexpr (V == 1) {
+        *p = (uint8_t)codes_of(y[0], y[0], y[0], y[0], scale, inv);
+    } else {
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) w[i] = codes_of(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3], scale, inv);
+        if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+}
+
+__device__ __forceinline__ uint32_t requantised(uint32_t c, float held, float scale, float inv) {
+    const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3)));
+    const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3)));
+    return codes_of(lo.x * held, lo.y * held, hi.x * held, hi.y * held, scale, inv);
+}
+
+// The codes that a block holds already, in a larger scale.  One warp.
+__device__ __noinline__ void requantise(uint4* at, int units, float held, float scale, float inv, int lane) {
+    for (int i = lane; i < units; i += 128) {
+        uint4 c[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + 32 * u < units) c[u] = at[i + 32 * u];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + 32 * u < units)
+                at[i + 32 * u] = make_uint4(requantised(c[u].x, held, scale, inv), requantised(c[u].y, held, scale, inv),
+                                            requantised(c[u].z, held, scale, inv), requantised(c[u].w, held, scale, inv));
+    }
+}
+
+// The new rows of one block of one request.
+struct AppendPiece {
+    int tok, rows, off;  // first row, rows, offset of the first in its block
+    int blk;
+};
+
+// One unit: a piece, one kv head, K or V, by a warp.  Rows are slots of two chunks as in rope_write_kv, RPS rows side by
+// side.  Two passes, since the scale comes before the codes; the second reads the rows again, from L1 or L2, and rotates them
+// again: holding a block between the passes takes 32 to 64 registers more than there are (prompt chunks 70 us instead of 51).
+template <typename T, int D, int BS, int VB>
+__device__ __forceinline__ void append_unit(const RopeAppendArgs& a, const AppendPiece& piece, int h, bool is_value,
+                                            const float2* cs_of_first, int lane) {
+    constexpr int V = Chunk<T, VB>::V, NS = D / (2 * V), LPR = NS < 32 ? NS : 32, SPL = NS / LPR, RPS = 32 / LPR;
+    constexpr int STEPS = BS / RPS;
+    const RopeArgs& r = a.r;
+    const int sub = lane / LPR, half = r.rotary_dim / 2, n = piece.rows, off = piece.off;
+    const T* src = is_value ? static_cast<const T*>(r.value) + h * D + (long long)piece.tok * r.v_stride
+                            : static_cast<const T*>(r.key) + h * D + (long long)piece.tok * r.k_stride;
+    const long long stride = is_value ? r.v_stride : r.k_stride;
+    const size_t si = (size_t)piece.blk * r.num_kv_heads + h;
     float* scale_at = (is_value ? a.v_scale : a.k_scale) + si;
     const float held = off > 0 ? *scale_at : 0.f;  // a block that starts here has no scale yet
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int row = i * RPS + sub;
-        if (turns && row < n) {
-            const float2 t0 = turn(s0, pos + row, r.factor), t1 = turn(s1, pos + row, r.factor);
-            float *p0, *q0, *p1, *q1;
-            if (r.interleaved) {
-                p0 = &x[i][0], q0 = &x[i][1], p1 = &x[i][2], q1 = &x[i][3];
-            } else {
-                p0 = &x[i][0], q0 = &x[i][2], p1 = &x[i][1], q1 = &x[i][3];
-            }
-            const float u = *p0 * t0.x - *q0 * t0.y, v = *p0 * t0.y + *q0 * t0.x;
-            const float w = *p1 * t1.x - *q1 * t1.y, z = *p1 * t1.y + *q1 * t1.x;
-            *p0 = u, *q0 = v, *p1 = w, *q1 = z;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float m = fabsf(x[i][k]);
-            if (m <= 3.402823466e38f) most = fmaxf(most, m);  // infinities saturate, NaN stays: neither sets a scale
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float scale = fmaxf(fmaxf(held, most / 448.f), kScaleFloor);
+    float most = 0.f, scale = 0.f, inv = 0.f;
     const bool both = a.value_cache == nullptr;
     uint8_t* base = both ? a.key_cache + (si * 2 + (is_value ? 1 : 0)) * BS * D
                          : (is_value ? a.value_cache : a.key_cache) + si * BS * D;
-    if (scale > held && off > 0) {  // the codes that the block holds already, in the larger scale
-        for (int i = lane; i < off * (D / 4); i += 32) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(base) + i;
-            const uint32_t c = *w;
-            const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3)));
-            const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3)));
-            *w = (uint32_t)to_codes(lo.x * held / scale, lo.y * held / scale) |
-                 ((uint32_t)to_codes(hi.x * held / scale, hi.y * held / scale) << 16);
-        }
-    }
+    // one slot of one row: pass 0 its largest magnitude, pass 1 its codes
+    auto slot_of = [&](auto pass, const Chunk<T, VB>& x0, const Chunk<T, VB>& x1, int row, int sl, int e0, int e1, bool turns) {
+        float2 cs[V];
+        float y0[V], y1[V];
+        if (turns) load_turns<V>(cs, cs_of_first + row * half, sl, half / V);
+        turned<T, VB>(x0, x1, cs, turns, r.interleaved, y0, y1);
+        if constexpr (decltype(pass)::value == 0) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int row = i * RPS + sub;
-        if (row < n) {
+            for (int i = 0; i < V; ++i) {  // infinities saturate, NaN stays: neither sets a scale
+                const float m0 = fabsf(y0[i]), m1 = fabsf(y1[i]);
+                if (m0 <= 3.402823466e38f) most = fmaxf(most, m0);
+                if (m1 <= 3.402823466e38f) most = fmaxf(most, m1);
+            }
+        } else {
             uint8_t* p = base + (off + row) * D;
-            *reinterpret_cast<uint16_t*>(p + e) = to_codes(x[i][0] / scale, x[i][1] / scale);
-            *reinterpret_cast<uint16_t*>(p + f) = to_codes(x[i][2] / scale, x[i][3] / scale);
+            store_codes<V>(p + e0, y0, scale, inv);
+            store_codes<V>(p + e1, y1, scale, inv);
         }
-    }
+    };
+    auto all = [&](auto pass) {
+#pragma unroll 1
+        for (int j = 0; j < STEPS * SPL; ++j) {
+            const int row = j / SPL * RPS + sub, sl = j % SPL * LPR + lane % LPR;
+            if (row >= n) continue;
+            const bool turns = !is_value && sl < half / V, pairs = !turns || r.interleaved;  // neighbouring chunks
+            const int e0 = pairs ? 2 * V * sl : V * sl, e1 = pairs ? e0 + V : e0 + half;
+            Chunk<T, VB> x0, x1;
+            x0.load(src + row * stride + e0);
+            x1.load(src + row * stride + e1);
+            slot_of(pass, x0, x1, row, sl, e0, e1, turns);
+        }
+    };
+    all(std::integral_constant<int, 0>());
+    // (magnitudes are not negative: their order is that of their bits)
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    scale = fmaxf(fmaxf(held, most / 448.f), kScaleFloor);
+    inv = 1.f / scale;
+    if (scale > held && off > 0) requantise(reinterpret_cast<uint4*>(base), off * (D / 16), held, scale, inv, lane);
+    all(std::integral_constant<int, 1>());
     __syncwarp();
     if (lane == 0 && scale != held) *scale_at = scale;
 }
 
-// CTAs [0, kv_ctas): warps over (window of `window` tokens, kv head, K or V), each owning the blocks whose first
-// row of this call lies in its window.  The others: a warp per token's query heads.
-template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kAppendThreads) rope_append_fp8_kernel(const RopeAppendArgs a, int kv_ctas, int window) {
+// CTA (window, part): the query rows of a window of `window` tokens, and the blocks whose first row of this call lies in it.
+// Their positions are found and their angles computed once, in shared memory; warps then take units and groups of query
+// heads in turn, every parts-th CTA's worth of them.
+template <typename T, int D, int BS, int VB>
+__global__ void __launch_bounds__(kAppendThreads, 2) rope_append_fp8_kernel(const RopeAppendArgs a, int window, int parts) {
+    constexpr int V = Chunk<T, VB>::V, NS = D / (2 * V), LPR = NS < 32 ? NS : 32, SPL = NS / LPR, RPS = 32 / LPR;
+    constexpr int kBatch = 2, kGroup = kBatch * RPS;  // query heads of a warp's turn
+    extern __shared__ __align__(16) float2 cs[];      // [window + BS - 1][rotary_dim / 2], see turn_place()
+    __shared__ AppendPiece pieces[BS];
+    __shared__ uint64_t steps[D / 2];
+    __shared__ int position[2 * BS];
+    __shared__ int num_pieces, num_positions;
+    __shared__ unsigned rotated;  // tokens of the window that belong to a request
     griddep_wait();
     griddep_launch_dependents();
     const RopeArgs& r = a.r;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int B = a.num_seqs;
-    if ((int)blockIdx.x < kv_ctas) {
-        long long w = (long long)blockIdx.x * (kAppendThreads / 32) + warp;
-        const bool is_value = w & 1;
-        w >>= 1;
-        const int h = (int)(w % r.num_kv_heads);
-        const long long win = w / r.num_kv_heads;
-        long long t = win * window;
-        const int end = (int)min((long long)r.num_tokens, (win + 1) * window);
-        while (t < end) {
-            const int b = warp_find(a.q_offsets, B + 1, (int)t, lane);
-            if (b < 0 || b >= B) return;  // rows behind the last request
-            const int first = a.q_offsets[b], last = min(a.q_offsets[b + 1], r.num_tokens), L = a.context_lens[b];
-            const long long start = (long long)L - ((long long)a.q_offsets[b + 1] - first);  // position of its first row
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.num_seqs, half = r.rotary_dim / 2;
+    const int part = blockIdx.x % parts;
+    const int t0 = (int)(blockIdx.x / parts) * window;
+    if (warp == 0) {
+        const int t = t0 + lane, tokens = min(window, r.num_tokens - t0);
+        int lo = warp_find(a.q_offsets, B + 1, t0, lane);
+        int hi = (tokens > 1 ? warp_find(a.q_offsets, B + 1, t0 + tokens - 1, lane) : lo) + 1;
+        while (hi - lo > 1) {  // largest b in [lo, hi) whose rows begin at or before t
+            const int mid = lo + (hi - lo) / 2;
+            if (a.q_offsets[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        const bool in = lane < tokens && lo >= 0 && lo < B;
+        bool own = false;
+        int pos = 0, n = 0, off = 0, blk = 0;
+        if (in) {
+            const int first = a.q_offsets[lo], next = a.q_offsets[lo + 1], L = a.context_lens[lo];
+            const long long start = (long long)L - ((long long)next - first);  // position of its first row
+            pos = (int)(start + (t - first));
             if (start < 0 || L > (long long)a.max_blocks * BS) {
-                if (lane == 0 && t == first) atomicOr(r.err, kErrBadContext);
-                t = last;
-                continue;
-            }
-            const int pos = (int)(start + (t - first)), off = pos % BS;
-            if (t != first && off != 0) {  // the block belongs to an earlier window
-                t += BS - off;
-                if (t > last) t = last;
-                continue;
-            }
-            const int n = min(BS - off, last - (int)t);
-            const long long blk = a.block_tables[(size_t)b * a.max_blocks + pos / BS];
-            if (blk < 0 || blk >= r.num_blocks) {
-                if (lane == 0) atomicOr(r.err, kErrBadTable);
+                if (t == first && part == 0) atomicOr(r.err, kErrBadContext);
             } else {
-                append_unit<T, D, BS>(a, (int)t, n, off, pos, blk, h, is_value, lane);
+                off = pos % BS;
+                n = min(BS - off, min(next, r.num_tokens) - t);
+                own = n > 0 && (t == first || off == 0);
+                if (own) blk = a.block_tables[(size_t)lo * a.max_blocks + pos / BS];
+                if (own && (blk < 0 || blk >= r.num_blocks)) {
+                    if (part == 0) atomicOr(r.err, kErrBadTable);
+                    own = false;
+                }
             }
-            t += n;
+            position[lane] = pos;
         }
-        return;
+        const unsigned owners = __ballot_sync(0xffffffffu, own), some = __ballot_sync(0xffffffffu, in);
+        if (own) pieces[__popc(owners & ((1u << lane) - 1))] = AppendPiece{t, n, off, blk};
+        // the last piece may reach past the window
+        const int last = owners ? 31 - __clz(owners) : 0;
+        const int end = owners ? last + __shfl_sync(0xffffffffu, n, last) : 0, last_pos = __shfl_sync(0xffffffffu, pos, last);
+        if (tokens + lane < end) position[tokens + lane] = last_pos + (tokens + lane - last);
+        if (lane == 0) {
+            num_pieces = __popc(owners);
+            num_positions = max(some ? 32 - __clz(some) : 0, end);
+            rotated = some;
+        }
+    } else {
+        for (int i = tid - 32; i < half; i += kAppendThreads - 32) steps[i] = turn_step(r.inv_freq[i]);
     }
-    // query rows: lanes as in append_unit
-    constexpr int LPR = D / 4, RPS = 32 / LPR;
-    const int t = (int)(((long long)blockIdx.x - kv_ctas) * (kAppendThreads / 32) + warp);
-    if (t >= r.num_tokens) return;
-    const int b = warp_find(a.q_offsets, B + 1, t, lane);
-    if (b < 0 || b >= B) return;
-    const int pos = a.context_lens[b] - (a.q_offsets[b + 1] - t);
-    const int l = lane % LPR, sub = lane / LPR, half = r.rotary_dim / 2;
-    const bool turns = 4 * l < r.rotary_dim;
-    int e = 4 * l, f = 4 * l + 2;
-    if (turns && !r.interleaved) {
-        e = 2 * l;
-        f = 2 * l + half;
+    __syncthreads();
+    for (int i = tid; i < num_positions * half; i += kAppendThreads) {
+        const int t = i / half, pair = i - t * half;
+        const float2 x = turn(steps[pair], position[t], r.factor);
+        cs[t * half + turn_place<V>(pair, half / V)] = x;
     }
-    float2 t0 = make_float2(1.f, 0.f), t1 = t0;
-    if (turns) {
-        t0 = turn(turn_step(r.inv_freq[2 * l]), pos, r.factor);
-        t1 = turn(turn_step(r.inv_freq[2 * l + 1]), pos, r.factor);
-    }
-    const T* src = static_cast<const T*>(r.query) + (long long)t * r.q_stride;
-    T* dst = static_cast<T*>(r.query_out) + (long long)t * r.num_heads * D;
-#pragma unroll 4
-    for (int h = sub; h < r.num_heads; h += RPS) {
-        T y[4] = {src[h * D + e], src[h * D + e + 1], src[h * D + f], src[h * D + f + 1]};
-        if (turns) {
-            const float x0 = to_float(y[0]), x1 = to_float(y[1]), x2 = to_float(y[2]), x3 = to_float(y[3]);
-            if (r.interleaved) {
-                y[0] = from_float<T>(x0 * t0.x - x1 * t0.y), y[1] = from_float<T>(x0 * t0.y + x1 * t0.x);
-                y[2] = from_float<T>(x2 * t1.x - x3 * t1.y), y[3] = from_float<T>(x2 * t1.y + x3 * t1.x);
-            } else {
-                y[0] = from_float<T>(x0 * t0.x - x2 * t0.y), y[2] = from_float<T>(x0 * t0.y + x2 * t0.x);
-                y[1] = from_float<T>(x1 * t1.x - x3 * t1.y), y[3] = from_float<T>(x1 * t1.y + x3 * t1.x);
+    __syncthreads();
+    const int units = num_pieces * r.num_kv_heads * 2, groups = (r.num_heads + kGroup - 1) / kGroup;
+    const int tokens = min(window, r.num_tokens - t0), items = units + tokens * groups;
+    for (int item = part * kAppendWarps + warp; item < items; item += parts * kAppendWarps) {
+        if (item < units) {
+            const int of_piece = item / (r.num_kv_heads * 2), u = item - of_piece * (r.num_kv_heads * 2);
+            const AppendPiece piece = pieces[of_piece];
+            append_unit<T, D, BS, VB>(a, piece, u >> 1, u & 1, cs + (piece.tok - t0) * half, lane);
+            continue;
+        }
+        const int i = (item - units) / groups, head0 = (item - units - i * groups) * kGroup;
+        if (!(rotated >> i & 1)) continue;
+        const T* src = static_cast<const T*>(r.query) + (long long)(t0 + i) * r.q_stride;
+        T* dst = static_cast<T*>(r.query_out) + (long long)(t0 + i) * r.num_heads * D;
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+            const int sl = s * LPR + lane % LPR;
+            const bool turns = sl < half / V, pairs = !turns || r.interleaved;  // neighbouring chunks
+            const int e0 = pairs ? 2 * V * sl : V * sl, e1 = pairs ? e0 + V : e0 + half;
+            float2 c[V];
+            if (turns) load_turns<V>(c, cs + i * half, sl, half / V);
+            Chunk<T, VB> x0[kBatch], x1[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int h = head0 + k * RPS + lane / LPR;
+                if (h < r.num_heads) {
+                    x0[k].load(src + h * D + e0);
+                    x1[k].load(src + h * D + e1);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int h = head0 + k * RPS + lane / LPR;
+                if (h >= r.num_heads) continue;
+                if (turns && r.interleaved) rotate<T, VB, true>(x0[k], x1[k], c);
+                else if (turns) rotate<T, VB, false>(x0[k], x1[k], c);
+                x0[k].store(dst + h * D + e0);
+                x1[k].store(dst + h * D + e1);
             }
         }
-        dst[h * D + e] = y[0], dst[h * D + e + 1] = y[1], dst[h * D + f] = y[2], dst[h * D + f + 1] = y[3];
     }
 }
 
@@ -372,48 +532,56 @@ cudaError_t rope_write_typed(const RopeWriteArgs& a, cudaStream_t stream) {
 
 // Whether a row splits into chunks of vb bytes: aligned bases and strides, and slots of two chunks that do not
 // straddle the end of the pairs.
-bool rope_splits(const RopeWriteArgs& a, int eb, int vb) {
-    const RopeArgs& r = a.r;
+bool rope_splits(const RopeArgs& r, int eb, int vb) {
     const int v = vb / eb;
     if (r.head_dim % (2 * v) || r.head_dim / (2 * v) > kRopeThreads || (r.rotary_dim / 2) % v) return false;
     if ((r.head_dim - r.rotary_dim) % (2 * v)) return false;
-    for (const void* p : {(const void*)r.query_out, r.query, r.key, r.value, (const void*)a.key_cache, (const void*)a.value_cache})
+    for (const void* p : {(const void*)r.query_out, r.query, r.key, r.value})
         if (!multiple(p, vb)) return false;
     return (r.q_stride * eb) % vb == 0 && (r.k_stride * eb) % vb == 0 && (r.v_stride * eb) % vb == 0;
 }
 
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, int VB>
 cudaError_t append_typed(const RopeAppendArgs& a, cudaStream_t stream) {
     const RopeArgs& r = a.r;
-    constexpr int warps = kAppendThreads / 32;
-    // A window is a block long, so that a prompt has one unit per window; while one window per token does not
-    // fill the GPU, every token has its own, so that the units of a decode step do not queue behind one another.
-    const long long per_token = (long long)r.num_tokens * r.num_kv_heads * 2;
-    const int window = per_token <= (long long)a.num_sms * warps * 4 ? 1 : BS;
-    const long long kv_warps = (long long)((r.num_tokens + window - 1) / window) * r.num_kv_heads * 2;
-    const long long kv_ctas = (kv_warps + warps - 1) / warps;
-    const long long q_ctas = (r.num_tokens + warps - 1) / warps;
-    return launch_pdl(rope_append_fp8_kernel<T, D, BS>, dim3((unsigned)(kv_ctas + q_ctas)), dim3(kAppendThreads), 0, stream,
-                      a, (int)kv_ctas, window);
+    constexpr int V = VB / (int)sizeof(T), NS = D / (2 * V), RPS = NS < 32 ? 32 / NS : 1;
+    // A window is a block long, so that a prompt has one block per window; while a window per token does not fill the
+    // GPU, every token has its own, so that the tokens of a decode step do not queue behind one another.  (2300 tokens of 37 requests,
+    // 32 kv heads: 59 us, with a window per token 129; 64 decode tokens: 9.8 us on the GPU, 19.6 with warps that took several.)
+    const int window = r.num_tokens <= 2 * a.num_sms ? 1 : BS;
+    const long long windows = (r.num_tokens + window - 1) / window;
+    // The rows of a window are shared among parts of CTAs, down to a turn per warp, while that makes at most four CTAs per SM
+    // (prompt chunks / 32 kv heads, us: two 50 / 69, four 49 / 55, eight 53 / 59, sixteen 59 / 58).
+    const long long items = 2ll * r.num_kv_heads + (long long)window * ((r.num_heads + 2 * RPS - 1) / (2 * RPS));
+    const long long parts = std::max(1ll, std::min((items + kAppendWarps - 1) / kAppendWarps, 4ll * a.num_sms / windows));
+    const size_t smem = (size_t)(window + BS - 1) * (r.rotary_dim / 2) * sizeof(float2);
+    return launch_pdl(rope_append_fp8_kernel<T, D, BS, VB>, dim3((unsigned)(windows * parts)), dim3(kAppendThreads), smem, stream,
+                      a, window, (int)parts);
+}
+
+template <typename T, int VB>
+cudaError_t append_dispatch(const RopeAppendArgs& a, cudaStream_t stream) {
+    const int d = a.r.head_dim, bs = a.r.block_size;
+    if (d == 128 && bs == 16) return append_typed<T, 128, 16, VB>(a, stream);
+    if (d == 128 && bs == 32) return append_typed<T, 128, 32, VB>(a, stream);
+    if (d == 64 && bs == 16) return append_typed<T, 64, 16, VB>(a, stream);
+    if (d == 64 && bs == 32) return append_typed<T, 64, 32, VB>(a, stream);
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t append_dispatch(const RopeAppendArgs& a, cudaStream_t stream) {
-    const int d = a.r.head_dim, bs = a.r.block_size;
-    if (d == 128 && bs == 16) return append_typed<T, 128, 16>(a, stream);
-    if (d == 128 && bs == 32) return append_typed<T, 128, 32>(a, stream);
-    if (d == 64 && bs == 16) return append_typed<T, 64, 16>(a, stream);
-    if (d == 64 && bs == 32) return append_typed<T, 64, 32>(a, stream);
-    return cudaErrorInvalidValue;
+cudaError_t append_split(const RopeAppendArgs& a, cudaStream_t stream) {
+    return rope_splits(a.r, sizeof(T), 16) ? append_dispatch<T, 16>(a, stream) : append_dispatch<T, (int)sizeof(T)>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t rope_write_kv_launch(const RopeWriteArgs& a, cudaStream_t stream) {
     const int eb = a.r.dtype == 0 ? 4 : 2;
+    auto splits = [&](int vb) { return multiple(a.key_cache, vb) && multiple(a.value_cache, vb) && rope_splits(a.r, eb, vb); };
     if (a.r.dtype == 0)
-        return rope_splits(a, eb, 16) ? rope_write_typed<float, 16>(a, stream) : rope_write_typed<float, 4>(a, stream);
-    const int vb = rope_splits(a, eb, 16) ? 16 : rope_splits(a, eb, 4) ? 4 : 2;
+        return splits(16) ? rope_write_typed<float, 16>(a, stream) : rope_write_typed<float, 4>(a, stream);
+    const int vb = splits(16) ? 16 : splits(4) ? 4 : 2;
     if (a.r.dtype == 1)
         return vb == 16  ? rope_write_typed<__half, 16>(a, stream)
                : vb == 4 ? rope_write_typed<__half, 4>(a, stream)
@@ -425,9 +593,9 @@ cudaError_t rope_write_kv_launch(const RopeWriteArgs& a, cudaStream_t stream) {
 
 cudaError_t rope_append_fp8_launch(const RopeAppendArgs& a, cudaStream_t stream) {
     switch (a.r.dtype) {
-        case 0: return append_dispatch<float>(a, stream);
-        case 1: return append_dispatch<__half>(a, stream);
-        default: return append_dispatch<__nv_bfloat16>(a, stream);
+        case 0: return append_split<float>(a, stream);
+        case 1: return append_split<__half>(a, stream);
+        default: return append_split<__nv_bfloat16>(a, stream);
     }
 }
 
