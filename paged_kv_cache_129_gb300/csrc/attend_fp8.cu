@@ -1179,7 +1179,8 @@ cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUt
     if (e != cudaSuccess) return e;
     e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, kmap, vmap);
     if (e != cudaSuccess || ctas < 2) return e;
-    return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 4), dim3(kJoinThreads), 0, stream, a, ws, ctas);
+    // (a boundary's 256 rows on 16 CTAs, two rows a warp: short mixed requests 95 to 90 us against 4 CTAs, 93 with 32)
+    return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 16), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
 
 }  // namespace
