@@ -157,8 +157,7 @@ int pa_rope_write_kv(void* query_out, const void* query, const void* key, const 
     a.value_cache = value_cache;
     a.positions = positions;
     a.slot_mapping = slot_mapping;
-    int sms = 0;
-    st = device_state(&a.r.err, &sms);
+    st = device_state(&a.r.err, &a.num_sms);
     if (st != PA_OK) return st;
     const cudaError_t e = rope_write_kv_launch(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : launch_failed(e, "pa_rope_write_kv");

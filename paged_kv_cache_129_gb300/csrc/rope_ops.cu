@@ -98,7 +98,7 @@ struct Chunk {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 4;  // tokens of a CTA, at most
-constexpr int kRopeBatch = 4;   // rows that a thread has in flight
+constexpr int kRopeBatch = 2;   // rows that a thread has in flight (8192 tokens: two 31.0 us, four 33.5)
 
 // Turns the V pairs of one slot of a head row, held in two chunks.  Half layout: chunk 0 holds the pairs' first
 // elements, chunk 1 their second; interleaved: the two chunks are 2V neighbours.
@@ -521,8 +521,9 @@ bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_
 
 template <typename T, int VB>
 cudaError_t rope_write_typed(const RopeWriteArgs& a, cudaStream_t stream) {
-    // Four tokens share a CTA when that still fills the GPU; few tokens take a CTA each.
-    const int per = a.r.num_tokens >= 4096 ? kRopeTokens : 1;
+    // Four tokens share a CTA when that still gives every SM one; fewer tokens take a CTA each.  (8192 tokens, bf16: 31 us, with a
+    // CTA per token 42; 1001 tokens, f32: 5.3, 7.4; 64 tokens: 8.0, 5.4.)
+    const int per = a.r.num_tokens >= kRopeTokens * a.num_sms ? kRopeTokens : 1;
     const unsigned grid = (unsigned)((a.r.num_tokens + per - 1) / per);
     const size_t smem = (size_t)per * (a.r.rotary_dim / 2) * sizeof(float2);
     if (a.r.interleaved)

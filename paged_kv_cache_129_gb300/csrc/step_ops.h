@@ -46,6 +46,7 @@ struct RopeWriteArgs {
     void* value_cache;
     const int32_t* positions;
     const int64_t* slot_mapping;
+    int num_sms;
 };
 
 struct RopeAppendArgs {
