@@ -328,6 +328,62 @@ def test_rope_append_fp8(case, dtype, records, layout):
     assert np.array_equal(gk[rest], kc[rest])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_append_fp8_of_views_at_odd_addresses(dtype, layout):
+    """Rows that begin at any element and follow one another at an odd distance."""
+    rng = np.random.default_rng(21)
+    hq, hkv, d, bs, old, new = 3, 2, 64, 16, [5, 0, 30], [1, 40, 3]
+    kc, vc, ks, vs, tables, lens = ref.paged(rng, np.array(old) + new, hkv, d, bs, nan_tail=False)
+    off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    t, width = int(off[-1]), (hq + 2 * hkv) * d + 3
+    flat = torch.from_numpy((rng.standard_normal(t * width + 1) * 3).astype(np.float32)).to(T[dtype]).cuda()
+    rows = flat[1:].view(t, width)
+    q, k, v = (rows[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, hq), (hq, hq + hkv), (hq + hkv, hq + 2 * hkv)))
+    inv = pa.rope_frequencies(d, device="cuda")
+    dk, dv, dks, dvs = up(kc), up(vc), up(ks), up(vs)
+    got = pa.rope_append_fp8(q, k, v, dk, dv, dks, dvs, inv, up(tables), up(lens), up(off), layout=layout)
+    pa.check_error()
+    pos = np.concatenate([np.arange(a, a + n) for a, n in zip(old, new)])
+    want, slack = ref.rotate(f64(q), pos, inv.cpu().numpy(), layout, 1.0)
+    near(f64(got), want, slack, dtype)
+    _, want_v, want_s = expected_append(f64(v), True, vc, vs, tables, lens, off, bs)
+    assert np.array_equal(dv.cpu().numpy(), want_v) and np.array_equal(dvs.cpu().numpy(), want_s)
+    xk, _ = ref.rotate(f64(k), pos, inv.cpu().numpy(), layout, 1.0)
+    units, _, _ = expected_append(xk, False, kc, ks, tables, lens, off, bs)
+    gk, gs = dk.cpu().numpy(), dks.cpu().numpy().astype(np.float64)
+    for (blk, h), (row, o, n, s, held) in units.items():
+        assert abs(gs[blk, h] - s) <= 1.5e-6 * s
+        x = xk[row:row + n, h]
+        err = np.abs(ref.E4M3[gk[blk, h, o:o + n]] * gs[blk, h] - x)
+        assert (err <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * s) + 2e-6 * 448 * s).all()
+
+
+@pytest.mark.parametrize("scale", [1.0, 3.0, 0.7, 1.1e-30, 5e35])
+def test_rope_append_fp8_codes_of_values_next_to_ties(scale):
+    """Codes are those of the float32 quotient, at the midpoints between E4M3 values and a few float32 steps beside them too."""
+    finite = ref.E4M3[:0x7F].astype(np.float64)
+    mid = (finite[1:] + finite[:-1]) / 2
+    d, bs, hkv = 128, 16, 1
+    scale = np.float32(scale)
+    x = np.zeros((bs, hkv, d), np.float32)
+    base = (np.concatenate([mid, [0.0, 448.0]]).astype(np.float64) * float(scale)).astype(np.float32)
+    for r in range(bs):  # row r: r - 8 steps of float32 beside them
+        y = base.copy()
+        y[y > 0] = (y[y > 0].view(np.int32) + (r - 8)).view(np.float32)
+        x[r, 0] = np.minimum(y, np.float32(448) * scale) * np.where(np.arange(d) % 2, -1, 1)
+    tables, lens, off = np.zeros((1, 1), np.int32), np.array([bs], np.int32), np.array([0, bs], np.int32)
+    kc, ks = np.zeros((1, hkv, bs, d), np.uint8), np.zeros((1, hkv), np.float32)
+    dk, dv, dks, dvs = up(kc), up(kc), up(ks), up(ks)
+    pa.rope_append_fp8(torch.zeros(bs, 1, d, device="cuda"), up(x), up(x), dk, dv, dks, dvs, None, up(tables), up(lens), up(off))
+    pa.check_error()
+    _, codes, want = expected_append(x.astype(np.float64), True, kc, ks, tables, lens, off, bs)
+    for c, s in ((dk, dks), (dv, dvs)):
+        assert np.array_equal(s.cpu().numpy(), want)
+        assert np.array_equal(c.cpu().numpy() & 0x7F, codes & 0x7F)
+        assert np.array_equal(c.cpu().numpy()[codes & 0x7F != 0], codes[codes & 0x7F != 0])
+
+
 def test_rope_append_fp8_special_values():
     """Zeros, infinities, NaN and values next to float32's ends; no rotation."""
     hkv, d, bs = 2, 64, 16
@@ -598,6 +654,51 @@ def test_captured_steps_share_a_workspace_and_match_direct_calls():
         t = int(direct.buffers[2][-1])
         assert torch.equal(a.out[:t], direct.out[:t]) and torch.equal(a.tables, direct.tables)
         assert torch.equal(a.kc, direct.kc) and torch.equal(a.ks, direct.ks)
+
+
+@pytest.mark.parametrize("t", [607, 608, 611])
+def test_rope_write_kv_of_many_tokens_is_that_of_each(t):
+    rng = np.random.default_rng(t)
+    q, k, v = qkv(rng, t, 4, 2, 64, "bf16", True)
+    inv, pos = pa.rope_frequencies(64, device="cuda"), up(rng.integers(0, 9999, t).astype(np.int32))
+    slots = up(rng.permutation(700)[:t].astype(np.int64))
+    kc, vc = (torch.zeros(44, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc1, vc1 = torch.zeros_like(kc), torch.zeros_like(vc)
+    out = pa.rope_write_kv(q, k, v, kc, vc, inv, pos, slots)
+    one = [pa.rope_write_kv(q[i:i + 100], k[i:i + 100], v[i:i + 100], kc1, vc1, inv, pos[i:i + 100], slots[i:i + 100])
+           for i in range(0, t, 100)]
+    pa.check_error()
+    assert torch.equal(out, torch.cat(one)) and torch.equal(kc, kc1) and torch.equal(vc, vc1)
+
+
+def test_blocks_past_four_gigabytes():
+    """The same requests in the first and in the last blocks of a pool whose K alone is larger than 2^32 bytes."""
+    hq, hkv, d, bs, blocks = 8, 8, 128, 32, 140_000
+    rng = np.random.default_rng(5)
+    old, new = [0, 100], [70, 3]
+    off, lens = up(np.array([0, 70, 73], np.int32)), up(np.array([70, 103], np.int32))
+    q, k, v = qkv(rng, 73, hq, hkv, d, "bf16", True)
+    inv = pa.rope_frequencies(d, device="cuda")
+    low = np.array([[1, 5, 2, -1], [0, 4, 3, 6]], np.int32)
+    seed = torch.randint(0, 0x78, (8, hkv, bs, d), dtype=torch.uint8, device="cuda")
+    results = []
+    for count, tables in ((8, low), (blocks, np.where(low >= 0, low + blocks - 8, -1).astype(np.int32))):
+        kc, vc = (torch.empty(count, hkv, bs, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+        kc[-8:] = seed
+        vc[-8:] = seed.flip(0)
+        ks, vs = (torch.full((count, hkv), x, device="cuda") for x in (0.25, 0.5))
+        turned = pa.rope_append_fp8(q, k, v, kc, vc, ks, vs, inv, up(tables), lens, off)
+        out = pa.attend_fp8(turned, kc, vc, ks, vs, up(tables), lens, off)
+        pos = up(np.concatenate([np.arange(a, a + n) for a, n in zip(old, new)]).astype(np.int32))
+        slots = torch.arange(73, device="cuda") + (count * bs - 73)
+        results.append((turned, out, kc[-8:].clone(), vc[-8:].clone(), ks[-8:].clone(), vs[-8:].clone()))
+        k16, v16 = (torch.zeros(count, 2, bs, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        pa.rope_write_kv(q, k[:, :2], v[:, :2], k16, v16, inv, pos, slots)
+        results[-1] += (k16[-3:].clone(), v16[-3:].clone())
+        del kc, vc, k16, v16
+    pa.check_error()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 def test_two_streams_at_once():
