@@ -1112,6 +1112,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     griddep_wait();
     griddep_launch_dependents();
     constexpr int E = D / 32;
+    using Vec = typename std::conditional<E == 4, float4, float2>::type;
     const long long cost = ws.head->cost, share = share_of(cost, ctas);
     const int c1 = blockIdx.x + 1;  // boundary: the start of CTA c1's share
     const long long x = share * c1;
@@ -1149,16 +1150,20 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
             if (lc != lc) fc = 1.f;
             l = l * f + lc * fc;
             m = mn;
-            const float* src = rec + 2 * kTile + (size_t)rr * D + lane * E;
+            alignas(16) float x[E];
+            *reinterpret_cast<Vec*>(x) = *reinterpret_cast<const Vec*>(rec + 2 * kTile + (size_t)rr * D + lane * E);
 #pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = o[i] * f + src[i] * fc;
+            for (int i = 0; i < E; ++i) o[i] = o[i] * f + x[i] * fc;
         }
         const int v = en.row0 + r, token = v / group;
         T* dst = static_cast<T*>(a.out) +
                  ((size_t)(max(0, a.q_offsets[en.seq]) + token) * a.num_heads + kvh * group + (v - token * group)) * D + lane * E;
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        alignas(8) T y[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) dst[i] = from_float<T>(o[i] * inv);
+        for (int i = 0; i < E; ++i) y[i] = from_float<T>(o[i] * inv);
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
+        else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(y);
     }
 }
 
@@ -1179,8 +1184,8 @@ cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUt
     if (e != cudaSuccess) return e;
     e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, kmap, vmap);
     if (e != cudaSuccess || ctas < 2) return e;
-    // (a boundary's 256 rows on 16 CTAs, two rows a warp: short mixed requests 95 to 90 us against 4 CTAs, 93 with 32)
-    return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 16), dim3(kJoinThreads), 0, stream, a, ws, ctas);
+    // (a boundary's 256 rows on 8 CTAs, four rows a warp: short mixed requests 88.7 us; 4 CTAs 95, 16 89.7, 32 93)
+    return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 8), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
 
 }  // namespace
