@@ -140,7 +140,8 @@ __device__ __forceinline__ void rotate(Chunk<T, VB>& x0, Chunk<T, VB>& x1, const
 
 // Rows of a token: its query heads, key heads, value heads.  A row is ns = head_dim / 2V slots of two chunks; a
 // thread keeps one slot, so its place in a row and its pairs are fixed, and walks over the rows of the CTA's
-// tokens.  The (cos, sin) of a token are computed once per CTA, not once per head.
+// tokens.  The (cos, sin) of a token are computed once per CTA, not once per head.  Rows are moved once, so HBM bounds it
+// for prompts and latency for steps: 8192 tokens of 28 + 2 * 4 heads of 128 (bf16) take 31 us, 4.9 TB/s; 64 tokens 5.2 us.
 template <typename T, int VB, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_write_kv_kernel(const RopeWriteArgs a, int tokens_per_cta) {
     constexpr int V = Chunk<T, VB>::V;
@@ -356,7 +357,7 @@ struct AppendPiece {
 
 // One unit: a piece, one kv head, K or V, by a warp.  Rows are slots of two chunks as in rope_write_kv, RPS rows side by
 // side.  Two passes, since the scale comes before the codes; the second reads the rows again, from L1 or L2, and rotates them
-// again: holding a block between the passes takes 32 to 64 registers more than there are (prompt chunks 70 us instead of 51).
+// again: holding a block between the passes takes 32 to 64 registers more than there are (prompt chunks 70 us instead of 55).
 template <typename T, int D, int BS, int VB>
 __device__ __forceinline__ void append_unit(const RopeAppendArgs& a, const AppendPiece& piece, int h, bool is_value,
                                             const float2* cs_of_first, int lane) {
@@ -419,7 +420,10 @@ __device__ __forceinline__ void append_unit(const RopeAppendArgs& a, const Appen
 
 // CTA (window, part): the query rows of a window of `window` tokens, and the blocks whose first row of this call lies in it.
 // Their positions are found and their angles computed once, in shared memory; warps then take units and groups of query
-// heads in turn, every parts-th CTA's worth of them.
+// heads in turn, every parts-th CTA's worth of them.  Dependent steps bound it (rows, then the scale, then the codes), at two CTAs
+// per SM: 8300 prompt tokens of 28 + 2 * 4 heads of 128 (bf16) take 46 us (3.1 TB/s), 2240 of 3 * 32 heads 54 us (1.7), a decode step
+// of 64 tokens 7.4 us.  80 registers for three CTAs spilled (prompts 64 us); the rows' prefetch into L2 while positions are
+// found gained nothing.
 template <typename T, int D, int BS, int VB>
 __global__ void __launch_bounds__(kAppendThreads, 2) rope_append_fp8_kernel(const RopeAppendArgs a, int window, int parts) {
     constexpr int V = Chunk<T, VB>::V, NS = D / (2 * V), LPR = NS < 32 ? NS : 32, SPL = NS / LPR, RPS = 32 / LPR;
@@ -559,8 +563,9 @@ cudaError_t append_typed(const RopeAppendArgs& a, cudaStream_t stream) {
     const RopeArgs& r = a.r;
     constexpr int V = VB / (int)sizeof(T), NS = D / (2 * V), RPS = NS < 32 ? 32 / NS : 1;
     // A window is a block long, so that a prompt has one block per window; while a window per token does not fill the
-    // GPU, every token has its own, so that the tokens of a decode step do not queue behind one another.  (2300 tokens of 37 requests,
-    // 32 kv heads: 59 us, with a window per token 129; 64 decode tokens: 9.8 us on the GPU, 19.6 with warps that took several.)
+    // GPU, every token has its own, so that the tokens of a decode step do not queue behind one another.  (2240 tokens of 37 requests,
+    // 32 kv heads: 59 us, with a window per token 129; 64 decode tokens: 7.4 us on the GPU,
+    // 19.6 with warps that took several.)
     const int window = r.num_tokens <= 2 * a.num_sms ? 1 : BS;
     const long long windows = (r.num_tokens + window - 1) / window;
     // The rows of a window are shared among parts of CTAs, down to a turn per warp, while that makes at most four CTAs per SM
