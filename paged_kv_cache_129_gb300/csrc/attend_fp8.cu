@@ -18,9 +18,10 @@
 // two near the largest seen, so that P stays in f16 range.  Scores, maxima, sums and the output accumulate in float32;
 // P alone is rounded to f16 (half a step 2^-11, below the half step 2^-9 of a bf16 output).  The maximum that exponents are
 // taken from follows the true one by steps of 2^8 at least: rescaling the output in tensor memory is rare that way.
-// Bound.  Prompt chunks: the chain of scores, softmax, P and output of two row tiles per SM; issue slots are 52 % busy, the tensor
-// pipe 39 % (four requests of 1500 - 2048 new tokens on 2048 - 6144: 623 us, 0.88 PFLOP/s).  Few rows: the same chain per key tile,
-// with a third of the tensor pipe and of HBM busy (eight requests of 32k - 128k tokens: 391 us, 3.2 TB/s).
+// Bound.  Shared memory: a split key tile at D = 128 moves 256 KB through it (codes in and out, widened, query rows for two halves,
+// K, V), 2048 of the 3000 cycles that it takes; a paired one 384 KB.  Prompt chunks (four requests of 1500 - 2048 new tokens on
+// 2048 - 6144) take 622 us, 0.88 PFLOP/s, issue slots 52 % and the tensor pipe 39 % busy; few rows on long contexts (eight
+// requests of 32k - 128k tokens) 391 us, 3.2 TB/s.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
