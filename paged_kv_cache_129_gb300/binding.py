@@ -134,6 +134,8 @@ _SIGNATURES = [
 def library() -> ctypes.CDLL:
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -175,8 +177,11 @@ def _need(cond: bool, what: str) -> None:
 
 
 def _cuda(t: torch.Tensor, name: str) -> None:
-    _need(t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    # (messages are formatted only when needed: these checks are much of a small call's time)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def diag_merge_timeout(out: torch.Tensor, context_lens: torch.Tensor, num_kv_heads: int, block_size: int,

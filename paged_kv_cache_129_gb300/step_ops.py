@@ -28,8 +28,16 @@ class TableStep(NamedTuple):
 
 
 def _one_device(device: torch.device, *tensors) -> None:
+    index = device.index
     for t in tensors:
-        _need(t is None or t.device == device, "all tensors of a call must be on one device")
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors of a call must be on one device")
+
+
+def _int32(t: torch.Tensor, name: str) -> None:
+    _cuda(t, name)
+    if t.dtype is not torch.int32:
+        raise ValueError(f"{name} must be int32")
 
 
 def _fresh(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
@@ -47,7 +55,7 @@ def _launch(fn, device: torch.device, stream, *args) -> None:
     """One library call on ``device``, on ``stream`` or the device's current stream."""
     index = device.index
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_ptr(stream, device)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         _check(fn(*args, raw))
     else:
         with torch.cuda.device(device):
@@ -67,8 +75,7 @@ def advance_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, new_l
     """
     for name, t in (("block_tables", block_tables), ("context_lens", context_lens), ("new_lens", new_lens),
                     ("free_blocks", free_blocks), ("num_free", num_free)):
-        _cuda(t, name)
-        _need(t.dtype == torch.int32, f"{name} must be int32")
+        _int32(t, name)
     _need(block_tables.dim() == 2, "block_tables: int32 [B, max_blocks]")
     b, width = block_tables.shape
     dev = block_tables.device
@@ -84,7 +91,8 @@ def advance_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, new_l
         out = TableStep(*out)
         for t, n, dt in zip(out, (b, 1, b + 1, num_tokens, num_tokens), (torch.int32,) * 4 + (torch.int64,)):
             _cuda(t, "out")
-            _need(t.dtype == dt and t.numel() == n, f"out: {n} elements of {dt}")
+            if t.dtype is not dt or t.numel() != n:
+                raise ValueError(f"out: {n} elements of {dt}")
     _one_device(dev, context_lens, new_lens, free_blocks, num_free, *out)
     _launch(library().pa_advance_tables, dev, stream, block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(),
             free_blocks.data_ptr(), num_free.data_ptr(), *[t.data_ptr() for t in out], b, width, free_blocks.numel(),
@@ -123,19 +131,25 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
 
 def _rows(t: torch.Tensor, name: str, d: int) -> int:
     """Checks [T, heads, d] rows with contiguous heads; returns the stride between tokens."""
-    _need(t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.dim() == 3 and t.shape[2] == d, f"{name} must be [T, heads, {d}]")
-    heads, stride = t.shape[1], t.stride()
-    _need(stride[2] == 1 and (heads == 1 or stride[1] == d), f"{name}: the heads of a token must be contiguous")
-    if t.shape[0] <= 1:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"{name} must be [T, heads, {d}]")
+    tokens, heads, _ = shape
+    if stride[2] != 1 or (heads != 1 and stride[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if tokens <= 1:
         return heads * d
-    _need(stride[0] >= heads * d, f"{name}: tokens must not overlap")
+    if stride[0] < heads * d:
+        raise ValueError(f"{name}: tokens must not overlap")
     return stride[0]
 
 
 def _rope_inputs(query, key, value, inv_freq, layout, query_out, hkv, d, stream):
     """Shared checks of the rotary calls; returns (query_out, token strides, rotary_dim, layout code)."""
-    _need(layout in LAYOUTS, f"layout must be one of {sorted(LAYOUTS)}")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
     strides = _rows(query, "query", d), _rows(key, "key", d), _rows(value, "value", d)
     t = query.shape[0]
     _need(key.shape == (t, hkv, d) and value.shape == key.shape, "key/value must be [T, H_kv, d]")
@@ -184,8 +198,7 @@ def rope_write_kv(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k
 
 def _runs(block_tables, context_lens, q_offsets) -> None:
     for name, t in (("block_tables", block_tables), ("context_lens", context_lens), ("q_offsets", q_offsets)):
-        _cuda(t, name)
-        _need(t.dtype == torch.int32, f"{name} must be int32")
+        _int32(t, name)
     _need(block_tables.dim() == 2, "block_tables: int32 [B, max_blocks]")
     b = block_tables.shape[0]
     _need(context_lens.numel() == b, "context_lens: int32 [B]")
