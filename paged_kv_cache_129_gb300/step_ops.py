@@ -260,8 +260,12 @@ def attend_fp8(query: torch.Tensor, key_cache: torch.Tensor, value_cache: Option
     b, width = block_tables.shape
     code = _dtype_code(query)
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = library().pa_attend_fp8_workspace_size(t, b, hq, hkv, d, bs, width, code)
+        size_of = library().pa_attend_fp8_workspace_size
+        if dev.index == torch._C._cuda_getDevice():
+            need = size_of(t, b, hq, hkv, d, bs, width, code)
+        else:
+            with torch.cuda.device(dev):
+                need = size_of(t, b, hq, hkv, d, bs, width, code)
         workspace = _fresh(max(int(need), 256), torch.uint8, dev, stream)
     _cuda(workspace, "workspace")
     _one_device(dev, query, value_cache, k_scale, v_scale, block_tables, context_lens, q_offsets, out, workspace)
