@@ -547,8 +547,10 @@ int pa_rope_append_fp8(void* query_out, const void* query, const void* key, cons
  * pa_decode_multi.  n_b may be 0, and differ from request to request; a row before position 0 gets
  * zeros; rows behind q_offsets[num_seqs] are left as they were.  Codes, scales and layouts as
  * pa_decode_fp8; query and out f16 or bf16, contiguous, 16-byte aligned.  Scores, softmax and sums
- * are float32.  Compiled for head_dim 64 and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED
- * otherwise).  A block id outside the pool reads as masked positions and sets PA_ERR_BAD_TABLE, a length
+ * are float32; the weights that multiply the codes of V (exponential times V scale) are rounded to
+ * f16, relative to the largest one of the positions that the row sees: off by 2^-11 of themselves, or by
+ * 2^-25 of the largest, whichever is more; exponentials below 2^-110 may count as zero.  Compiled
+ * for head_dim 64 and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED otherwise).  A block id outside the pool reads as masked positions and sets PA_ERR_BAD_TABLE, a length
  * outside its table is clamped and sets PA_ERR_BAD_CONTEXT, in the device error word.
  *  workspace  pa_attend_fp8_workspace_size() bytes, 256-byte aligned, no initialisation; calls that
  *             share one must not overlap on the GPU.

@@ -14,10 +14,12 @@
 // cost, and cut into one equal contiguous share per SM, so every SM works equally long whatever the length mix; units cut by a
 // share boundary leave float32 partial results (two slots per CTA), joined by a third kernel.
 // Numbers.  E4M3 codes widen to f16 exactly; a query row is moved into f16 range by a power of two (f16 queries as they
-// are), undone in the score factor.  A block's K scale multiplies its scores; its V scale multiplies P, relative to a power of
-// two near the largest seen, so that P stays in f16 range.  Scores, maxima, sums and the output accumulate in float32;
-// P alone is rounded to f16 (half a step 2^-11, below the half step 2^-9 of a bf16 output).  The maximum that exponents are
-// taken from follows the true one by steps of 2^8 at least: rescaling the output in tensor memory is rare that way.
+// are), undone in the score factor.  A block's K scale multiplies its scores; its V scale multiplies P, so that V goes into the
+// products as codes.  Scores, maxima, sums and the output accumulate in float32; P alone is rounded to f16, relative to a power of
+// two (vref) near the row's largest exponential times V scale: half a step 2^-11 of a weight (below the half step 2^-9 of a bf16
+// output), and 2^-25 of the largest one for weights below 2^-14 of it.  Only what a row sees counts for that: neither a block behind its
+// position nor one of a negligible weight takes bits from it.  Both references, the maximum that exponents are taken from and vref, follow
+// the true ones by steps of 2^8 at least: rescaling the output in tensor memory is rare that way.
 // Bound.  Shared memory: a split key tile at D = 128 moves 256 KB through it (codes in and out, widened, query rows for two halves,
 // K, V), 2048 of the 3000 cycles that it takes; a paired one 384 KB.  Prompt chunks (four requests of 1500 - 2048 new tokens on
 // 2048 - 6144) take 622 us, 0.88 PFLOP/s, issue slots 52 % and the tensor pipe 39 % busy; few rows on long contexts (eight
@@ -371,7 +373,7 @@ struct Smem {
     unsigned char q[2][kOperand];
     unsigned char kv[kBuffers][kOperand];
     unsigned char raw[kRaw][kTile * D];
-    float ks[kRing][8], vs[kRing][8];                   // scales of the tile's blocks
+    float ks[kRing][8], vs[kRing][8], lv[kRing][8];     // scales of the tile's blocks; the exponent of the V scale
     int rows[kRing][8];                                 // and their rows of the K map (of the V map: the next)
     unsigned present[kRing], masked[kRing];             // blocks of the tile: there; with an id outside the pool
     unsigned nan_any[kNanRing][kWidenWarps];            // whether a warp found NaN in V of a tile that some row sees in part,
@@ -487,6 +489,7 @@ __device__ __forceinline__ void look_ahead(const AttendArgs& a, const Workspace&
             if (lane < 8) {
                 sm.ks[slot][lane] = ks;
                 sm.vs[slot][lane] = vs;
+                sm.lv[slot][lane] = (float)((int)(__float_as_uint(vs) >> 23) - 127);  // (of zero and subnormal ones -127)
                 sm.rows[slot][lane] = both ? 2 * record : record;
             }
             if (lane == 0) {
@@ -774,10 +777,11 @@ __device__ __forceinline__ void mask_scores(uint32_t (&s)[64], int cols, unsigne
         if (i >= cols || (masked >> (i / BS) & 1)) s[i] = 0xff800000u;
 }
 
-// Largest of 64 scores, times the factors of their blocks.
+// Largest of 64 scores, times the factors of their blocks; weight: the largest sum of such a score and its block's lv.
 template <int BS>
-__device__ __forceinline__ float row_max(const uint32_t (&s)[64], const float (&kf)[64 / BS]) {
+__device__ __forceinline__ float row_max(const uint32_t (&s)[64], const float (&kf)[64 / BS], const float (&lv)[64 / BS], float& weight) {
     float top = -INFINITY;
+    weight = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 64 / BS; ++h) {
         float x = -INFINITY, y = -INFINITY;  // two chains
@@ -786,15 +790,17 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[64], const float (&
             x = fmaxf(x, fmaxf(__uint_as_float(s[BS * h + k]), __uint_as_float(s[BS * h + k + 1])));
             y = fmaxf(y, fmaxf(__uint_as_float(s[BS * h + k + 2]), __uint_as_float(s[BS * h + k + 3])));
         }
-        top = fmaxf(top, fmaxf(x, y) * kf[h]);
+        const float most = fmaxf(x, y) * kf[h];
+        top = fmaxf(top, most);
+        weight = fmaxf(weight, most + lv[h]);
     }
     return top;
 }
 
-// P of 64 scores: exp2(score - mu) times the block's V scale, as f16, over the scores in tensor memory; returns the sum of the
+// P of 64 scores: exp2(score - mu) times its block's factor vf, as f16, over the scores in tensor memory; returns the sum of the
 // exponentials.
 template <int BS>
-__device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, const float (&kf)[64 / BS], const float* vs, float vinv, float mu) {
+__device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, const float (&kf)[64 / BS], const float (&vf)[64 / BS], float mu) {
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < 64; c += 32) {
@@ -805,14 +811,28 @@ __device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, const
                                   make_float2(-mu, -mu));
             const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
             sum = add2(sum, e);
-            const float vf = vs[h] * vinv;
-            const float2 w = mul2(e, make_float2(vf, vf));
+            const float2 w = mul2(e, make_float2(vf[h], vf[h]));
             const __half2 p = __floats2half2_rn(w.x, w.y);
             s[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
         }
         tmem_st16(s_at + c / 2, *reinterpret_cast<uint32_t(*)[16]>(&s[c / 2]));
     }
     return sum.x + sum.y;
+}
+
+// What the side ring holds of a half's blocks.
+template <int N>
+__device__ __forceinline__ void load_blocks(float (&x)[N], const float* from) {
+    static_assert(N == 4 || N == 2, "blocks of 16 or 32 tokens");
+    if constexpr (N == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from);
+    else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(from);
+}
+__device__ __forceinline__ float inverse(float p) { return __int_as_float(0x7f000000 - __float_as_int(p)); }  // of 2^-126 .. 2^126
+__device__ __forceinline__ float power_of_two(float e) { return __int_as_float(((int)e + 127) << 23); }  // |e| <= 126, whole
+// log2 of the power of two that P is relative to, from the references of weights and of exponents: P of the former's weight is in [1, 4).
+__device__ __forceinline__ float reference(float weight, float m) {
+    const float e = floorf(weight - m);
+    return e == e ? fminf(fmaxf(e, -126.f), 126.f) : 0.f;  // (nothing seen yet, or an infinite score)
 }
 
 // A softmax warp: 32 rows of a stream's row tile, one per lane.
@@ -831,7 +851,8 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
         float* rec;
         bool live, warp_live, cut, join;
     } res{};
-    float m = -INFINITY, l = 0.f, vref = 0.f;
+    // the row's references of exponents and of weights; the sum of its exponentials; 1 / the power of two that P is relative to
+    float m = -INFINITY, w = -INFINITY, l = 0.f, vinv = 1.f;
     bool has_nan = false, pending = false;
 #pragma unroll 1
     for (;;) {
@@ -873,6 +894,7 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
             if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
             tc_fence_after();
             ++pieces;
+            const float vref = inverse(vinv);
             float f0 = vref, f1 = 0.f;  // factors of this stream's output and of the other's
             uint32_t nan_from = has_nan ? 1u << t : 0u;
             if (res.join) {  // both streams have a part of the same rows, in the same lanes of tensor memory
@@ -951,8 +973,8 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
 
         res = now;
         pending = true;
-        m = -INFINITY;
-        l = vref = 0.f;
+        m = w = -INFINITY;
+        l = 0.f;
         has_nan = false;
 #pragma unroll 1
         for (int step = 0; step < my_jobs; ++step, ++steps) {
@@ -971,38 +993,38 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                 uint32_t s[64];
                 tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                 tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                const float* vs = sm.vs[slot] + half * (64 / BS);
+                alignas(16) float ks[64 / BS], vs[64 / BS], lv[64 / BS];
+                load_blocks(ks, sm.ks[slot] + half * (64 / BS));
+                load_blocks(lv, sm.lv[slot] + half * (64 / BS));
                 // factors of the scores; kept above zero, so that masked scores stay -inf
                 float kf[64 / BS];
-                float vmax = 0.f;
 #pragma unroll
-                for (int k = 0; k < 64 / BS; ++k) {
-                    kf[k] = fmaxf(sm.ks[slot][half * (64 / BS) + k] * qf, 1e-38f);
-                    vmax = fmaxf(vmax, vs[k]);
-                }
+                for (int k = 0; k < 64 / BS; ++k) kf[k] = fmaxf(ks[k] * qf, 1e-38f);
                 const unsigned masked = sm.masked[slot] >> (half * (64 / BS));
                 const int cols = bound - p0 - 64 * half + 1;  // columns that the row sees, if below 64
                 const bool whole = __all_sync(0xffffffffu, !now.live || cols >= 64) && (masked & ((1u << (64 / BS)) - 1)) == 0;
                 tc_wait_ld(s);
                 if (!whole) mask_scores<BS>(s, cols, masked);
-                const float top = row_max<BS>(s, kf);
-                // the power of two that P's V scales are relative to
-                const float vnew = fmaxf(vref, __int_as_float(__float_as_int(fmaxf(vmax, 7.888609052210118e-31f)) & 0x7f800000));
+                float weight;  // log2 of the row's largest exponential times V scale, less what the scale has past its power of two
+                const float top = row_max<BS>(s, kf, lv, weight);
                 if (step == 0 && half == 0) {
                     m = top;
-                    vref = vnew;
-                } else if (__any_sync(0xffffffffu, vnew > vref || top > m + 8.f)) {
+                    w = weight;
+                    vinv = power_of_two(-reference(w, m));
+                } else if (__any_sync(0xffffffffu, top > m + 8.f || weight > w + 8.f)) {
                     // The output so far has to be there.  (Its barrier is waited for only here: the phase before the one that is
                     // meant is over, because this half's scores were issued after the output of the half before the last.)
                     const unsigned last = half ? steps : steps - 1;
                     if (!warp_wait(&sm.pv_done[t][half ^ 1], last & 1, a.err, abort)) return;
                     tc_fence_after();
-                    const float mn = fmaxf(m, top);
+                    const float mn = fmaxf(m, top), wn = fmaxf(w, weight), vn = -reference(wn, mn);
                     const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-                    const float of = f * (vref / vnew);
+                    // (one power: the two that it is made of may be past float32's ends where it is not)
+                    const float of = mn == -INFINITY ? 1.f : exp2_approx(m - mn + (vn + reference(w, m)));
                     l *= f;
                     m = mn;
-                    vref = vnew;
+                    w = wn;
+                    vinv = power_of_two(vn);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
@@ -1013,8 +1035,13 @@ __device__ __forceinline__ void softmax_rows(const AttendArgs& a, const Workspac
                         tmem_st16(o_at + c, o);
                     }
                 }
-                const float vinv = __int_as_float(0x7f000000 - __float_as_int(vref));  // 1 / vref, a power of two
-                l += row_exp<BS>(s, at, kf, vs, vinv, m == -INFINITY ? 0.f : m);
+                // Factors of P.  (One past float32's end is that of a block that the row does not see, or of one whose exponentials are below
+                // 2^-110: kept finite, it leaves their zeros zeros.)
+                load_blocks(vs, sm.vs[slot] + half * (64 / BS));
+                float vf[64 / BS];
+#pragma unroll
+                for (int k = 0; k < 64 / BS; ++k) vf[k] = fminf(vs[k] * vinv, 1e38f);
+                l += row_exp<BS>(s, at, kf, vf, m == -INFINITY ? 0.f : m);
                 if (half == 1 && p0 + kTile - 1 > seen_by_all) {  // a tile whose V was searched for NaN
                     const unsigned f = 2 * tiles_before + value_fill(p.paired, n, local);
                     if (!warp_wait(&sm.kv_full[f % kBuffers], (f / kBuffers) & 1, a.err, abort)) return;
