@@ -497,7 +497,8 @@ int pa_advance_tables(int32_t* block_tables, const int32_t* context_lens, const 
  * (2i, 2i + 1) (PA_ROPE_INTERLEAVED), is turned by p * inv_freq[i]:
  *     (x, y) -> factor * (x cos - y sin, x sin + y cos);
  * elements at and past rotary_dim pass unchanged.  float32 arithmetic, one rounding to dtype; the
- * angle is exact to 2^-32 turns for every position (inv_freq: device float64 [rotary_dim / 2]).
+ * angle is off by at most 2^-28 turns, for every position (inv_freq: device float64 [rotary_dim / 2], below
+ * 2^30 in magnitude; cosine and sine of it are float32's).
  *  query      [num_tokens, num_heads, head_dim], key and value [num_tokens, num_kv_heads, head_dim]:
  *             heads of a token contiguous, q_stride, k_stride and v_stride elements from token to
  *             token (the views that a joint projection leaves).

@@ -5,8 +5,9 @@
 // are formed in float32 and rounded once to the stored type.
 //
 // Angles of far positions: p * inv_freq in float32 is off by p * 2^-24 radians, useless at p = 10^6.  A turn is
-// therefore a 64-bit fixed-point fraction: u = frac(inv_freq / 2 pi) * 2^64, and p * u modulo 2^64 is the angle
-// in turns without whole ones, exactly.  Its distance from the nearest quarter turn, at most an eighth, goes to sincospi in
+// therefore a 64-bit fixed-point fraction: u = frac(inv_freq / 2 pi) * 2^64, rounded to half a unit (a double alone would be off
+// by 2^-54 of the quotient, 2^-25 turns at p = 2^31), and p * u modulo 2^64 is the angle in turns without whole ones, off by
+// p * 2^-65.  Its distance from the nearest quarter turn, at most an eighth, goes to sincospi in
 // float32, off by 2^-28 turns at most, and the quarters swap and negate (the whole angle in float32 would be off by 2^-26: rotated
 // float32 rows 4.0e-8 from the exact ones instead of 2.8e-8).  One integer product per angle.
 #include <algorithm>
@@ -22,10 +23,15 @@ namespace pa {
 
 namespace {
 
+// u of an angle per position (of magnitude below 2^30).  1 / 2 pi is the sum of two doubles, and an fma gives what the first's product
+// was rounded by.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
-    double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-    t -= floor(t);
-    return __double2ull_rz(t * 18446744073709551616.0);  // * 2^64; a double below 1 stays below 2^64
+    const double x = fabs(inv_freq), high = x * 0.15915494309189535;
+    const double low = fma(x, -9.839338337591243e-18, fma(x, 0.15915494309189535, -high));
+    const double units = (high - floor(high)) * 18446744073709551616.0;  // * 2^64, below it
+    const double whole = floor(units);
+    const uint64_t u = __double2ull_rz(whole) + (uint64_t)__double2ll_rn(fma(low, 18446744073709551616.0, units - whole));
+    return inv_freq < 0.0 ? 0 - u : u;
 }
 
 __device__ __forceinline__ float2 turn(uint64_t step, int pos, float factor) {
@@ -140,24 +146,26 @@ __device__ __forceinline__ void rotate(Chunk<T, VB>& x0, Chunk<T, VB>& x1, const
 
 // Rows of a token: its query heads, key heads, value heads.  A row is ns = head_dim / 2V slots of two chunks; a
 // thread keeps one slot, so its place in a row and its pairs are fixed, and walks over the rows of the CTA's
-// tokens.  The (cos, sin) of a token are computed once per CTA, not once per head.  Rows are moved once, so HBM bounds it
-// for prompts and latency for steps: 8192 tokens of 28 + 2 * 4 heads of 128 (bf16) take 31 us, 4.9 TB/s; 64 tokens 5.2 us.
+// tokens.  The (cos, sin) of a token are computed once per CTA, not once per head, and the steps of the pairs, in float64, once for
+// its tokens.  Rows are moved once, so HBM bounds it for prompts and latency for steps: 8192 tokens of 28 + 2 * 4 heads of 128 (bf16)
+// take 30 us, 5.0 TB/s (31 with a step per token and pair); 64 tokens 5.2 us.
 template <typename T, int VB, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_write_kv_kernel(const RopeWriteArgs a, int tokens_per_cta) {
     constexpr int V = Chunk<T, VB>::V;
-    extern __shared__ float2 cs[];  // [tokens][rotary_dim / 2]
+    extern __shared__ float2 cs[];  // [tokens][rotary_dim / 2], then the pairs' steps
     __shared__ long long dest[kRopeTokens];
     griddep_wait();
     griddep_launch_dependents();
     const RopeArgs& r = a.r;
     const int half = r.rotary_dim / 2, tid = threadIdx.x;
-    const int tok0 = blockIdx.x * tokens_per_cta, ntok = min(tokens_per_cta, r.num_tokens - tok0);
-    for (int i = tid; i < ntok * half; i += kRopeThreads) {
-        const int t = i / half;
-        cs[i] = turn(turn_step(r.inv_freq[i - t * half]), a.positions[tok0 + t], r.factor);
-    }
-    if (tid < ntok) {
-        const long long slot = a.slot_mapping[tok0 + tid];
+    uint64_t* steps = reinterpret_cast<uint64_t*>(cs + tokens_per_cta * half);
+    const int tok0 = blockIdx.x * tokens_per_cta, ntok = min(tokens_per_cta, r.num_tokens - tok0), pairs = ntok * half;
+    // (loads that do not wait for one another, before the steps; destinations by threads that have no steps, where there are some)
+    const int pos0 = tid < pairs ? a.positions[tok0 + tid / half] : 0;
+    const int own = kRopeThreads - 1 - tid;
+    const long long slot = own < ntok ? a.slot_mapping[tok0 + own] : -1;
+    for (int i = tid; i < half; i += kRopeThreads) steps[i] = turn_step(r.inv_freq[i]);
+    if (own < ntok) {
         long long d = -1;  // in rows of the cache, without the head
         if (slot >= (long long)r.num_blocks * r.block_size) {
             atomicOr(r.err, kErrBadSlot);
@@ -165,7 +173,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kv_kernel(const RopeW
             const long long blk = slot / r.block_size;
             d = blk * r.num_kv_heads * r.block_size + (slot - blk * r.block_size);
         }
-        dest[tid] = d;
+        dest[own] = d;
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += kRopeThreads) {
+        const int t = i / half;
+        cs[i] = turn(steps[i - t * half], i == tid ? pos0 : a.positions[tok0 + t], r.factor);
     }
     __syncthreads();
     const int ns = r.head_dim / (2 * V), groups = kRopeThreads / ns;
@@ -541,7 +554,7 @@ cudaError_t rope_write_typed(const RopeWriteArgs& a, cudaStream_t stream) {
     // CTA per token 42; 1001 tokens, f32: 5.3, 7.4; 64 tokens: 8.0, 5.4.)
     const int per = a.r.num_tokens >= kRopeTokens * a.num_sms ? kRopeTokens : 1;
     const unsigned grid = (unsigned)((a.r.num_tokens + per - 1) / per);
-    const size_t smem = (size_t)per * (a.r.rotary_dim / 2) * sizeof(float2);
+    const size_t smem = (size_t)(per + 1) * (a.r.rotary_dim / 2) * sizeof(float2);  // (steps are as large as a token's pairs)
     if (a.r.interleaved)
         return launch_pdl(rope_write_kv_kernel<T, VB, true>, dim3(grid), dim3(kRopeThreads), smem, stream, a, per);
     return launch_pdl(rope_write_kv_kernel<T, VB, false>, dim3(grid), dim3(kRopeThreads), smem, stream, a, per);
