@@ -526,8 +526,9 @@ int pa_rope_write_kv(void* query_out, const void* query, const void* key, const 
  *  - the new rows are stored as e4m3(x / scale): round to nearest even, magnitudes above 448
  *    (infinities) saturating, NaN staying NaN.
  * k_scale, v_scale and value_cache as pa_decode_fp8 (NULL value_cache: K and V records).  Rows
- * behind q_offsets[num_seqs] are neither read nor written.  A block that takes new rows must belong
- * to one request.  dtype PA_F32, PA_F16 or PA_BF16; rotary_dim 0: no rotation (inv_freq may be
+ * behind q_offsets[num_seqs] are neither read nor written.  q_offsets ascends from 0 or more to at most
+ * num_tokens; offsets that do not set PA_ERR_BAD_CONTEXT, and rows of theirs may be skipped.  A block that
+ * takes new rows must belong to one request.  dtype PA_F32, PA_F16 or PA_BF16; rotary_dim 0: no rotation (inv_freq may be
  * NULL).  Compiled for head_dim 64 and 128, block_size 16 and 32, rotary_dim a multiple of 4
  * (PA_ERR_UNSUPPORTED otherwise).  A block id outside the pool skips its rows and sets
  * PA_ERR_BAD_TABLE, a length outside its table or below its new rows those of the request and sets
@@ -544,7 +545,7 @@ int pa_rope_append_fp8(void* query_out, const void* query, const void* key, cons
  * pa_attend_fp8 — causal attention of ragged runs of new tokens over an FP8 cache: prompt chunks,
  * verification and decode steps in one call.  Request b has n_b = q_offsets[b + 1] - q_offsets[b]
  * rows of query [num_tokens, num_heads, head_dim], the last n_b of its context_lens[b] positions
- * (their K and V are in the cache already); the row at position p attends positions 0 .. p, as
+ * (their K and V are in the cache already; q_offsets as for pa_rope_append_fp8); the row at position p attends positions 0 .. p, as
  * pa_decode_multi.  n_b may be 0, and differ from request to request; a row before position 0 gets
  * zeros; rows behind q_offsets[num_seqs] are left as they were.  Codes, scales and layouts as
  * pa_decode_fp8; query and out f16 or bf16, contiguous, 16-byte aligned.  Scores, softmax and sums

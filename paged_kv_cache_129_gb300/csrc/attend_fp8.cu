@@ -191,9 +191,9 @@ constexpr uint32_t idesc_of(int n, bool b_n_major) {
 __device__ __forceinline__ int clamped_length(const AttendArgs& a, int b) {
     return max(0, min(a.context_lens[b], a.max_blocks * a.block_size));
 }
-__device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {  // request b's new tokens
-    const int lo = max(0, a.q_offsets[b]), hi = min(a.num_tokens, a.q_offsets[b + 1]);
-    return max(0, hi - lo);
+__device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {  // request b's new tokens; none if its offsets are no run
+    const int lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
+    return is_run(lo, hi, a.num_tokens) ? hi - lo : 0;
 }
 
 // Key tiles of rows row0 .. row0 + 255 of a request: up to the last row's position.
@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendA
         long long n = 0;
         if (b < a.num_seqs) {
             const int L = a.context_lens[b];
-            if (L < 0 || L > a.max_blocks * a.block_size) atomicOr(a.err, kErrBadContext);
+            if (L < 0 || L > a.max_blocks * a.block_size || !is_run(a.q_offsets[b], a.q_offsets[b + 1], a.num_tokens))
+                atomicOr(a.err, kErrBadContext);
             n = ((long long)rows_of(a, b) * group + 2 * kTile - 1) / (2 * kTile);
         }
         const long long at = base + block_scan(n, scratch, &total);
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendA
         base += total;
     }
     int entries = (int)min(base, (long long)entry_cap);
-    if (base > entry_cap) {  // offsets that do not ascend
+    if (base > entry_cap) {  // runs that overlap
         if (tid == 0) atomicOr(a.err, kErrBadContext);
         entries = 0;
     }
@@ -430,7 +431,7 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, const Piece& p) {
     it.n = rows_of(a, p.seq);
     it.group = a.num_heads / a.num_kv_heads;
     it.rows = it.n * it.group;
-    it.first_token = max(0, a.q_offsets[p.seq]);
+    it.first_token = a.q_offsets[p.seq];
     it.jobs = (p.end - p.begin) * (p.paired ? 2 : 1);
     return it;
 }
@@ -1188,7 +1189,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
         }
         const int v = en.row0 + r, token = v / group;
         T* dst = static_cast<T*>(a.out) +
-                 ((size_t)(max(0, a.q_offsets[en.seq]) + token) * a.num_heads + kvh * group + (v - token * group)) * D + lane * E;
+                 ((size_t)(a.q_offsets[en.seq] + token) * a.num_heads + kvh * group + (v - token * group)) * D + lane * E;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         alignas(8) T y[E];
 #pragma unroll

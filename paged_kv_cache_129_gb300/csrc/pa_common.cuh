@@ -167,6 +167,11 @@ __device__ __forceinline__ unsigned long long ld_acquire_gpu(const unsigned long
     return v;
 }
 
+// Whether [first, next) can be the rows of a request among num_tokens.
+__device__ __forceinline__ bool is_run(int first, int next, int num_tokens) {
+    return first >= 0 && first <= next && next <= num_tokens;
+}
+
 // ---- programmatic dependent launch ---------------------------------------------------------
 // Every kernel of the library is launched with programmatic stream serialisation, so
 // that its CTAs can become resident while the previous grid in the stream drains.  Each

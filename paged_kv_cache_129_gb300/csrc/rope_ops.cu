@@ -462,18 +462,22 @@ __global__ void __launch_bounds__(kAppendThreads, 2) rope_append_fp8_kernel(cons
             if (a.q_offsets[mid] <= t) lo = mid;
             else hi = mid;
         }
-        const bool in = lane < tokens && lo >= 0 && lo < B;
-        bool own = false;
-        int pos = 0, n = 0, off = 0, blk = 0;
+        bool in = lane < tokens && lo >= 0 && lo < B, own = false;
+        int pos = 0, n = 0, off = 0, blk = 0, first = 0, next = 0;
+        if (in) {  // (where offsets do not ascend, the search may end anywhere: CTA 0 reports them)
+            first = a.q_offsets[lo];
+            next = a.q_offsets[lo + 1];
+            in = first >= 0 && first <= t && t < next && next <= r.num_tokens;
+        }
         if (in) {
-            const int first = a.q_offsets[lo], next = a.q_offsets[lo + 1], L = a.context_lens[lo];
+            const int L = a.context_lens[lo];
             const long long start = (long long)L - ((long long)next - first);  // position of its first row
             pos = (int)(start + (t - first));
             if (start < 0 || L > (long long)a.max_blocks * BS) {
                 if (t == first && part == 0) atomicOr(r.err, kErrBadContext);
             } else {
                 off = pos % BS;
-                n = min(BS - off, min(next, r.num_tokens) - t);
+                n = min(BS - off, next - t);
                 own = n > 0 && (t == first || off == 0);
                 if (own) blk = a.block_tables[(size_t)lo * a.max_blocks + pos / BS];
                 if (own && (blk < 0 || blk >= r.num_blocks)) {
@@ -496,6 +500,11 @@ __global__ void __launch_bounds__(kAppendThreads, 2) rope_append_fp8_kernel(cons
         }
     } else {
         for (int i = tid - 32; i < half; i += kAppendThreads - 32) steps[i] = turn_step(r.inv_freq[i]);
+        if (blockIdx.x == 0) {
+            bool bad = false;
+            for (int b = tid - 32; b < B; b += kAppendThreads - 32) bad |= !is_run(a.q_offsets[b], a.q_offsets[b + 1], r.num_tokens);
+            if (bad) atomicOr(r.err, kErrBadContext);
+        }
     }
     __syncthreads();
     for (int i = tid; i < num_positions * half; i += kAppendThreads) {
