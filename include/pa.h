@@ -482,9 +482,11 @@ int pa_stepper_wait(pa_stepper* st, int step);
  * count may have been written), and the device error word says why: PA_ERR_POOL_EXHAUSTED;
  * PA_ERR_BAD_CONTEXT (a negative length, one past max_blocks_per_seq * block_size, more than
  * num_tokens new tokens); PA_ERR_BAD_TABLE (an id outside [0, num_blocks) in a table or on the
- * stack, a count outside it).  num_seqs <= PA_MAX_STEP_SEQS.
+ * stack, a count outside it).  num_seqs <= PA_MAX_STEP_SEQS; num_tokens and num_blocks <=
+ * PA_MAX_STEP_ROWS (so is num_tokens of the rotary calls).
  */
 #define PA_MAX_STEP_SEQS 8192
+#define PA_MAX_STEP_ROWS 0x7fff0000
 int pa_advance_tables(int32_t* block_tables, const int32_t* context_lens, const int32_t* new_lens, int32_t* free_blocks,
                       const int32_t* num_free, int32_t* context_lens_out, int32_t* num_free_out, int32_t* q_offsets,
                       int32_t* positions, int64_t* slot_mapping, int num_seqs, int max_blocks_per_seq, int num_blocks,

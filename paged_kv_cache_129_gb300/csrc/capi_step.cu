@@ -41,6 +41,7 @@ int rope_args(const char* fn, RopeArgs* r, void* query_out, const void* query, c
     if (dtype != PA_F32 && dtype != PA_F16 && dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
     if (num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0)
         return fail(PA_ERR_INVALID_ARG, "%s: bad sizes", fn);
+    if (num_tokens > kMaxStepRows) return fail(PA_ERR_INVALID_ARG, "%s: num_tokens=%d > %d", fn, num_tokens, kMaxStepRows);
     if (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED)
         return fail(PA_ERR_INVALID_ARG, "%s: unknown layout %d", fn, layout);
     if (!std::isfinite(factor)) return fail(PA_ERR_INVALID_ARG, "%s: factor is not finite", fn);
@@ -88,7 +89,7 @@ int rope_args(const char* fn, RopeArgs* r, void* query_out, const void* query, c
 
 extern "C" {
 
-static_assert(PA_MAX_STEP_SEQS == kMaxStepSeqs, "the header's limit is the kernel's");
+static_assert(PA_MAX_STEP_SEQS == kMaxStepSeqs && PA_MAX_STEP_ROWS == kMaxStepRows, "the header's limits are the kernels'");
 
 int pa_advance_tables(int32_t* block_tables, const int32_t* context_lens, const int32_t* new_lens, int32_t* free_blocks,
                       const int32_t* num_free, int32_t* context_lens_out, int32_t* num_free_out, int32_t* q_offsets,
@@ -100,6 +101,8 @@ int pa_advance_tables(int32_t* block_tables, const int32_t* context_lens, const 
         return fail(PA_ERR_INVALID_ARG, "pa_advance_tables: num_seqs=%d outside [0, %d]", num_seqs, kMaxStepSeqs);
     if (max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0 || num_tokens < 0)
         return fail(PA_ERR_INVALID_ARG, "pa_advance_tables: bad sizes");
+    if (num_tokens > kMaxStepRows || num_blocks > kMaxStepRows)
+        return fail(PA_ERR_INVALID_ARG, "pa_advance_tables: num_tokens=%d or num_blocks=%d > %d", num_tokens, num_blocks, kMaxStepRows);
     if (!fits_int((long long)max_blocks_per_seq * block_size))
         return fail(PA_ERR_INVALID_ARG, "pa_advance_tables: max_blocks_per_seq * block_size must be < 2^31");
     if (!num_free || !num_free_out || !q_offsets || !free_blocks || (num_tokens > 0 && (!positions || !slot_mapping)) ||

@@ -10,6 +10,7 @@
 namespace pa {
 
 constexpr int kMaxStepSeqs = 8192;  // requests of one call
+constexpr int kMaxStepRows = 0x7fff0000;  // tokens or blocks of one call: int counters go past them by a grid's step
 
 struct AdvanceArgs {
     int32_t* block_tables;        // [num_seqs, max_blocks], new entries written

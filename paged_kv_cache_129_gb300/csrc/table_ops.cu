@@ -24,7 +24,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTableThreads = 1024;
+constexpr int kTableThreads = 1024, kTableCtas = 8;
+static_assert((long long)kMaxStepRows + kTableCtas * kTableThreads < (1ll << 31), "int counters pass the end by one step");
 
 struct Sums {
     long long tok, need, give;
@@ -218,7 +219,7 @@ cudaError_t advance_tables_launch(const AdvanceArgs& a, cudaStream_t stream) {
                                          (int)((4 * kMaxStepSeqs + 3) * sizeof(int)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const unsigned ctas = 8;
+    const unsigned ctas = kTableCtas;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTableThreads);
     cfg.dynamicSmemBytes = smem;
