@@ -457,12 +457,15 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7
 // across the ends of pieces, so that the tables' and scales' latencies are not waited for.  (It also prefetched the codes into L2 at
 // first, line by line: 144 / 676 / 439 us on verification, chunks, long contexts with, 134 / 656 / 412 without; the raw ring's
 // 48 KB in flight per SM cover HBM's latency.)
-// Side data of tile i sits in slot i % 16, which was tile i - 16's.  When K of tile j is copied, the raw slot that it takes was widened,
-// so the f16 buffer three fills before that one was free: scores of tile j - 3 at least are done, so the softmax of tile j - 5.
-// Tile i is looked at once K of tile i - 10 is copied.
+// Side data of tile i sits in slot i % kRing, which was tile i - kRing's.  When K of tile j is copied, at least 2j - 1 fills went before
+// (see fill_of()).  The raw slot that it takes was widened: fill 2j - 1 - kRaw; so the f16 buffer that this one went to was released by
+// the products of fill 2j - 1 - kRaw - kBuffers and all before it.  V of tile g is fill 2g + 2 at most: with 2g <= 2j - 3 - kRaw - kBuffers,
+// the outputs of tile g are issued, so its softmax, the last to look at its side data, is done.  Tile i is looked at once K of tile
+// i - kAhead is copied, so g = i - kRing has to satisfy that for j = i - kAhead.
 template <int D, int BS>
 __device__ __forceinline__ void look_ahead(const AttendArgs& a, const Workspace& ws, Smem<D>& sm) {
     constexpr int BLOCKS = kTile / BS;
+    static_assert(2 * (kRing - kAhead) >= Smem<D>::kRaw + kBuffers + 3, "a slot's tile is done with when it is written again");
     const int lane = threadIdx.x & 31;
     const bool both = a.value_cache == nullptr;
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
