@@ -523,7 +523,7 @@ int pa_rope_write_kv(void* query_out, const void* query, const void* key, const 
  * into, K and V each on their own, with a = the largest finite magnitude among those rows (K after
  * its rotation, in float32):
  *  - the block's offset 0 is among them: scale = max(a / 448, 2^-100);
- *  - else scale = max(held scale, a / 448); if that is larger, the codes before the new rows are
+ *  - else scale = max(held scale, a / 448, 2^-100); if that is larger, the codes before the new rows are
  *    brought to it: e4m3(code * held / scale);
  *  - the new rows are stored as e4m3(x / scale): round to nearest even, magnitudes above 448
  *    (infinities) saturating, NaN staying NaN.
@@ -547,15 +547,17 @@ int pa_rope_append_fp8(void* query_out, const void* query, const void* key, cons
  * pa_attend_fp8 — causal attention of ragged runs of new tokens over an FP8 cache: prompt chunks,
  * verification and decode steps in one call.  Request b has n_b = q_offsets[b + 1] - q_offsets[b]
  * rows of query [num_tokens, num_heads, head_dim], the last n_b of its context_lens[b] positions
- * (their K and V are in the cache already; q_offsets as for pa_rope_append_fp8); the row at position p attends positions 0 .. p, as
- * pa_decode_multi.  n_b may be 0, and differ from request to request; a row before position 0 gets
- * zeros; rows behind q_offsets[num_seqs] are left as they were.  Codes, scales and layouts as
+ * (their K and V are in the cache already; q_offsets as for pa_rope_append_fp8); the row at position
+ * p attends positions 0 .. p, as pa_decode_multi.  n_b may be 0, and differ from request to request;
+ * a row before position 0 gets zeros; rows behind q_offsets[num_seqs] are left as they were.  Codes, scales and layouts as
  * pa_decode_fp8; query and out f16 or bf16, contiguous, 16-byte aligned.  Scores, softmax and sums
  * are float32; the weights that multiply the codes of V (exponential times V scale) are rounded to
  * f16, relative to the largest one of the positions that the row sees: off by 2^-11 of themselves, or by
  * 2^-25 of the largest, whichever is more; exponentials below 2^-110 may count as zero.  Compiled
- * for head_dim 64 and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED otherwise).  A block id outside the pool reads as masked positions and sets PA_ERR_BAD_TABLE, a length
- * outside its table is clamped and sets PA_ERR_BAD_CONTEXT, in the device error word.
+ * for head_dim 64 and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED otherwise).  A block id outside
+ * the pool reads as masked positions and sets PA_ERR_BAD_TABLE, a length outside its table is clamped
+ * and sets PA_ERR_BAD_CONTEXT, in the device error word.  A request's rows of a kv head are worked on 128
+ * at a time: for steps of one token per request alone, pa_decode_fp8 takes less than half the time.
  *  workspace  pa_attend_fp8_workspace_size() bytes, 256-byte aligned, no initialisation; calls that
  *             share one must not overlap on the GPU.
  */

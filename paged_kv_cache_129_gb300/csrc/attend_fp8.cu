@@ -22,8 +22,9 @@
 // the true ones by steps of 2^8 at least: rescaling the output in tensor memory is rare that way.
 // Bound.  Shared memory: a split key tile at D = 128 moves 256 KB through it (codes in and out, widened, query rows for two halves,
 // K, V), 2048 of the 3000 cycles that it takes; a paired one 384 KB.  Prompt chunks (four requests of 1500 - 2048 new tokens on
-// 2048 - 6144) take 622 us, 0.88 PFLOP/s, issue slots 52 % and the tensor pipe 39 % busy; few rows on long contexts (eight
-// requests of 32k - 128k tokens) 391 us, 3.2 TB/s.
+// 2048 - 6144) take 616 us, 0.90 PFLOP/s, issue slots 51 % and the tensor pipe 39 % busy; few rows on long contexts (eight
+// requests of 32k - 128k tokens) 394 us, 3.15 TB/s.  That bound is the 128-row tile's: few rows pay for all of it.  64 requests of four
+// tokens take 117 us, pa_decode_multi over a 16-bit cache, twice the bytes, 68; of one token 108 us, pa_decode_fp8 46.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -48,7 +49,7 @@ constexpr int kRing = 16;              // slots of per-tile side data (block ids
 constexpr int kAhead = kRing - 6;      // key tiles that look_ahead() may be ahead of the copies
 constexpr int kNanRing = 2;            // V of tile i is widened once the scores of tile i (i - 1) are done: the softmax of i - 2 too
 // Cost of work in shares: of a key tile of a pair, of a split tile (half the products and exponentials, but the same loads and
-// widening), and of a unit besides its tiles (queries staged, streams joined, output written: about six split tiles).  Measured
+// widening), and of a unit besides its tiles (queries staged, streams joined, output written: about six split tiles).  Measured when chosen
 // (verification / prompt chunks / long contexts / short mixed D = 64, us): 6, 4, 24: 115 / 625 / 387 / 95; 4, 3, 8: 135 / 656 / 412 /
 // 98.  With prefetches as in look_ahead()'s note, 4, 3, 0 (no cost of a unit) took 175 / 694 / 430 / 125, 4, 3, 8 143 / 675 / 439 / 99.
 constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 24;
@@ -1219,7 +1220,7 @@ cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUt
     if (e != cudaSuccess) return e;
     e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, kmap, vmap);
     if (e != cudaSuccess || ctas < 2) return e;
-    // (a boundary's 256 rows on 8 CTAs, four rows a warp: short mixed requests 88.7 us; 4 CTAs 95, 16 89.7, 32 93)
+    // (a boundary's 256 rows on 8 CTAs, four rows a warp, measured when chosen: short mixed requests 88.7 us; 4 CTAs 95, 16 89.7, 32 93)
     return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 8), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
 

@@ -116,7 +116,7 @@ struct Chunk {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 4;  // tokens of a CTA, at most
-constexpr int kRopeBatch = 2;   // rows that a thread has in flight (8192 tokens: two 31.0 us, four 33.5)
+constexpr int kRopeBatch = 2;   // rows that a thread has in flight (8192 tokens: two 29.6 us, four 31.5)
 
 // Turns the V pairs of one slot of a head row, held in two chunks.  Half layout: chunk 0 holds the pairs' first
 // elements, chunk 1 their second; interleaved: the two chunks are 2V neighbours.
@@ -148,7 +148,7 @@ __device__ __forceinline__ void rotate(Chunk<T, VB>& x0, Chunk<T, VB>& x1, const
 // thread keeps one slot, so its place in a row and its pairs are fixed, and walks over the rows of the CTA's
 // tokens.  The (cos, sin) of a token are computed once per CTA, not once per head, and the steps of the pairs, in float64, once for
 // its tokens.  Rows are moved once, so HBM bounds it for prompts and latency for steps: 8192 tokens of 28 + 2 * 4 heads of 128 (bf16)
-// take 30 us, 5.0 TB/s (31 with a step per token and pair); 64 tokens 5.2 us.
+// take 30 us, 5.0 TB/s (31 with a step per token and pair); 64 tokens 5 us, 2.8 among others in a graph.
 template <typename T, int VB, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_write_kv_kernel(const RopeWriteArgs a, int tokens_per_cta) {
     constexpr int V = Chunk<T, VB>::V;
@@ -435,7 +435,8 @@ __device__ __forceinline__ void append_unit(const RopeAppendArgs& a, const Appen
 // Their positions are found and their angles computed once, in shared memory; warps then take units and groups of query
 // heads in turn, every parts-th CTA's worth of them.  Dependent steps bound it (rows, then the scale, then the codes), at two CTAs
 // per SM: 8300 prompt tokens of 28 + 2 * 4 heads of 128 (bf16) take 46 us (3.1 TB/s), 2240 of 3 * 32 heads 54 us (1.7), a decode step
-// of 64 tokens 7.4 us.  80 registers for three CTAs spilled (prompts 64 us); the rows' prefetch into L2 while positions are
+// of 64 tokens 7.4 us.  At 128 registers the 16-byte instances of 16-bit types spill 24 - 28 bytes; 80 registers for three CTAs spilled
+// far more (prompts 64 us); the rows' prefetch into L2 while positions are
 // found gained nothing.
 template <typename T, int D, int BS, int VB>
 __global__ void __launch_bounds__(kAppendThreads, 2) rope_append_fp8_kernel(const RopeAppendArgs a, int window, int parts) {
@@ -559,8 +560,8 @@ bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_
 
 template <typename T, int VB>
 cudaError_t rope_write_typed(const RopeWriteArgs& a, cudaStream_t stream) {
-    // Four tokens share a CTA when that still gives every SM one; fewer tokens take a CTA each.  (8192 tokens, bf16: 31 us, with a
-    // CTA per token 42; 1001 tokens, f32: 5.3, 7.4; 64 tokens: 8.0, 5.4.)
+    // Four tokens share a CTA when that still gives every SM one; fewer tokens take a CTA each.  (In a graph, four against one: 8192
+    // tokens, bf16, 29.6 and 38.6 us; 1001 tokens, f32, 2.8 and 4.7; 64 tokens 4.8 and 2.8.)
     const int per = a.r.num_tokens >= kRopeTokens * a.num_sms ? kRopeTokens : 1;
     const unsigned grid = (unsigned)((a.r.num_tokens + per - 1) / per);
     const size_t smem = (size_t)(per + 1) * (a.r.rotary_dim / 2) * sizeof(float2);  // (steps are as large as a token's pairs)
@@ -587,7 +588,7 @@ cudaError_t append_typed(const RopeAppendArgs& a, cudaStream_t stream) {
     // A window is a block long, so that a prompt has one block per window; while a window per token does not fill the
     // GPU, every token has its own, so that the tokens of a decode step do not queue behind one another.  (2240 tokens of 37 requests,
     // 32 kv heads: 59 us, with a window per token 129; 64 decode tokens: 7.4 us on the GPU,
-    // 19.6 with warps that took several.)
+    // 19.6 with warps that took several.  Decode steps either side, in a graph: 304 tokens 8.8 us, 305 9.4, 512 9.5.)
     const int window = r.num_tokens <= 2 * a.num_sms ? 1 : BS;
     const long long windows = (r.num_tokens + window - 1) / window;
     // The rows of a window are shared among parts of CTAs, down to a turn per warp, while that makes at most four CTAs per SM

@@ -244,6 +244,7 @@ def attend_fp8(query: torch.Tensor, key_cache: torch.Tensor, value_cache: Option
     """``pa_attend_fp8``: query ``[T, H_q, d]`` (f16/bf16) holds each request's last ``q_offsets[b + 1] - q_offsets[b]``
     positions; each row attends its request's positions up to its own over the E4M3 cache (``value_cache`` None: K and V
     records).  Rows behind ``q_offsets[B]`` of ``out`` are left as they were.  ``workspace`` defaults to a fresh one.
+    For one token of every request and no longer run, ``decode_fp8`` takes less than half the time.
     """
     num_blocks, hkv, bs, d = _fp8_cache(key_cache, value_cache, k_scale, v_scale)
     _cuda(query, "query")
