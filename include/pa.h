@@ -528,13 +528,13 @@ int pa_rope_write_kv(void* query_out, const void* query, const void* key, const 
  *  - the new rows are stored as e4m3(x / scale): round to nearest even, magnitudes above 448
  *    (infinities) saturating, NaN staying NaN.
  * k_scale, v_scale and value_cache as pa_decode_fp8 (NULL value_cache: K and V records).  Rows
- * behind q_offsets[num_seqs] are neither read nor written.  q_offsets ascends from 0 or more to at most
- * num_tokens; offsets that do not set PA_ERR_BAD_CONTEXT, and rows of theirs may be skipped.  A block that
- * takes new rows must belong to one request.  dtype PA_F32, PA_F16 or PA_BF16; rotary_dim 0: no rotation (inv_freq may be
- * NULL).  Compiled for head_dim 64 and 128, block_size 16 and 32, rotary_dim a multiple of 4
- * (PA_ERR_UNSUPPORTED otherwise).  A block id outside the pool skips its rows and sets
- * PA_ERR_BAD_TABLE, a length outside its table or below its new rows those of the request and sets
- * PA_ERR_BAD_CONTEXT, in the device error word.
+ * behind q_offsets[num_seqs] are neither read nor written.  q_offsets ascends from 0 or more to at
+ * most num_tokens; offsets that do not set PA_ERR_BAD_CONTEXT, and rows of theirs may be skipped.  A
+ * block that takes new rows must belong to one request.  dtype PA_F32, PA_F16 or PA_BF16; rotary_dim 0:
+ * no rotation (inv_freq may be NULL).  Compiled for head_dim 64 and 128, block_size 16 and 32,
+ * rotary_dim a multiple of 4 (PA_ERR_UNSUPPORTED otherwise).  A block id outside the pool skips its rows
+ * and sets PA_ERR_BAD_TABLE, a length outside its table or below its new rows those of the request and
+ * sets PA_ERR_BAD_CONTEXT, in the device error word.
  */
 int pa_rope_append_fp8(void* query_out, const void* query, const void* key, const void* value, void* key_cache,
                        void* value_cache, float* k_scale, float* v_scale, const double* inv_freq,
