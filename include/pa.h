@@ -569,6 +569,108 @@ int pa_attend_fp8(void* out, const void* query, const void* key_cache, const voi
 size_t pa_attend_fp8_workspace_size(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                     int block_size, int max_blocks_per_seq, int dtype);
 
+/* ---- a speculative step with a drafted tree -------------------------------------------- */
+/*
+ * A step that verifies a tree of drafted tokens for each request in one pass of the model:
+ * pa_advance_tables makes room (the tree's nodes are the request's new tokens, in any order in which
+ * a parent comes before its children), pa_tree_masks gives positions and masks from the parents,
+ * pa_norm_rope_write_kv (or pa_rope_write_kv) and pa_attend_tree run in every layer, pa_accept_tree
+ * follows the target's choices, and pa_compact_tree leaves the accepted branch as if it alone had been
+ * appended.  All arrays are device memory and no call needs a value on the host, so that the whole
+ * step can be captured into one graph.  Request b has n_b = q_offsets[b + 1] - q_offsets[b] nodes, the
+ * last n_b of its context_lens[b] positions (q_offsets ascends from 0 or more to at most num_tokens;
+ * offsets that do not set PA_ERR_BAD_CONTEXT and their request is left out); parents[t] is the index,
+ * among the request's nodes, of node t's parent, -1 for a root.  n_b may be 0 and differs from request
+ * to request.  num_seqs <= PA_MAX_STEP_SEQS, num_tokens <= PA_MAX_STEP_ROWS.
+ *
+ * pa_tree_masks — tree_mask [num_tokens, mask_words] int64: bit j % 64 of word j / 64 of a node's row is
+ * set where node j of its request is the node itself or one of its ancestors; positions [num_tokens]:
+ * context_lens[b] - n_b + the number of its ancestors.  Rows behind q_offsets[num_seqs] get position 0 and an
+ * empty mask.  A tree has at most PA_MAX_TREE_NODES nodes and at most 64 * mask_words: more set
+ * PA_ERR_BAD_CONTEXT, and the request's rows are not written.  A parent that does not come before its node makes
+ * a root of it and sets PA_ERR_BAD_CONTEXT; so does a length below n_b (positions from 0).
+ */
+#define PA_MAX_TREE_NODES 1024
+int pa_tree_masks(int32_t* positions, int64_t* tree_mask, const int32_t* parents, const int32_t* context_lens,
+                  const int32_t* q_offsets, int num_seqs, int num_tokens, int mask_words, void* stream);
+
+/*
+ * pa_norm_rope_write_kv — pa_rope_write_kv with a norm of every query and key head before its rotation: a
+ * head x becomes x / sqrt(sum x^2 / head_dim + eps) * (weight + weight_offset), with q_weight and k_weight
+ * [head_dim] of weight_dtype (PA_F32, PA_F16 or PA_BF16), shared by the heads (NULL: the norm alone).
+ * float32 arithmetic, the sum of squares included, and one rounding, behind the rotation; values are not
+ * normed.  rotary_dim 0: no rotation (inv_freq may be NULL).  Other arguments, layouts and errors as
+ * pa_rope_write_kv.
+ */
+int pa_norm_rope_write_kv(void* query_out, const void* query, const void* key, const void* value, void* key_cache,
+                          void* value_cache, const void* q_weight, const void* k_weight, const double* inv_freq,
+                          const int32_t* positions, const int64_t* slot_mapping, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, int num_tokens, int num_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                          int layout, float factor, float eps, float weight_offset, int weight_dtype, int block_size,
+                          int num_blocks, int dtype, void* stream);
+
+/*
+ * pa_attend_tree — attention of the nodes over a paged f16 / bf16 cache (which holds their own K and V
+ * already): a row of query [num_tokens, num_heads, head_dim] attends the context_lens[b] - n_b positions
+ * before the request's nodes, and node j of its request where bit j of its row of tree_mask is set (any
+ * bits: pa_tree_masks gives those of a tree; a chain's are those of causal runs, one node is a decode
+ * step).  A row that sees nothing gets zeros; rows behind q_offsets[num_seqs] are left as they were.  What a row does not
+ * see does not reach it, whatever its K and V hold (infinities and NaN too), nor does what lies behind a context.
+ * Scores, softmax and sums are float32; the weights that multiply V are rounded to dtype, relative to an
+ * exponential of the row's that is at most 2^8 below its largest (f16: weights below 2^-14 of it lose bits).  query and out f16 or bf16, contiguous, 16-byte aligned; caches
+ * [num_blocks, num_kv_heads, block_size, head_dim] of the same type, 16-byte aligned.  Compiled for head_dim 64
+ * and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED otherwise).  Nodes past 64 * mask_words are seen by no row
+ * and set PA_ERR_BAD_CONTEXT; a block id outside the pool reads as masked positions and sets
+ * PA_ERR_BAD_TABLE; a length outside its table is clamped and sets PA_ERR_BAD_CONTEXT, as does one below
+ * n_b (nodes before position 0 are not seen).
+ *  workspace  pa_attend_tree_workspace_size() bytes, 256-byte aligned, no initialisation; calls that
+ *             share one must not overlap on the GPU.
+ */
+int pa_attend_tree(void* out, const void* query, const void* key_cache, const void* value_cache, const int64_t* tree_mask,
+                   const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_offsets, int num_seqs,
+                   int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                   int num_blocks, int mask_words, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                   void* stream);
+size_t pa_attend_tree_workspace_size(int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                     int block_size, int max_blocks_per_seq, int dtype);
+
+/*
+ * pa_accept_tree — greedy acceptance: from node 0 of a request (the token that is certain already) on to the first
+ * child, by index, whose tokens[] entry is choices[] (the target model's choice after a node) at the node,
+ * as long as there is one and at most max_accepted nodes in all.  accepted [num_seqs, max_accepted] int32
+ * receives the nodes' indices in their request, ascending, -1 behind them; num_accepted [num_seqs] their
+ * number (0 for a request without nodes); next_tokens [num_seqs] the choice at the last of them (-1 without one), the token that
+ * the step adds.  tokens, choices and next_tokens are int32 or int64 (token_bytes 4 or 8).
+ * 1 <= max_accepted <= PA_MAX_TREE_NODES.  A tree of more than PA_MAX_TREE_NODES nodes accepts none, a parent
+ * that does not come before its node (or of node 0) is no parent; both set PA_ERR_BAD_CONTEXT.
+ */
+int pa_accept_tree(int32_t* accepted, int32_t* num_accepted, void* next_tokens, const int32_t* parents, const void* tokens,
+                   const void* choices, const int32_t* q_offsets, int num_seqs, int num_tokens, int max_accepted,
+                   int token_bytes, void* stream);
+
+/*
+ * pa_compact_tree — what stays of the step's nodes.  K and V of the accepted node accepted[b, j] move to the slot of node j
+ * (slot_mapping [num_tokens], of pa_advance_tables: the j-th position behind the cached ones), in every
+ * layer's caches, byte for byte; context_lens_out [num_seqs] receives context_lens[b] - n_b +
+ * num_accepted[b], and the blocks behind that go back: pushed onto free_blocks, by request, in table
+ * order, with num_free_out [1] the new count.  context_lens_out and num_free_out may be context_lens and
+ * num_free.  Table entries of blocks given back stay; nothing reads them.  key_caches and value_caches are HOST arrays of num_layers
+ * device pointers, as pa_write_kv_layers'; all caches of a block geometry; dtype PA_F32, PA_F16 or PA_BF16.  Requests'
+ * blocks must be their own (as pa_advance_tables').
+ * accepted is any ascending choice of a request's nodes (pa_accept_tree's, or a sampling rule's).  A
+ * request whose accepted nodes are not, or whose length is below n_b or outside its table, keeps its length and
+ * blocks (of the latter two, nodes may have moved) and sets PA_ERR_BAD_CONTEXT; one with an id outside
+ * [0, num_blocks) among the blocks that it would give back keeps them and its length and sets PA_ERR_BAD_TABLE; a node whose own or new slot
+ * lies outside the pool does not move and sets PA_ERR_BAD_SLOT.  A stack without room for what is given back
+ * sets PA_ERR_BAD_TABLE, and lengths and count stay as they are.
+ */
+int pa_compact_tree(void* const* key_caches, void* const* value_caches, int num_layers, const int64_t* slot_mapping,
+                    const int32_t* q_offsets, const int32_t* accepted, const int32_t* num_accepted,
+                    const int32_t* block_tables, const int32_t* context_lens, int32_t* free_blocks, const int32_t* num_free,
+                    int32_t* context_lens_out, int32_t* num_free_out, int num_seqs, int num_tokens, int max_accepted,
+                    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, int dtype,
+                    void* stream);
+
 /* ---- host block pool ----------------------------------------------------------------- */
 /*
  * Fixed-size block allocator with reference counts, fork and copy-on-write

@@ -45,6 +45,18 @@ from .step_ops import (  # noqa: F401,E402
     rope_frequencies,
     rope_write_kv,
 )
+from .tree_ops import (  # noqa: F401,E402
+    MAX_TREE_NODES,
+    TreeMasks,
+    TreePath,
+    TreeState,
+    accept_tree,
+    attend_tree,
+    attend_tree_workspace_size,
+    compact_tree,
+    norm_rope_write_kv,
+    tree_masks,
+)
 
 
 def build(force: bool = False) -> str:

@@ -101,6 +101,12 @@ _SIGNATURES = [
     ("pa_rope_append_fp8", _I, [_P] * 12 + [_I64] * 3 + [_I] * 7 + [_F] + [_I] * 4 + [_P]),
     ("pa_attend_fp8", _I, [_P] * 9 + [_I] * 8 + [_F, _I, _P, _SZ, _P]),
     ("pa_attend_fp8_workspace_size", _SZ, [_I] * 8),
+    ("pa_tree_masks", _I, [_P] * 5 + [_I] * 3 + [_P]),
+    ("pa_norm_rope_write_kv", _I, [_P] * 11 + [_I64] * 3 + [_I] * 6 + [_F] * 3 + [_I] * 4 + [_P]),
+    ("pa_attend_tree", _I, [_P] * 8 + [_I] * 9 + [_F, _I, _P, _SZ, _P]),
+    ("pa_attend_tree_workspace_size", _SZ, [_I] * 8),
+    ("pa_accept_tree", _I, [_P] * 7 + [_I] * 4 + [_P]),
+    ("pa_compact_tree", _I, [_P, _P, _I] + [_P] * 10 + [_I] * 9 + [_P]),
     ("pa_stepper_create", _I, [_I, _P, _P, _P, ctypes.POINTER(_P)]),
     ("pa_stepper_destroy", None, [_P]),
     ("pa_stepper_set_slot", _I, [_P, _I, _P, _P, _SZ, _P, _P, _SZ]),

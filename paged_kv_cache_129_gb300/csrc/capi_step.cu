@@ -2,36 +2,15 @@
 #include <cmath>
 #include <cstdint>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "capi_checks.h"
 #include "pa.h"
 #include "pa_internal.h"
 #include "step_ops.h"
+#include "tree_ops.h"
 
 using namespace pa;
 
 namespace {
-
-struct CallRange {
-    explicit CallRange(const char* name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-    CallRange(const CallRange&) = delete;
-    CallRange& operator=(const CallRange&) = delete;
-};
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool fits_int(long long x) { return x < (1ll << 31); }
-int bytes_of(int dtype) { return dtype == PA_F32 ? 4 : 2; }
-
-// Whether [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void* p, long long n, const void* q, long long m) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return n > 0 && m > 0 && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
-}
-
-int launch_failed(cudaError_t e, const char* what) {
-    return fail(PA_ERR_CUDA, "%s launch: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
 
 // Checks shared by the two rotary entry points; fills what they share.
 int rope_args(const char* fn, RopeArgs* r, void* query_out, const void* query, const void* key, const void* value,
@@ -164,6 +143,44 @@ int pa_rope_write_kv(void* query_out, const void* query, const void* key, const 
     if (st != PA_OK) return st;
     const cudaError_t e = rope_write_kv_launch(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : launch_failed(e, "pa_rope_write_kv");
+}
+
+int pa_norm_rope_write_kv(void* query_out, const void* query, const void* key, const void* value, void* key_cache,
+                          void* value_cache, const void* q_weight, const void* k_weight, const double* inv_freq,
+                          const int32_t* positions, const int64_t* slot_mapping, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          int num_tokens, int num_heads, int num_kv_heads, int head_dim, int rotary_dim, int layout, float factor,
+                          float eps, float weight_offset, int weight_dtype, int block_size, int num_blocks, int dtype, void* stream) {
+    CallRange range("pa_norm_rope_write_kv");
+    clear_error();
+    NormRopeArgs a{};
+    int st = rope_args("pa_norm_rope_write_kv", &a.r, query_out, query, key, value, q_stride, k_stride, v_stride, inv_freq,
+                       rotary_dim, layout, factor, num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype);
+    if (st != PA_OK) return st;
+    if (head_dim > 512) return fail(PA_ERR_UNSUPPORTED, "pa_norm_rope_write_kv: head_dim=%d > 512", head_dim);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(PA_ERR_INVALID_ARG, "pa_norm_rope_write_kv: eps must be finite and not negative");
+    if (!std::isfinite(weight_offset)) return fail(PA_ERR_INVALID_ARG, "pa_norm_rope_write_kv: weight_offset is not finite");
+    if ((q_weight || k_weight) && weight_dtype != PA_F32 && weight_dtype != PA_F16 && weight_dtype != PA_BF16)
+        return fail(PA_ERR_INVALID_ARG, "pa_norm_rope_write_kv: unknown weight_dtype %d", weight_dtype);
+    if (num_tokens == 0) return PA_OK;
+    if (!key_cache || !value_cache || !positions || !slot_mapping)
+        return fail(PA_ERR_INVALID_ARG, "pa_norm_rope_write_kv: NULL pointer");
+    const int eb = bytes_of(dtype), wb = bytes_of(weight_dtype);
+    if (!aligned(key_cache, eb) || !aligned(value_cache, eb) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
+        !aligned(q_weight, wb) || !aligned(k_weight, wb))
+        return fail(PA_ERR_INVALID_ARG, "pa_norm_rope_write_kv: misaligned buffer");
+    a.key_cache = key_cache;
+    a.value_cache = value_cache;
+    a.positions = positions;
+    a.slot_mapping = slot_mapping;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.weight_dtype = weight_dtype;
+    a.weight_offset = weight_offset;
+    a.eps = eps;
+    st = device_state(&a.r.err, &a.num_sms);
+    if (st != PA_OK) return st;
+    const cudaError_t e = norm_rope_write_kv_launch(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : launch_failed(e, "pa_norm_rope_write_kv");
 }
 
 int pa_rope_append_fp8(void* query_out, const void* query, const void* key, const void* value, void* key_cache,

@@ -1,0 +1,231 @@
+// Drafted trees of a speculative step: which nodes a node sees, which of them the target confirms, and the confirmed branch
+// moved together in the caches.
+//
+// Request b has the nodes q_offsets[b] .. q_offsets[b + 1] - 1; parents[t] < the node's own index is the index, in the request, of its
+// parent (-1: a root).  With a(i) the set of i and its ancestors:
+//   masks     bit j of node i's words is set where j is in a(i); position = cached tokens + |a(i)| - 1;
+//   accept    the path from node 0 that always goes to the first child whose token is the target's choice at the node;
+//   compact   with accepted nodes a_0 < a_1 < .. (so a_j >= j), K and V of node a_j go to the slot of node j, in every layer; the
+//             request keeps its cached tokens and the accepted ones, blocks behind them go back on the stack.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "pa_common.cuh"
+#include "tree_ops.h"
+
+namespace pa {
+
+namespace {
+
+// A request's nodes: none if its offsets are no run, or are more than a tree may have.
+__device__ __forceinline__ int nodes_of(const int32_t* q_offsets, int b, int num_tokens, int most, int* first, bool* bad) {
+    const int lo = q_offsets[b], hi = q_offsets[b + 1];
+    *first = lo;
+    *bad = !is_run(lo, hi, num_tokens) || hi - lo > most;
+    return *bad ? 0 : hi - lo;
+}
+
+// ---- masks -------------------------------------------------------------------------------------------
+
+constexpr int kMaskThreads = 128;
+
+// A CTA per request, a thread per node: the ancestors of a node come in descending order, so a thread fills one word after the other,
+// from the last, and writes each once.  The CTA behind the last request clears the rows behind its nodes.
+__global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const TreeMaskArgs a) {
+    __shared__ int parent[kMaxTreeNodes];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int b = blockIdx.x, W = a.mask_words;
+    if (b == a.num_seqs) {
+        const int end = max(0, min(a.q_offsets[b], a.num_tokens));
+        for (long long i = (long long)end * W + threadIdx.x; i < (long long)a.num_tokens * W; i += kMaskThreads) a.tree_mask[i] = 0;
+        for (int t = end + threadIdx.x; t < a.num_tokens; t += kMaskThreads) a.positions[t] = 0;
+        return;
+    }
+    int first;
+    bool bad;
+    const int n = nodes_of(a.q_offsets, b, a.num_tokens, min(kMaxTreeNodes, 64 * W), &first, &bad);
+    const int cached = a.context_lens[b] - n;
+    if (cached < 0) bad = true;
+    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+        const int p = a.parents[first + i];
+        if (p < -1 || p >= i) bad = true;  // (a node without a parent before it is a root)
+        parent[i] = p < i ? max(p, -1) : -1;
+    }
+    if (bad) atomicOr(a.err, kErrBadContext);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+        int64_t* row = a.tree_mask + (long long)(first + i) * W;
+        int node = i, depth = 0;
+        for (int w = W - 1; w >= 0; --w) {
+            unsigned long long word = 0;
+            for (; node >= 64 * w; node = parent[node], ++depth) word |= 1ull << (node - 64 * w);
+            row[w] = (int64_t)word;
+        }
+        a.positions[first + i] = max(0, cached) + depth - 1;
+    }
+}
+
+// ---- acceptance ----------------------------------------------------------------------------------------
+
+constexpr int kAcceptThreads = 128;
+
+// A CTA per request: every node bids for its parent's step, the first child wins; one thread then follows the steps.
+template <typename Token>
+__global__ void __launch_bounds__(kAcceptThreads) accept_tree_kernel(const AcceptArgs a) {
+    __shared__ int next[kMaxTreeNodes];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int b = blockIdx.x;
+    const Token* tokens = static_cast<const Token*>(a.tokens);
+    const Token* choices = static_cast<const Token*>(a.choices);
+    int first;
+    bool bad;
+    const int n = nodes_of(a.q_offsets, b, a.num_tokens, kMaxTreeNodes, &first, &bad);
+    for (int i = threadIdx.x; i < n; i += kAcceptThreads) next[i] = INT_MAX;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kAcceptThreads) {
+        const int p = a.parents[first + i];
+        if (p < -1 || p >= i || (i == 0 && p != -1)) bad = true;
+        if (p >= 0 && p < i && tokens[first + i] == choices[first + p]) atomicMin(&next[p], i);
+    }
+    if (bad) atomicOr(a.err, kErrBadContext);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    int32_t* row = a.accepted + (long long)b * a.max_accepted;
+    int count = 0, last = -1;
+    for (int node = n > 0 ? 0 : INT_MAX; node != INT_MAX && count < a.max_accepted; node = next[node]) {
+        row[count++] = node;
+        last = node;
+    }
+    for (int j = count; j < a.max_accepted; ++j) row[j] = -1;
+    a.num_accepted[b] = count;
+    static_cast<Token*>(a.next_tokens)[b] = last >= 0 ? choices[first + last] : (Token)-1;
+}
+
+// ---- compaction ----------------------------------------------------------------------------------------
+
+constexpr int kCompactThreads = 256;
+
+// Whether request b's accepted nodes are some of its n nodes in ascending order.  Any number of threads, each for itself.
+__device__ __forceinline__ bool is_path(const CompactArgs& a, int b, int n, int count) {
+    if (count < 0 || count > n || count > a.max_accepted) return false;
+    int before = -1;
+    for (int j = 0; j < count; ++j) {
+        const int node = a.accepted[(long long)b * a.max_accepted + j];
+        if (node <= before || node >= n) return false;
+        before = node;
+    }
+    return true;
+}
+
+// New lengths, and the blocks given back: one CTA, a contiguous run of requests per thread.
+__device__ __forceinline__ void trim(const CompactArgs& a) {
+    __shared__ int sums[kCompactThreads + 1];
+    const int tid = threadIdx.x, B = a.num_seqs, bs = a.block_size;
+    const int per = (B + kCompactThreads - 1) / kCompactThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    const int free0 = *a.num_free;
+    unsigned bits = 0;
+    // blocks that request b gives back, from which on; -1: it keeps its length
+    auto give = [&](int b, int* keep, int* length) {
+        int first;
+        bool bad;
+        const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), L = a.context_lens[b], k = a.num_accepted[b];
+        *length = L;
+        if (bad || L < n || L > (long long)a.max_blocks * bs || !is_path(a, b, n, k)) {
+            bits |= kErrBadContext;
+            return -1;
+        }
+        *keep = (int)(((long long)L - n + k + bs - 1) / bs);
+        const int had = (int)(((long long)L + bs - 1) / bs);
+        for (int j = *keep; j < had; ++j) {
+            const int id = a.block_tables[(long long)b * a.max_blocks + j];
+            if (id < 0 || id >= a.num_blocks) {
+                bits |= kErrBadTable;
+                return -1;
+            }
+        }
+        *length = L - n + k;
+        return had - *keep;
+    };
+    int keep, length, mine = 0;
+    for (int b = b0; b < b1; ++b) mine += max(0, give(b, &keep, &length));
+    if (tid == 0) sums[0] = 0;
+    sums[tid + 1] = mine;
+    __syncthreads();
+    if (tid == 0)
+        for (int i = 0; i < kCompactThreads; ++i) sums[i + 1] += sums[i];
+    __syncthreads();
+    const int total = sums[kCompactThreads];
+    const bool room = free0 >= 0 && (long long)free0 + total <= a.num_blocks;
+    if (!room) bits |= kErrBadTable;
+    int at = free0 + sums[tid];
+    for (int b = b0; b < b1; ++b) {
+        const int n = give(b, &keep, &length);
+        if (room)
+            for (int j = 0; j < n; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + keep + j];
+        a.context_lens_out[b] = room ? length : a.context_lens[b];
+    }
+    if (tid == 0) *a.num_free_out = room ? free0 + total : free0;
+    if (bits) atomicOr(a.err, bits);
+}
+
+// Row (node a_j, layer, K or V, kv head) goes to the place of node j.  A thread has a column of VB bytes and takes the nodes in order: a
+// node's place is written behind every read of it, since a_j >= j.
+template <typename Vec>
+__global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const CompactArgs a, const __grid_constant__ CachePtrs caches) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if (blockIdx.x == (unsigned)a.num_seqs) {
+        trim(a);
+        return;
+    }
+    const int b = blockIdx.x, H = a.num_kv_heads, bs = a.block_size;
+    int first;
+    bool bad;
+    const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), count = a.num_accepted[b];
+    if (bad || !is_path(a, b, n, count)) return;
+    const int columns = a.row_bytes / (int)sizeof(Vec);
+    const long long slots = (long long)a.num_blocks * bs, items = 2ll * a.num_layers * H * columns;
+    for (long long x = threadIdx.x; x < items; x += kCompactThreads) {
+        const int unit = (int)(x / columns), column = (int)(x - (long long)unit * columns);
+        const int layer = unit / (2 * H), h = unit % H;
+        char* cache = (unit / H & 1 ? caches.value[layer] : caches.key[layer]);
+        for (int j = 0; j < count; ++j) {
+            const int node = a.accepted[(long long)b * a.max_accepted + j];
+            if (node == j) continue;
+            const long long from = a.slot_mapping[first + node], to = a.slot_mapping[first + j];
+            if (from < 0 || from >= slots || to < 0 || to >= slots) {
+                atomicOr(a.err, kErrBadSlot);
+                continue;
+            }
+            auto place = [&](long long slot) {
+                const long long row = (slot / bs * H + h) * bs + slot % bs;
+                return reinterpret_cast<Vec*>(cache + row * a.row_bytes) + column;
+            };
+            *place(to) = *place(from);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t tree_masks_launch(const TreeMaskArgs& a, cudaStream_t stream) {
+    return launch_pdl(tree_masks_kernel, dim3((unsigned)a.num_seqs + 1), dim3(kMaskThreads), 0, stream, a);
+}
+
+cudaError_t accept_tree_launch(const AcceptArgs& a, cudaStream_t stream) {
+    if (a.token_bytes == 4)
+        return launch_pdl(accept_tree_kernel<int32_t>, dim3((unsigned)a.num_seqs), dim3(kAcceptThreads), 0, stream, a);
+    return launch_pdl(accept_tree_kernel<int64_t>, dim3((unsigned)a.num_seqs), dim3(kAcceptThreads), 0, stream, a);
+}
+
+cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.num_seqs + 1), block(kCompactThreads);
+    if (a.vector) return launch_pdl(compact_tree_kernel<uint4>, grid, block, 0, stream, a, caches);
+    if (a.elem_bytes == 4) return launch_pdl(compact_tree_kernel<uint32_t>, grid, block, 0, stream, a, caches);
+    return launch_pdl(compact_tree_kernel<uint16_t>, grid, block, 0, stream, a, caches);
+}
+
+}  // namespace pa

@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpagedkv.so")
 
 CUDA_SOURCES = ["capi.cu", "kv_ops.cu", "decode_f32.cu", "decode_f16.cu", "decode_bf16.cu", "decode_fp8.cu",
-                "decode_static_scratch.cu", "capi_step.cu", "table_ops.cu", "rope_ops.cu", "attend_fp8.cu"]
+                "decode_static_scratch.cu", "capi_step.cu", "table_ops.cu", "rope_ops.cu", "attend_fp8.cu",
+                "capi_tree.cu", "tree_ops.cu", "norm_rope_ops.cu", "attend_tree.cu"]
 CXX_SOURCES = ["block_pool.cpp", "stepper.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
