@@ -31,14 +31,15 @@
 
 #include <cuda_fp8.h>
 
+#include "attend_units.cuh"
 #include "pa_common.cuh"
 #include "step_ops.h"
+#include "tcgen05.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kTile = 128;             // rows of a row tile, tokens of a key tile
 constexpr int kSoftmaxWarps = 8;       // four per stream
 constexpr int kWidenWarps = 4;
 constexpr int kIssueWarp = kSoftmaxWarps + kWidenWarps;  // two, one per stream
@@ -52,119 +53,21 @@ constexpr int kNanRing = 2;            // V of tile i is widened once the scores
 // widening), and of a unit besides its tiles (queries staged, streams joined, output written: about six split tiles).  Measured when chosen
 // (verification / prompt chunks / long contexts / short mixed D = 64, us): 6, 4, 24: 115 / 625 / 387 / 95; 4, 3, 8: 135 / 656 / 412 /
 // 98.  With prefetches as in look_ahead()'s note, 4, 3, 0 (no cost of a unit) took 175 / 694 / 430 / 125, 4, 3, 8 143 / 675 / 439 / 99.
-constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 24;
-constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
-
-// ---- work list (made by plan_kernel) ------------------------------------------------------------
-
-struct Entry {
-    long long first;  // cost before this entry
-    int seq, row0;    // request, first row
-    int tiles;        // key tiles, >= 1
-    int paired;
+struct Fp8Rule {
+    static constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 24;
+    static constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
+    // Key tiles of rows row0 .. row0 + 255 of a request: up to the last row's position.
+    static __device__ __forceinline__ int tiles(int L, int n, int group, int row0) {
+        const int last = min(n * group, row0 + 2 * kTile) - 1;
+        const int bound = L - n + last / group;
+        return max(1, (bound + kTile) / kTile);
+    }
+    static __device__ __forceinline__ bool refuses(const AttendArgs&, int, int) { return false; }
 };
-static_assert(sizeof(Entry) == 24, "packed");
-
-struct PlanHead {
-    long long cost;
-    int entries, pad;
-};
-
-struct Workspace {
-    PlanHead* head;
-    Entry* entries;   // [max_entries + 1], the last one a sentinel
-    float* records;   // [CTAs][2 slots][2 tiles][m 128 | l 128 | o 128 x D]
-};
-
-__host__ __device__ inline size_t record_floats(int D) { return (size_t)kTile * (D + 2); }
-inline size_t max_entries(int num_seqs, int num_tokens, int group) {
-    return (size_t)num_seqs + ((size_t)num_tokens * group) / (2 * kTile);
-}
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+using Walk = UnitWalk<Fp8Rule>;
 
 // ---- PTX ------------------------------------------------------------------------------------------
 
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, int columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst_smem)), "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr, int columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Products and commits are issued by whole warps, in which one lane is elected each time: control flow and operands are then
-// uniform for the compiler too.  In a branch of one lane every descriptor has to be moved to uniform registers before
-// each product: 70 to 125 cycles apart instead of the 64 that one takes.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
-        : "memory");
-}
-// Waits for this warp's loads; r are registers that they fill (so that nothing reads them earlier).
-template <int N>
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
-
-// 32 columns of this warp's 32 lanes of tensor memory.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-        : "memory");
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Four rows y of a tensor map whose box is one row, into shared memory one after the other; x in elements.  One elected lane.
 __device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int x, int4 y, uint64_t* bar) {
     asm volatile(
@@ -174,198 +77,6 @@ __device__ __forceinline__ void gather4(void* dst, const CUtensorMap* map, int x
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_addr(bar))
         : "memory");
 }
-// Operand tiles in shared memory: panels of 64 elements (128 bytes) by 128 rows, 128-byte swizzle (16-byte unit u of row r
-// at u ^ (r % 8)), 16 KB apart.  Descriptors: bits 0-13 address / 16, 16-29 and 32-45 byte offsets / 16, 46 version 1,
-// 61-63 the 128-byte swizzle (2).
-constexpr uint32_t kPanel = kTile * 128;
-__device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t leading, uint32_t stride) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor: f16 x f16 -> f32; bit 16: B is given with N contiguous (V: [token][d]).
-constexpr uint32_t idesc_of(int n, bool b_n_major) {
-    return (1u << 4) | ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-}
-
-// ---- the plan ------------------------------------------------------------------------------------------
-
-__device__ __forceinline__ int clamped_length(const AttendArgs& a, int b) {
-    return max(0, min(a.context_lens[b], a.max_blocks * a.block_size));
-}
-__device__ __forceinline__ int rows_of(const AttendArgs& a, int b) {  // request b's new tokens; none if its offsets are no run
-    const int lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
-    return is_run(lo, hi, a.num_tokens) ? hi - lo : 0;
-}
-
-// Key tiles of rows row0 .. row0 + 255 of a request: up to the last row's position.
-__device__ __forceinline__ int tiles_of(int L, int n, int group, int row0) {
-    const int last = min(n * group, row0 + 2 * kTile) - 1;
-    const int bound = L - n + last / group;
-    return max(1, (bound + kTile) / kTile);
-}
-
-__device__ __forceinline__ long long unit_cost(int tiles, int paired) {
-    return kUnitCost + (long long)tiles * (paired ? kPairedCost : kSplitCost);
-}
-
-constexpr int kPlanThreads = 1024;
-
-// Exclusive sum of x over the CTA; *total the whole.  scratch: 33 entries.
-__device__ __forceinline__ long long block_scan(long long x, long long* scratch, long long* total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    long long s = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
-    __syncthreads();
-    if (lane == 31) scratch[wid] = s;
-    __syncthreads();
-    if (wid == 0) {
-        long long w = scratch[lane], t = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
-        }
-        scratch[lane] = t - w;
-        if (lane == 31) scratch[32] = t;
-    }
-    __syncthreads();
-    *total = scratch[32];
-    return scratch[wid] + s - x;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendArgs a, const Workspace ws, int entry_cap) {
-    extern __shared__ int first_entry[];  // [num_seqs + 1]
-    __shared__ long long scratch[33];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int group = a.num_heads / a.num_kv_heads, tid = threadIdx.x;
-    long long base = 0, total = 0;
-    for (int b0 = 0; b0 < a.num_seqs; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        long long n = 0;
-        if (b < a.num_seqs) {
-            const int L = a.context_lens[b];
-            if (L < 0 || L > a.max_blocks * a.block_size || !is_run(a.q_offsets[b], a.q_offsets[b + 1], a.num_tokens))
-                atomicOr(a.err, kErrBadContext);
-            n = ((long long)rows_of(a, b) * group + 2 * kTile - 1) / (2 * kTile);
-        }
-        const long long at = base + block_scan(n, scratch, &total);
-        if (b < a.num_seqs) first_entry[b] = (int)min(at, (long long)entry_cap);
-        base += total;
-    }
-    int entries = (int)min(base, (long long)entry_cap);
-    if (base > entry_cap) {  // runs that overlap
-        if (tid == 0) atomicOr(a.err, kErrBadContext);
-        entries = 0;
-    }
-    if (tid == 0) first_entry[a.num_seqs] = entries;
-    __syncthreads();
-    long long cost = 0;
-    for (int e0 = 0; e0 < entries; e0 += kPlanThreads) {
-        const int e = e0 + tid;
-        Entry x{};
-        long long c = 0;
-        if (e < entries) {
-            int lo = 0, hi = a.num_seqs;  // the last request whose first entry is <= e: one with rows
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (first_entry[mid] <= e)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            const int n = rows_of(a, lo);
-            x.seq = lo;
-            x.row0 = (e - first_entry[lo]) * 2 * kTile;
-            x.paired = n * group - x.row0 > kTile;
-            x.tiles = tiles_of(clamped_length(a, lo), n, group, x.row0);
-            c = unit_cost(x.tiles, x.paired) * a.num_kv_heads;
-        }
-        x.first = cost + block_scan(c, scratch, &total);
-        cost += total;
-        if (e < entries) ws.entries[e] = x;
-    }
-    if (tid == 0) {
-        ws.entries[entries].first = cost;
-        ws.head->cost = cost;
-        ws.head->entries = entries;
-    }
-}
-
-__device__ __forceinline__ long long share_of(long long cost, int ctas) {
-    const long long s = (cost + ctas - 1) / ctas;
-    return s > kMinShare ? s : kMinShare;
-}
-
-// The entry that cost position x falls into; whole CTA or warp, any number of threads.
-__device__ __forceinline__ int find_entry(const Entry* e, int n, long long x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (e[mid].first <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-// Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).
-__device__ __forceinline__ int tiles_in(long long x, int tiles, bool paired) {
-    const unsigned cost = (unsigned)max(0ll, min(x - kUnitCost, (long long)tiles * (paired ? kPairedCost : kSplitCost)));
-    return (int)(paired ? (cost + kPairedCost - 1) / kPairedCost : (cost + kSplitCost - 1) / kSplitCost);
-}
-
-// The part of one unit that a share covers: key tiles [begin, end) of `tiles`.
-struct Piece {
-    int seq, row0, kvh, tiles, begin, end;
-    bool paired;
-};
-
-// Walks over the pieces of share [pos, stop) of the plan.
-struct Walk {
-    const Entry* entries;
-    int count, heads, e, kvh;
-    long long pos, stop;
-    __device__ __forceinline__ Walk(const Workspace& ws, int heads_, int cta, int ctas) : entries(ws.entries), heads(heads_) {
-        const long long cost = ws.head->cost, share = share_of(cost, ctas);
-        count = ws.head->entries;
-        pos = share * cta;
-        stop = min(pos + share, cost);
-        e = kvh = 0;
-        if (pos < stop) {
-            e = find_entry(entries, count, pos);
-            const Entry x = entries[e];
-            kvh = (int)((pos - x.first) / unit_cost(x.tiles, x.paired));
-        }
-    }
-    __device__ __forceinline__ bool next(Piece* p) {
-        while (pos < stop) {
-            const Entry x = entries[e];
-            const long long cost = unit_cost(x.tiles, x.paired), unit = x.first + kvh * cost;
-            const long long from = pos > unit ? pos - unit : 0, to = stop - unit;
-            p->seq = x.seq;
-            p->row0 = x.row0;
-            p->kvh = kvh;
-            p->tiles = x.tiles;
-            p->paired = x.paired != 0;
-            p->begin = tiles_in(from, x.tiles, p->paired);
-            p->end = tiles_in(to, x.tiles, p->paired);
-            pos = unit + cost;
-            if (++kvh == heads) {
-                kvh = 0;
-                ++e;
-            }
-            if (p->begin < p->end) return true;
-        }
-        return false;
-    }
-};
-
 // ---- shared memory of the attention kernel -----------------------------------------------------------------
 
 template <int D>
@@ -406,36 +117,6 @@ __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
 }
 
 static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "fits an SM");
-
-// mbar_wait_bounded, with the clock and the abort flag read only now and then: waiting warps share their scheduler with warps
-// that work.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_bounded(bar, parity, err, abort);
-}
-// The same by a whole warp: all lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait_for(bar, parity, err, abort));
-}
-
-// What a piece is to every role.
-struct Item {
-    int L, n, group, rows;  // length, new tokens, heads per kv head, rows of the request
-    int first_token;        // row of the request's first new token in query / out
-    int jobs;               // score tiles: two streams take them in turn
-};
-__device__ __forceinline__ Item item_of(const AttendArgs& a, const Piece& p) {
-    Item it;
-    it.L = clamped_length(a, p.seq);
-    it.n = rows_of(a, p.seq);
-    it.group = a.num_heads / a.num_kv_heads;
-    it.rows = it.n * it.group;
-    it.first_token = a.q_offsets[p.seq];
-    it.jobs = (p.end - p.begin) * (p.paired ? 2 : 1);
-    return it;
-}
 
 // Sixteen E4M3 codes as f16 (exact), in two 16-byte units.
 __device__ __forceinline__ void widen_store(unsigned char* unit0, unsigned char* unit1, uint4 c) {
@@ -703,25 +384,6 @@ __device__ __forceinline__ void issue_products(const AttendArgs& a, const Worksp
         }
         fills += 2 * n;
     }
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-        "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-        "l"(*reinterpret_cast<uint64_t*>(&b)));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-        "l"(*reinterpret_cast<uint64_t*>(&b)));
-    return d;
 }
 
 // A warp's 32 query rows to f16, into the swizzled tile; row_at: where this lane's row begins (live: if it exists).  D / 8 lanes load a
@@ -1140,69 +802,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp8_kernel(const AttendArg
     if (warp == kIssueWarp) tmem_free(sm.tmem, 512);
 }
 
-// Joins the partial results of the units that share boundaries cut.  CTA (boundary, rows): the first boundary inside a unit
-// has it; a warp per row, D / 32 elements per lane.
-constexpr int kJoinThreads = 256;
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, const Workspace ws, int ctas) {
-    griddep_wait();
-    griddep_launch_dependents();
-    constexpr int E = D / 32;
-    using Vec = typename std::conditional<E == 4, float4, float2>::type;
-    const long long cost = ws.head->cost, share = share_of(cost, ctas);
-    const int c1 = blockIdx.x + 1;  // boundary: the start of CTA c1's share
-    const long long x = share * c1;
-    if (x >= cost) return;
-    const Entry en = ws.entries[find_entry(ws.entries, ws.head->entries, x)];
-    const long long each = unit_cost(en.tiles, en.paired);
-    const int kvh = (int)((x - en.first) / each);
-    const long long unit = en.first + kvh * each, end = unit + each;
-    if (x == unit || share * (c1 - 1) > unit) return;  // not inside, or not the first inside
-    // pieces: CTA c has tiles [cut(c), cut(c + 1))
-    auto cut = [&](int c) {
-        const long long from = share * c - unit;
-        return tiles_in(from, en.tiles, en.paired != 0);
-    };
-    const int first = c1 - 1, last = (int)((end - 1) / share);
-    bool parts = false;  // (a boundary inside the cost may still fall before the first tile or behind the last)
-    for (int c = first + 1; c <= last; ++c) parts |= cut(c) > 0 && cut(c) < en.tiles;
-    if (!parts) return;
-    const int n = rows_of(a, en.seq), group = a.num_heads / a.num_kv_heads;
-    const int rows = min(n * group - en.row0, 2 * kTile);
-    const int lane = threadIdx.x & 31;
-    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows; r += gridDim.y * (kJoinThreads / 32)) {
-        const int tile = r / kTile, rr = r % kTile;
-        float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = 0.f;
-        for (int c = first; c <= last; ++c) {
-            const int from = cut(c);
-            if (from >= cut(c + 1)) continue;
-            const float* rec = ws.records + ((size_t)c * 4 + (from > 0 ? 0 : 2) + tile) * record_floats(D);
-            const float mc = rec[rr], lc = rec[kTile + rr];
-            const float mn = fmaxf(m, mc);
-            float f = m == -INFINITY ? 0.f : exp2_approx(m - mn), fc = mc == -INFINITY ? 0.f : exp2_approx(mc - mn);
-            if (l != l) f = 1.f;
-            if (lc != lc) fc = 1.f;
-            l = l * f + lc * fc;
-            m = mn;
-            alignas(16) float x[E];
-            *reinterpret_cast<Vec*>(x) = *reinterpret_cast<const Vec*>(rec + 2 * kTile + (size_t)rr * D + lane * E);
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = o[i] * f + x[i] * fc;
-        }
-        const int v = en.row0 + r, token = v / group;
-        T* dst = static_cast<T*>(a.out) +
-                 ((size_t)(a.q_offsets[en.seq] + token) * a.num_heads + kvh * group + (v - token * group)) * D + lane * E;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        alignas(8) T y[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = from_float<T>(o[i] * inv);
-        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
-        else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(y);
-    }
-}
-
 template <typename T, int D, int BS>
 cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
     const int group = a.num_heads / a.num_kv_heads, ctas = a.num_sms;
@@ -1212,7 +811,7 @@ cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUt
     ws.head = reinterpret_cast<PlanHead*>(base);
     ws.entries = reinterpret_cast<Entry*>(base + 256);
     ws.records = reinterpret_cast<float*>(base + 256 + align256((cap + 1) * sizeof(Entry)));
-    cudaError_t e = launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)(a.num_seqs + 1) * sizeof(int), stream, a, ws,
+    cudaError_t e = launch_pdl(attend_plan_kernel<AttendArgs, Fp8Rule>, dim3(1), dim3(kPlanThreads), (size_t)(a.num_seqs + 1) * sizeof(int), stream, a, ws,
                                (int)cap);
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(Smem<D>) + 1024;
@@ -1221,7 +820,7 @@ cudaError_t attend_typed(const AttendArgs& a, const CUtensorMap& kmap, const CUt
     e = launch_pdl(attend_fp8_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, kmap, vmap);
     if (e != cudaSuccess || ctas < 2) return e;
     // (a boundary's 256 rows on 8 CTAs, four rows a warp, measured when chosen: short mixed requests 88.7 us; 4 CTAs 95, 16 89.7, 32 93)
-    return launch_pdl(attend_join_kernel<T, D>, dim3((unsigned)(ctas - 1), 8), dim3(kJoinThreads), 0, stream, a, ws, ctas);
+    return launch_pdl(attend_join_kernel<T, D, AttendArgs, Fp8Rule>, dim3((unsigned)(ctas - 1), 8), dim3(kJoinThreads), 0, stream, a, ws, ctas);
 }
 
 }  // namespace

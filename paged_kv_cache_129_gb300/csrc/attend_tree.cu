@@ -1,83 +1,795 @@
-// Attention of the nodes of drafted trees over a paged 16-bit cache.
+// Attention of the nodes of drafted trees over a paged 16-bit cache, on tcgen05 tensor cores.
 //
 // Request b has the rows q_offsets[b] .. q_offsets[b + 1] - 1, n_b nodes whose keys and values are the last n_b of its L_b positions.  A
 // row sees the L_b - n_b positions before them, and node j where bit j of its words of tree_mask is set:
 //     out = sum softmax(scale q k_j) v_j over what it sees; zeros where that is nothing.
+//
+// Rows.  The g query heads of a kv head and the request's nodes form n_b * g rows (row v: node v / g, head v % g), cut into tiles of 128,
+// the M of the products; keys come in tiles of 128 positions, whose scores are made and used in halves of 64 columns: while the softmax
+// warps work on one half, the other half's products run.  A CTA has two streams of softmax warps:
+//   paired  two row tiles share every key tile;
+//   split   a single row tile (small trees, single tokens, the rest of a wide tree): the streams take alternate key tiles, and join their
+//           results at the end.
+// Work.  Equal shares of all units' key tiles per SM, see attend_units.cuh.
+// Operands.  K and V go from the cache's blocks straight into operand tiles, one bulk tensor copy per block: a block's rows as groups of
+// eight by panels of 64 elements, which is the order that both products read (K by rows, V by columns) with uniform strides.  A block
+// that is not there is copied from behind the pool, as zeros.
+// What a row does not see.  Its scores become -inf, its weights zeros; but 0 * NaN is NaN, so V must be finite there.  Blocks behind the
+// context are zeros; in the tiles that hold nodes or the context's end a warp clears the rows behind the end, and looks for infinities and
+// NaN in the nodes' V: these are taken out, noted, and put into the outputs of the rows that see them.
+// Numbers.  Scores, maxima, sums and the output accumulate in float32.  A weight is rounded to the cache's type for the second
+// product (half a step: bf16 2^-9 of it, as many bits as the output has; f16 2^-12, and 2^-25 of the reference below 2^-14).  The
+// reference of the exponents follows the true maximum by steps of 2^8 at least: rescaling the output in tensor memory is rare that way, and weights stay
+// below 2^8.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
+#include "attend_units.cuh"
 #include "pa_common.cuh"
+#include "pa_internal.h"
+#include "tcgen05.cuh"
 #include "tree_ops.h"
 
 namespace pa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kSoftmaxWarps = 8;  // four per stream
+constexpr int kIssueWarp = kSoftmaxWarps;  // two, one per stream
+constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1;
+constexpr int kThreads = (kCleanWarp + 1) * 32;
+constexpr int kCleanRing = 8;  // cleaned V tiles whose notes are kept, see Tile
 
-// A warp per (row, query head), a key at a time; maximum, sum and output in float32 registers.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attend_tree_kernel(const TreeAttendArgs a) {
-    griddep_wait();
-    griddep_launch_dependents();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, group = a.num_heads / a.num_kv_heads;
-    const int b = blockIdx.y;
-    const int lo = a.q_offsets[b], hi = a.q_offsets[b + 1], width = a.max_blocks * a.block_size;
-    int L = a.context_lens[b];
-    const bool run = is_run(lo, hi, a.num_tokens);
-    const int n = run ? hi - lo : 0;
-    if ((!run || L < n || L > width || n > 64 * a.mask_words) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrBadContext);
-    L = max(0, min(L, width));
-    const long long rows = (long long)n * a.num_heads;
-    for (long long x = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); x < rows; x += gridDim.x * (kThreads / 32)) {
-        const int t = lo + (int)(x / a.num_heads), h = (int)(x % a.num_heads), kvh = h / group;
-        const T* q = static_cast<const T*>(a.query) + ((long long)t * a.num_heads + h) * D + lane * E;
-        float qf[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) qf[i] = to_float(q[i]) * a.scale, o[i] = 0.f;
-        for (int p = 0; p < L; ++p) {
-            const int node = p - (L - n);
-            if (node >= 0 && (node >= 64 * a.mask_words || !(a.tree_mask[(long long)t * a.mask_words + node / 64] >> (node % 64) & 1)))
-                continue;
-            const int id = a.block_tables[(long long)b * a.max_blocks + p / a.block_size];
-            if (id < 0 || id >= a.num_blocks) {
-                if (lane == 0) atomicOr(a.err, kErrBadTable);
-                continue;
+struct TreeRule {
+    static constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 16;
+    static constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
+    static __device__ __forceinline__ int tiles(int L, int, int, int) { return max(1, (L + kTile - 1) / kTile); }
+    static __device__ __forceinline__ bool refuses(const TreeAttendArgs& a, int L, int n) { return L < n || n > 64 * a.mask_words; }
+};
+using Walk = UnitWalk<TreeRule>;
+
+// Sizes and places of the operand tiles.  A key tile is 16 groups of 8 positions; a group is D / 64 panels of 8 rows by 128 bytes,
+// swizzled (16-byte unit u of row r at u ^ r), which is how a block's copy leaves it.
+template <int D>
+struct Tile {
+    static constexpr int kOperand = kTile * D * 2;
+    static constexpr int kBuffers = D == 128 ? 5 : 10;            // K or V tiles in shared memory: 160 KB
+    static constexpr int kRing = D == 128 ? 8 : 16;               // slots of per-tile side data (places of blocks), see look_ahead()
+    static constexpr int kAhead = kRing - (kBuffers + 4) / 2;     // key tiles that look_ahead() may be ahead of the copies
+    static constexpr int kGroup = D * 16;                         // bytes of a group
+    // offset of 16 bytes (8 elements, unit u) of row r
+    static __device__ __forceinline__ int at(int r, int u) { return (r >> 3) * kGroup + (u >> 3) * 1024 + (r & 7) * 128 + (((u & 7) ^ (r & 7)) << 4); }
+};
+
+template <int D>
+struct Smem {
+    unsigned char q[2][Tile<D>::kOperand];
+    unsigned char kv[Tile<D>::kBuffers][Tile<D>::kOperand];
+    int place[Tile<D>::kRing][8];          // a tile's blocks: their first group of eight rows
+    unsigned masked[Tile<D>::kRing];       // which have an id outside the pool; bit 31: the tile's V is cleaned
+    float2 state[2][kTile];                // at the end of a split piece: both streams' m and l (sign bit: there is a note)
+    unsigned special[kCleanRing];          // whether a cleaned tile had infinities or NaN
+    uint64_t side_full[Tile<D>::kRing], copied[Tile<D>::kRing], q_full[2], kv_full[Tile<D>::kBuffers], kv_empty[Tile<D>::kBuffers];
+    uint64_t dirty_full[kCleanRing], clean_full[kCleanRing];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
+    uint32_t tmem;
+    volatile int abort;
+};
+static_assert(sizeof(Smem<128>) <= 227 * 1024, "fits an SM");
+
+// Notes of infinities and NaN, in the workspace (there is hardly ever one): bit set where an element was +inf or NaN, and where it was
+// -inf or NaN.  at: per cleaned tile and position; row: per row of a stream, the elements of its output that they reach.
+template <int D>
+struct Notes {
+    uint8_t at[kCleanRing][2][kTile][D / 8];
+    uint32_t row[2][2][kTile][D / 32];
+};
+
+// The order in which a piece's n key tiles go through the buffers.  Paired: K0 V0 K1 V1 ...  Split: K one tile ahead, K0 K1 V0 K2
+// V1 ... V(n-2) V(n-1), because the scores of a tile are issued before the output of the tile before it.
+struct Fill {
+    int tile;
+    bool value;
+};
+__device__ __forceinline__ Fill fill_of(bool paired, int n, int i) {
+    if (paired) return {i >> 1, (i & 1) != 0};
+    if (i == 2 * n - 1) return {n - 1, true};
+    if (i == 0) return {0, false};
+    return (i & 1) ? Fill{(i + 1) >> 1, false} : Fill{(i >> 1) - 1, true};
+}
+__device__ __forceinline__ int key_fill(bool paired, int tile) { return paired ? 2 * tile : tile == 0 ? 0 : 2 * tile - 1; }
+__device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
+    return paired ? 2 * tile + 1 : tile == n - 1 ? 2 * n - 1 : 2 * tile + 2;
+}
+
+// The first key tile whose V is cleaned: the one with the request's first node (or the context's end).
+__device__ __forceinline__ int first_cleaned(const Item& it) { return max(0, it.L - it.n) / kTile; }
+
+// The look-ahead warp: the places of block after block into the side ring, up to kAhead tiles before they are copied and across the ends
+// of pieces, so that the tables' latency is not waited for.
+// Side data of tile i sits in slot i % kRing, which was tile i - kRing's, last looked at by the softmax before P of that tile is there, so before
+// its V's buffer is released.  When K of tile j is copied, fill 2j - 1 at least (see fill_of()), fill 2j - 1 - kBuffers was released by both
+// streams, which release in order; V of tile g is fill 2g + 2 at most.  Tile i is looked at once K of tile i - kAhead is copied: with g = i - kRing,
+// 2 (i - kRing) + 2 <= 2 (i - kAhead) - 1 - kBuffers.
+template <int D, int BS>
+__device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+    constexpr int BLOCKS = kTile / BS, RING = Tile<D>::kRing, AHEAD = Tile<D>::kAhead;
+    static_assert(2 * (RING - AHEAD) >= Tile<D>::kBuffers + 3 && AHEAD > 1, "a slot's tile is done with when it is written again");
+    const int lane = threadIdx.x & 31;
+    const int behind = a.num_blocks * a.num_kv_heads * (BS / 8);  // the first group behind the pool: copied as zeros
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned tiles = 0;
+    while (walk.next(&p)) {
+        const Item it = item_of(a, p);
+        const int used = (it.L + BS - 1) / BS, cleaned = first_cleaned(it);
+        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
+        // lane j < BLOCKS has block j of a tile
+        auto wanted = [&](int tile) { return lane < BLOCKS && tile < p.end && tile * BLOCKS + lane < used; };
+        int id = wanted(p.begin) ? table[p.begin * BLOCKS + lane] : -1;
+        for (int tile = p.begin; tile < p.end; ++tile, ++tiles) {
+            const bool mine = wanted(tile), in = mine && id >= 0 && id < a.num_blocks;
+            if (mine && !in) atomicOr(a.err, kErrBadTable);
+            const int place = in ? (id * a.num_kv_heads + p.kvh) * (BS / 8) : behind;
+            id = wanted(tile + 1) ? table[(tile + 1) * BLOCKS + lane] : -1;
+            const unsigned masked = __ballot_sync(0xffffffffu, mine && !in) | (tile >= cleaned ? 1u << 31 : 0u);
+            if (tiles >= AHEAD) {
+                const unsigned before = tiles - AHEAD;
+                if (!warp_wait(&sm.copied[before % RING], (before / RING) & 1, a.err, &sm.abort)) return;
             }
-            const long long at = (((long long)id * a.num_kv_heads + kvh) * a.block_size + p % a.block_size) * D + lane * E;
-            const T *k = static_cast<const T*>(a.key_cache) + at, *v = static_cast<const T*>(a.value_cache) + at;
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) s = fmaf(qf[i], to_float(k[i]), s);
-#pragma unroll
-            for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : __expf(m - mn), e = s == -INFINITY ? 0.f : __expf(s - mn);
-            m = mn;
-            l = l * f + e;
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = o[i] * f + e * to_float(v[i]);
+            const int slot = tiles % RING;
+            if (lane < 8) sm.place[slot][lane] = place;
+            if (lane == 0) sm.masked[slot] = masked;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.side_full[slot]);
         }
-        T* out = static_cast<T*>(a.out) + ((long long)t * a.num_heads + h) * D + lane * E;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int i = 0; i < E; ++i) out[i] = from_float<T>(o[i] * inv);
     }
 }
 
+// One block of a kv head, K or V: box (64 elements, 8 rows, panels, groups) at group `place`.  One elected lane.
+__device__ __forceinline__ void copy_block(void* dst, const CUtensorMap* map, int place, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %2, %2, %3}], [%4];\n\t}" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(place), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The copy warp.  V that is cleaned arrives on a barrier of the cleaning warp's, which then says that the buffer is full.
+template <int D, int BS>
+__device__ __forceinline__ void copy_tiles(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, const CUtensorMap* kmap,
+                                           const CUtensorMap* vmap) {
+    constexpr int BLOCKS = kTile / BS, N = Tile<D>::kBuffers, RING = Tile<D>::kRing;
+    const int lane = threadIdx.x & 31;
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned fills = 0, tiles = 0, cleaned = 0, dirty = 0;  // dirty: buffers whose last fill is one that is cleaned
+    bool ok = true;
+    while (ok && walk.next(&p)) {
+        const int n = p.end - p.begin;
+#pragma unroll 1
+        for (int i = 0; i < 2 * n; ++i, ++fills) {
+            const Fill f = fill_of(p.paired, n, i);
+            const int buf = fills % N;
+            const unsigned tile = tiles + f.tile, side = tile % RING;
+            ok = f.value || warp_wait(&sm.side_full[side], (tile / RING) & 1, a.err, &sm.abort);
+            ok = ok && warp_wait(&sm.kv_empty[buf], ((fills / N) & 1) ^ 1, a.err, &sm.abort);
+            if (!ok) break;
+            const bool clean = f.value && (sm.masked[side] >> 31);
+            uint64_t* bar = clean ? &sm.dirty_full[cleaned % kCleanRing] : &sm.kv_full[buf];
+            dirty = (dirty & ~(1u << buf)) | ((unsigned)clean << buf);
+            cleaned += clean;
+            const int place = sm.place[side][lane & 7];
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, Tile<D>::kOperand);
+                if (!f.value) mbar_arrive(&sm.copied[side]);
+            }
+            __syncwarp();
+            const CUtensorMap* map = f.value ? vmap : kmap;
+#pragma unroll
+            for (int j = 0; j < BLOCKS; ++j)
+                copy_block(sm.kv[buf] + j * (BS * D * 2), map, __shfl_sync(0xffffffffu, place, j), bar);
+        }
+        tiles += n;
+    }
+    if (!ok) {  // copies still under way must land before the CTA's shared memory goes
+        int never = 0;
+        for (unsigned f = fills; f > 0 && f + N > fills; --f) {
+            const int buf = (f - 1) % N;
+            if (dirty >> buf & 1) {
+                --cleaned;
+                mbar_wait_bounded(&sm.dirty_full[cleaned % kCleanRing], (cleaned / kCleanRing) & 1, a.err, &never);
+            } else {
+                mbar_wait_bounded(&sm.kv_full[buf], ((f - 1) / N) & 1, a.err, &never);
+            }
+        }
+    }
+}
+
+// Per element of a word of two: bit 15 set where it is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    constexpr uint32_t kStep = std::is_same<T, __half>::value ? 0x0400u : 0x0080u;  // from the largest exponent to bit 15
+    return ((w & 0x7fff7fffu) + (kStep * 0x10001u)) & 0x80008000u;
+}
+
+// The cleaning warp: V tiles from the first one with a node (or the context's end) on.  Rows between the context's end and its block's
+// become zeros (what lies there may be anything); infinities and NaN of nodes too, with notes.
+// Slots of dirty_full, clean_full, special and the notes are used in turn by cleaned tiles.  Slot c % kCleanRing is free when V of cleaned
+// tile c arrives: its buffer, and those of all fills kBuffers <= 10 or more before it, were released, so the softmax of tiles
+// c - 6 and older is done.  A softmax warp waits for clean_full only of its own tiles; the phase before the one that is meant is over when it
+// does: K of the tile has arrived then, so fills kBuffers or more before that one were released, among them V of cleaned tile
+// c - kCleanRing, at least 2 kCleanRing - 3 >= 10 before.
+template <typename T, int D, int BS>
+__device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, Notes<D>& notes) {
+    constexpr int N = Tile<D>::kBuffers, UNITS = D / 8, RPP = 32 / UNITS;  // rows per pass
+    static_assert(2 * kCleanRing - 3 >= N && kCleanRing >= 7, "see above");
+    const int lane = threadIdx.x & 31, u = lane % UNITS, sub = lane / UNITS;
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned fills = 0, cleaned = 0;
+    while (walk.next(&p)) {
+        const Item it = item_of(a, p);
+        const int n = p.end - p.begin, base = it.L - it.n;
+        for (int tile = max(p.begin, first_cleaned(it)); tile < p.end; ++tile, ++cleaned) {
+            const unsigned fill = fills + value_fill(p.paired, n, tile - p.begin), slot = cleaned % kCleanRing;
+            unsigned char* v = sm.kv[fill % N];
+            if (!warp_wait(&sm.dirty_full[slot], (cleaned / kCleanRing) & 1, a.err, &sm.abort)) return;
+            const int p0 = tile * kTile, end = min(kTile, it.L - p0), first = max(0, base - p0);
+            const int block_end = min(kTile, (end + BS - 1) / BS * BS);
+            for (int r = end + sub; r < block_end; r += RPP) *reinterpret_cast<uint4*>(v + Tile<D>::at(r, u)) = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t found = 0;
+#pragma unroll 4
+            for (int r = first + sub; r < end; r += RPP) {
+                const uint4 x = *reinterpret_cast<const uint4*>(v + Tile<D>::at(r, u));
+                found |= not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w);
+            }
+            const bool any = __any_sync(0xffffffffu, found != 0);
+            if (any) {
+                constexpr uint32_t kMantissa = std::is_same<T, __half>::value ? 0x03ffu : 0x007fu;
+                for (int r = first + sub; r < end; r += RPP) {
+                    uint4* at = reinterpret_cast<uint4*>(v + Tile<D>::at(r, u));
+                    uint32_t w[4] = {at->x, at->y, at->z, at->w}, plus = 0, minus = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t x = w[i / 2] >> (16 * (i & 1));
+                        if (!(not_finite<T>(x & 0xffffu))) continue;
+                        const bool nan = (x & kMantissa) != 0;
+                        if (nan || !(x & 0x8000u)) plus |= 1u << i;
+                        if (nan || (x & 0x8000u)) minus |= 1u << i;
+                        w[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                    }
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    notes.at[slot][0][r][u] = (uint8_t)plus;
+                    notes.at[slot][1][r][u] = (uint8_t)minus;
+                }
+            }
+            if (lane == 0) sm.special[slot] = any;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.kv_full[fill % N]);
+                mbar_arrive(&sm.clean_full[slot]);
+            }
+        }
+        fills += 2 * n;
+    }
+}
+
+// One warp per stream issues its products; while one waits, the other's keep the tensor cores busy.  Job j of a piece is a
+// score tile of stream j % 2, in two halves of 64 columns (64 positions): a half's scores are issued right behind the output of the
+// same half of the stream's previous job, which has then read the P that they overwrite, and are ready while the softmax warps are
+// still at the other half.
+// A buffer is free after two arrivals, one from either stream: by its products' commit, or, of a tile that is the other stream's, when it is
+// passed.  A wait tells a phase of a barrier from the one before it alone: so every stream takes the fills in order and waits for each.
 template <typename T, int D>
-cudaError_t attend_typed(const TreeAttendArgs& a, cudaStream_t stream) {
-    const long long most = ((long long)a.num_tokens * a.num_heads + 7) / 8;  // of one request
-    return launch_pdl(attend_tree_kernel<T, D>, dim3((unsigned)std::min(most, 128ll), (unsigned)a.num_seqs), dim3(kThreads), 0, stream, a);
+__device__ __forceinline__ void issue_products(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, int t) {
+    constexpr int N = Tile<D>::kBuffers;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    volatile int* abort = &sm.abort;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
+    const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), k0 = desc_of(smem_addr(sm.kv[0]), 16, Tile<D>::kGroup),
+                   v0 = desc_of(smem_addr(sm.kv[0]), 1024, Tile<D>::kGroup);
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    Piece p;
+    unsigned fill = 0, pieces = 0, steps = 0;  // fill: the next one that this stream has to take
+    while (walk.next(&p)) {
+        const int n = p.end - p.begin, jobs = n * (p.paired ? 2 : 1);
+        const unsigned fills = fill;
+        auto pass = [&](unsigned to) {
+            for (; fill < to; ++fill) {
+                if (!warp_wait(&sm.kv_full[fill % N], (fill / N) & 1, a.err, abort)) return false;
+                if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.kv_empty[fill % N]);
+            }
+            return true;
+        };
+        // unit u: half u % 2 of the stream's job u / 2
+        const int units = 2 * ((jobs + 1 - t) / 2);
+#pragma unroll 1
+        for (int u = -2; u < units; ++u) {
+            const int half = u & 1;
+            if (u >= 0) {
+                const int tile = p.paired ? u >> 1 : u - half + t;
+                const unsigned f = fills + value_fill(p.paired, n, tile), buf = f % N;
+                if (half == 0 && !(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
+                if (!warp_wait(&sm.p_full[t][half], steps & 1, a.err, abort)) return;
+                tc_fence_after();
+                const uint64_t vd = v0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ts(o_at, s_at + 64 * half + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), u > 0 || k > 0);
+                tc_commit(&sm.pv_done[t][half]);
+                if (half == 0) fill = f + 1;  // (released behind the other half)
+                if (half == 1) {
+                    tc_commit(&sm.kv_empty[buf]);
+                    ++steps;
+                }
+                if (u == units - 1) tc_commit(&sm.o_full[t]);
+            }
+            const int next = u + 2;
+            if (next < units) {
+                const int tile = p.paired ? next >> 1 : next - half + t;
+                const unsigned f = fills + key_fill(p.paired, tile), buf = f % N;
+                if (half == 0 && !(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
+                if (next == 0 && !warp_wait(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
+                tc_fence_after();
+                const uint64_t kd = k0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(s_at + 64 * half, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4),
+                           idesc_of(kTile / 2, false, kBf16), k > 0);
+                if (half == 0) fill = f + 1;
+                if (half == 1) tc_commit(&sm.kv_empty[buf]);
+                tc_commit(&sm.s_full[t][half]);
+            }
+        }
+        if (!pass(fills + 2 * n)) return;
+    }
+}
+
+// A warp's 32 query rows into the swizzled tile; row_at: where this lane's row begins (live: if it exists).  D / 8 lanes load a row together.
+template <typename T, int D>
+__device__ __forceinline__ void stage_query(const T* query, size_t row_at, bool live, bool negate, unsigned char* tile, int row0) {
+    constexpr int LPR = D / 8, RPS = 32 / LPR, BATCH = 8;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, i = lane % LPR;
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
+    const uint32_t flip = negate ? 0x80008000u : 0u;
+#pragma unroll 1
+    for (int b = 0; b < 32; b += BATCH * RPS) {
+        uint4 raw[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)  // (rows that do not exist read the first one: a branch would wait for each load)
+            raw[k] = *reinterpret_cast<const uint4*>(query + __shfl_sync(0xffffffffu, row_at, b + k * RPS + sub) + 8 * i);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int r = b + k * RPS + sub, row = row0 + r;
+            const bool there = alive >> r & 1;
+            *reinterpret_cast<uint4*>(tile + row * 128 + (i / 8) * kPanel + (((i & 7) ^ (row & 7)) << 4)) =
+                there ? make_uint4(raw[k].x ^ flip, raw[k].y ^ flip, raw[k].z ^ flip, raw[k].w ^ flip) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
+// Which of the 64 positions from `at` on a row sees: those before the nodes (base), and its nodes; less the blocks in masked.
+template <int BS>
+__device__ __forceinline__ uint64_t seen_from(const uint64_t* words, int num_words, int at, int base, int n, unsigned masked) {
+    auto word = [&](int w) {
+        const int left = n - 64 * w;
+        return w >= num_words || left <= 0 ? 0ull : words[w] & (left >= 64 ? ~0ull : (1ull << left) - 1);
+    };
+    const int node = at - base;
+    uint64_t seen;
+    if (node <= -64) {
+        seen = ~0ull;
+    } else if (node < 0) {
+        seen = (word(0) << -node) | ((1ull << -node) - 1);
+    } else {
+        seen = word(node >> 6) >> (node & 63);
+        if (node & 63) seen |= word((node >> 6) + 1) << (64 - (node & 63));
+    }
+    constexpr uint64_t kBlock = BS == 16 ? 0xffffull : 0xffffffffull;
+#pragma unroll
+    for (int k = 0; k < 64 / BS; ++k)
+        if (masked >> k & 1) seen &= ~(kBlock << (k * BS));
+    return seen;
+}
+
+__device__ __forceinline__ float row_max(const uint32_t (&s)[64]) {
+    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
+#pragma unroll
+    for (int i = 0; i < 64; i += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = fmaxf(x[j], fmaxf(__uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1])));
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t round2(float2 x);
+template <>
+__device__ __forceinline__ uint32_t round2<__half>(float2 x) {
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float2 x) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// P of 64 scores: exp2(score * factor - mu), rounded, over the scores in tensor memory; returns the sum of the exponentials.
+template <typename T>
+__device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, float factor, float mu) {
+    float2 sum = make_float2(0.f, 0.f);
+    const float2 f = make_float2(factor, factor), m = make_float2(-mu, -mu);
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+        for (int i = c; i < c + 32; i += 2) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f, m);
+            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum = add2(sum, e);
+            s[i / 2] = round2<T>(e);
+        }
+        tmem_st16(s_at + c / 2, *reinterpret_cast<uint32_t(*)[16]>(&s[c / 2]));
+    }
+    return sum.x + sum.y;
+}
+
+// A softmax warp: 32 rows of a stream's row tile, one per lane.
+template <typename T, int D, int BS>
+__device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, Notes<D>& notes) {
+    constexpr int RING = Tile<D>::kRing;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
+    volatile int* abort = &sm.abort;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = sm.tmem + lanes + t * kTile, o_at = sm.tmem + lanes + 2 * kTile + t * D;
+    const uint32_t other_o_at = sm.tmem + lanes + 2 * kTile + (t ^ 1) * D;
+    // (kept above zero, so that masked scores stay -inf)
+    const float factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-38f);
+    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    unsigned pieces = 0, steps = 0, joins = 0, tiles_before = 0, cleaned_before = 0;  // so far
+    // what the result of a piece needs; it is written after the next piece's queries are staged, which waits for nothing
+    struct Result {
+        size_t row_at;
+        float* rec;
+        bool live, warp_live, cut, join;
+    } res{};
+    float m = -INFINITY, l = 0.f;  // the row's reference of exponents, the sum of its exponentials
+    bool noted = false, pending = false;
+#pragma unroll 1
+    for (;;) {
+        Piece p;
+        Item it{};
+        int n = 0, my_jobs = 0, base = 0, first_clean = 0;
+        const uint64_t* words = nullptr;
+        Result now{};
+        const bool have = walk.next(&p);
+        if (have) {
+            it = item_of(a, p);
+            n = p.end - p.begin;
+            my_jobs = (it.jobs + 1 - t) / 2;
+            base = it.L - it.n;
+            first_clean = max(p.begin, first_cleaned(it));
+            if (my_jobs == 0 && !pending) {  // a single tile in a split piece is stream 0's
+                tiles_before += n;
+                cleaned_before += max(0, p.end - first_clean);
+                continue;
+            }
+            const int first = p.row0 + (p.paired ? t * kTile : 0), v = first + r;  // row of the request
+            const int token = v / it.group;
+            now.live = v < it.rows;
+            now.warp_live = first + (warp & 3) * 32 < it.rows;
+            now.cut = p.begin > 0 || p.end < p.tiles;
+            now.join = !p.paired && it.jobs > 1;
+            now.rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
+            now.row_at = now.live ? ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D : 0;
+            words = reinterpret_cast<const uint64_t*>(a.tree_mask) + (now.live ? (size_t)(it.first_token + token) * a.mask_words : 0);
+            if (my_jobs > 0) {
+                // the stream's last scores were waited for, so its query tile is free
+                stage_query<T, D>(static_cast<const T*>(a.query), now.row_at, now.live, a.scale < 0.f, sm.q[t], (warp & 3) * 32);
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.q_full[t]);
+            }
+        }
+
+        if (pending) {  // the previous piece's result
+            if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+            tc_fence_after();
+            ++pieces;
+            float f0 = 1.f, f1 = 0.f;  // factors of this stream's output and of the other's
+            uint32_t notes_from = noted ? 1u << t : 0u;
+            if (res.join) {  // both streams have a part of the same rows, in the same lanes of tensor memory
+                sm.state[t][r] = make_float2(m, __uint_as_float((__float_as_uint(l) & 0x7fffffffu) | (noted ? 0x80000000u : 0u)));
+                tc_fence_before();
+                mbar_arrive(&sm.join_full);
+                if (!warp_wait(&sm.join_full, joins & 1, a.err, abort)) return;
+                tc_fence_after();
+                const float2 o = sm.state[t ^ 1][r];
+                const float ol = __uint_as_float(__float_as_uint(o.y) & 0x7fffffffu);
+                const float mn = fmaxf(m, o.x);
+                // a state without a maximum is empty, unless its sum is NaN
+                f0 = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2_approx(m - mn);
+                f1 = o.x == -INFINITY ? (ol != ol ? 1.f : 0.f) : exp2_approx(o.x - mn);
+                l = l * f0 + ol * f1;
+                m = mn;
+                if (__float_as_uint(o.y) >> 31) notes_from |= 2u >> t;
+            }
+            if (res.warp_live) {
+                const float inv = res.cut ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                const int c0 = res.join ? t * (D / 2) : 0, c1 = res.join ? c0 + D / 2 : D;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    uint32_t s[32];
+                    tmem_ld32(o_at + c, s);
+                    tc_wait_ld(s);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
+                    if (res.join) {
+                        uint32_t o[32];
+                        tmem_ld32(other_o_at + c, o);
+                        tc_wait_ld(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k])));
+                    }
+                    if (notes_from) {
+                        uint32_t plus = 0, minus = 0;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (notes_from >> k & 1) {
+                                plus |= notes.row[k][0][r][c / 32];
+                                minus |= notes.row[k][1][r][c / 32];
+                            }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if ((plus | minus) >> k & 1) s[k] = !(minus >> k & 1) ? 0x7f800000u : !(plus >> k & 1) ? 0xff800000u : 0x7fc00000u;
+                    }
+                    if (res.live && res.cut) {
+                        uint4* d = reinterpret_cast<uint4*>(res.rec + 2 * kTile + (size_t)r * D + c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[k] = make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
+                    } else if (res.live) {
+                        uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + res.row_at + c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                y[i] = round2<T>(make_float2(__uint_as_float(s[8 * k + 2 * i]) * inv, __uint_as_float(s[8 * k + 2 * i + 1]) * inv));
+                            d[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                }
+                if (res.cut && res.live && c0 == 0) {
+                    res.rec[r] = m;
+                    res.rec[kTile + r] = l;
+                }
+            }
+            tc_fence_before();
+            if (res.join) {  // neither stream's output is written again before both have read it
+                mbar_arrive(&sm.join_done);
+                if (!warp_wait(&sm.join_done, joins & 1, a.err, abort)) return;
+                ++joins;
+            }
+            pending = false;
+        }
+        if (!have) return;
+        if (my_jobs == 0) {
+            tiles_before += n;
+            cleaned_before += max(0, p.end - first_clean);
+            continue;
+        }
+
+        res = now;
+        pending = true;
+        m = -INFINITY;
+        l = 0.f;
+        noted = false;
+#pragma unroll 1
+        for (int step = 0; step < my_jobs; ++step, ++steps) {
+            const int local = p.paired ? step : 2 * step + t, tile = p.begin + local;
+            const int p0 = tile * kTile, slot = (tiles_before + local) % RING;
+            uint64_t seen[2] = {~0ull, ~0ull};
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (!warp_wait(&sm.s_full[t][half], steps & 1, a.err, abort)) return;
+                tc_fence_after();
+                if (!now.warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
+                    if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
+                    continue;
+                }
+                const uint32_t at = s_at + 64 * half;
+                uint32_t s[64];
+                tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                const unsigned masked = sm.masked[slot];
+                tc_wait_ld(s);
+                if (masked) {  // a block that is not there, or (bit 31) a tile with nodes or the context's end
+                    const uint64_t mine = now.live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, it.n,
+                                                                  (masked & 0xffu) >> (half * (64 / BS)))
+                                                   : 0ull;
+                    if (half == 0) seen[0] = mine;
+                    else seen[1] = mine;
+                    const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (!(lo >> i & 1)) s[i] = 0xff800000u;
+                        if (!(hi >> i & 1)) s[32 + i] = 0xff800000u;
+                    }
+                }
+                const float top = row_max(s) * factor;
+                if (step == 0 && half == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                    // The output so far has to be there.  (Its barrier is waited for only here: the phase before the one that is
+                    // meant is over, because this half's scores were issued after the output of the half before the last.)
+                    const unsigned last = half ? steps : steps - 1;
+                    if (!warp_wait(&sm.pv_done[t][half ^ 1], last & 1, a.err, abort)) return;
+                    tc_fence_after();
+                    const float mn = fmaxf(m, top);
+                    const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                    l *= f;
+                    m = mn;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + c, o);
+                        tc_wait_ld(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st16(o_at + c, o);
+                    }
+                }
+                l += row_exp<T>(s, at, factor, m == -INFINITY ? 0.f : m);
+                if (half == 1 && (masked >> 31)) {  // a tile whose V was cleaned
+                    const unsigned c = cleaned_before + (tile - first_clean), note = c % kCleanRing;
+                    if (!warp_wait(&sm.clean_full[note], (c / kCleanRing) & 1, a.err, abort)) return;
+                    if (sm.special[note]) {
+                        const int from = max(0, base - p0);
+#pragma unroll 1
+                        for (int sign = 0; sign < 2; ++sign) {
+#pragma unroll 1
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint32_t bits = noted ? notes.row[t][sign][r][i] : 0u;
+#pragma unroll 1
+                                for (int k = from; k < kTile; ++k)
+                                    if (seen[k >> 6] >> (k & 63) & 1) bits |= *reinterpret_cast<const uint32_t*>(&notes.at[note][sign][k][4 * i]);
+                                notes.row[t][sign][r][i] = bits;
+                            }
+                        }
+                        noted = true;
+                    }
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
+            }
+        }
+        tiles_before += n;
+        cleaned_before += max(0, p.end - first_clean);
+    }
+}
+
+template <typename T, int D, int BS>
+__global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAttendArgs a, const Workspace ws, Notes<D>* all_notes,
+                                                                  const __grid_constant__ CUtensorMap kmap,
+                                                                  const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) unsigned char raw_smem[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw_smem);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 128);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm.s_full[i][h], 1);
+                mbar_init(&sm.p_full[i][h], 4);
+                mbar_init(&sm.pv_done[i][h], 1);
+            }
+            mbar_init(&sm.o_full[i], 1);
+        }
+        for (int i = 0; i < Tile<D>::kRing; ++i) {
+            mbar_init(&sm.side_full[i], 1);
+            mbar_init(&sm.copied[i], 1);
+        }
+        for (int i = 0; i < Tile<D>::kBuffers; ++i) {
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 2);
+        }
+        for (int i = 0; i < kCleanRing; ++i) {
+            mbar_init(&sm.dirty_full[i], 1);
+            mbar_init(&sm.clean_full[i], 1);
+        }
+        mbar_init(&sm.join_full, kSoftmaxWarps * 32);
+        mbar_init(&sm.join_done, kSoftmaxWarps * 32);
+        mbar_init(&sm.drain[0], 1);
+        mbar_init(&sm.drain[1], 1);
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kIssueWarp) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    Notes<D>& notes = all_notes[blockIdx.x];
+    if (warp < kSoftmaxWarps) {
+        softmax_rows<T, D, BS>(a, ws, sm, notes);
+    } else if (warp == kCopyWarp) {
+        copy_tiles<D, BS>(a, ws, sm, &kmap, &vmap);
+    } else if (warp == kLookWarp) {
+        look_ahead<D, BS>(a, ws, sm);
+    } else if (warp == kCleanWarp) {
+        clean_tiles<T, D, BS>(a, ws, sm, notes);
+    } else {
+        const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
+        issue_products<T, D>(a, ws, sm, t);
+        if (__any_sync(0xffffffffu, sm.abort)) {  // products still in flight read shared and tensor memory
+            int never = 0;
+            tc_commit(&sm.drain[t]);
+            mbar_wait_bounded(&sm.drain[t], 0, a.err, &never);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kIssueWarp) tmem_free(sm.tmem, 512);
+}
+
+// Places in the workspace of a call.
+template <int D>
+size_t lay_out(int num_sms, size_t cap, char* base, Workspace* ws, Notes<D>** notes) {
+    const size_t records = 256 + align256((cap + 1) * sizeof(Entry)), at = records + (size_t)num_sms * 4 * record_floats(D) * sizeof(float);
+    if (ws) {
+        ws->head = reinterpret_cast<PlanHead*>(base);
+        ws->entries = reinterpret_cast<Entry*>(base + 256);
+        ws->records = reinterpret_cast<float*>(base + records);
+        *notes = reinterpret_cast<Notes<D>*>(base + at);
+    }
+    return at + (size_t)num_sms * sizeof(Notes<D>);
+}
+
+template <typename T, int D, int BS>
+cudaError_t attend_typed(const TreeAttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+    const int group = a.num_heads / a.num_kv_heads, ctas = a.num_sms;
+    const size_t cap = max_entries(a.num_seqs, a.num_tokens, group);
+    Workspace ws;
+    Notes<D>* notes;
+    lay_out<D>(a.num_sms, cap, static_cast<char*>(a.workspace), &ws, &notes);
+    cudaError_t e = launch_pdl(attend_plan_kernel<TreeAttendArgs, TreeRule>, dim3(1), dim3(kPlanThreads),
+                               (size_t)(a.num_seqs + 1) * sizeof(int), stream, a, ws, (int)cap);
+    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(Smem<D>);
+    e = cudaFuncSetAttribute(attend_tree_kernel<T, D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attend_tree_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, notes, kmap, vmap);
+    if (e != cudaSuccess || ctas < 2) return e;
+    return launch_pdl(attend_join_kernel<T, D, TreeAttendArgs, TreeRule>, dim3((unsigned)(ctas - 1), 8), dim3(kJoinThreads), 0, stream, a, ws,
+                      ctas);
 }
 
 }  // namespace
 
-size_t attend_tree_workspace_bytes(int, int, int, int, int, int) { return 0; }
+size_t attend_tree_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim) {
+    const size_t cap = max_entries(num_seqs, num_tokens, num_heads / num_kv_heads);
+    return head_dim == 64 ? lay_out<64>(num_sms, cap, nullptr, nullptr, nullptr) : lay_out<128>(num_sms, cap, nullptr, nullptr, nullptr);
+}
 
-cudaError_t attend_tree_launch(const TreeAttendArgs& a, cudaStream_t stream) {
-    if (a.dtype == 1) return a.head_dim == 64 ? attend_typed<__half, 64>(a, stream) : attend_typed<__half, 128>(a, stream);
-    return a.head_dim == 64 ? attend_typed<__nv_bfloat16, 64>(a, stream) : attend_typed<__nv_bfloat16, 128>(a, stream);
+cudaError_t attend_tree_launch(const TreeAttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+    const int pick = (a.dtype == 1 ? 4 : 0) + (a.head_dim == 64 ? 2 : 0) + (a.block_size == 32 ? 1 : 0);
+    switch (pick) {
+        case 0: return attend_typed<__nv_bfloat16, 128, 16>(a, kmap, vmap, stream);
+        case 1: return attend_typed<__nv_bfloat16, 128, 32>(a, kmap, vmap, stream);
+        case 2: return attend_typed<__nv_bfloat16, 64, 16>(a, kmap, vmap, stream);
+        case 3: return attend_typed<__nv_bfloat16, 64, 32>(a, kmap, vmap, stream);
+        case 4: return attend_typed<__half, 128, 16>(a, kmap, vmap, stream);
+        case 5: return attend_typed<__half, 128, 32>(a, kmap, vmap, stream);
+        case 6: return attend_typed<__half, 64, 16>(a, kmap, vmap, stream);
+        default: return attend_typed<__half, 64, 32>(a, kmap, vmap, stream);
+    }
 }
 
 }  // namespace pa

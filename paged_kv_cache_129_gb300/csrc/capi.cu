@@ -19,6 +19,7 @@
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "step_ops.h"
+#include "tree_ops.h"
 
 // One error word per device, set by kernels with atomicOr (see pa_common.cuh).
 __device__ unsigned int g_pa_device_error_word;
@@ -441,6 +442,21 @@ int record_map(CUtensorMap* map, const void* base, long long records, int record
     if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     entries[next] = Entry{base, records, record_bytes, *map};
     next = (next + 1) % kEntries;
+    return PA_OK;
+}
+
+int group_map(CUtensorMap* map, const void* base, long long groups, int block_size, int head_dim) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t row = (cuuint64_t)head_dim * 2;
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)head_dim / 64, (cuuint64_t)groups};
+    cuuint64_t strides[3] = {row, 128, 8 * row};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)head_dim / 64, (cuuint32_t)block_size / 8};
+    cuuint32_t estrides[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, estrides,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     return PA_OK;
 }
 

@@ -184,7 +184,12 @@ int pa_attend_tree(void* out, const void* query, const void* key_cache, const vo
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return fail(PA_ERR_INVALID_ARG, "pa_attend_tree: needs a 256-byte aligned workspace of %zu bytes (%zu given)", need,
                     workspace ? workspace_bytes : (size_t)0);
-    const cudaError_t e = attend_tree_launch(a, static_cast<cudaStream_t>(stream));
+    const long long groups = (long long)num_blocks * num_kv_heads * (block_size / 8);
+    CUtensorMap kmap, vmap;
+    st = group_map(&kmap, key_cache, groups, block_size, head_dim);
+    if (st == PA_OK) st = group_map(&vmap, value_cache, groups, block_size, head_dim);
+    if (st != PA_OK) return st;
+    const cudaError_t e = attend_tree_launch(a, kmap, vmap, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : launch_failed(e, "pa_attend_tree");
 }
 

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kv_ops.h"
@@ -94,6 +95,11 @@ cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, c
 cudaError_t norm_rope_write_kv_launch(const NormRopeArgs& a, cudaStream_t stream);
 // Scratch of one attend_tree call.
 size_t attend_tree_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim);
-cudaError_t attend_tree_launch(const TreeAttendArgs& a, cudaStream_t stream);
+// kmap, vmap: group_map()s of K and V.
+cudaError_t attend_tree_launch(const TreeAttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream);
+
+// A 16-bit cache as groups of eight rows, in panels of 64 elements: what one copy brings of a block (of a kv head) is a box of
+// block_size / 8 groups, each panel with the 128-byte swizzle.  PA_OK or a failure with its message.
+int group_map(CUtensorMap* map, const void* base, long long groups, int block_size, int head_dim);
 
 }  // namespace pa
