@@ -37,9 +37,9 @@ namespace {
 
 constexpr int kSoftmaxWarps = 8;  // four per stream
 constexpr int kIssueWarp = kSoftmaxWarps;  // two, one per stream
-constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1;
-constexpr int kThreads = (kCleanWarp + 1) * 32;
-constexpr int kCleanRing = 8;  // cleaned V tiles whose notes are kept, see Tile
+constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1, kQueryWarp = kCleanWarp + 1;
+constexpr int kThreads = (kQueryWarp + 1) * 32;
+constexpr int kPieces = 4;  // pieces of the share that the roles may be apart
 
 struct TreeRule {
     static constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 16;
@@ -57,22 +57,31 @@ struct Tile {
     static constexpr int kBuffers = D == 128 ? 5 : 10;            // K or V tiles in shared memory: 160 KB
     static constexpr int kRing = D == 128 ? 8 : 16;               // slots of per-tile side data (places of blocks), see look_ahead()
     static constexpr int kAhead = kRing - (kBuffers + 4) / 2;     // key tiles that look_ahead() may be ahead of the copies
+    static constexpr int kCleanRing = D == 128 ? 4 : 8;           // cleaned V tiles whose notes are kept, see clean_tiles()
     static constexpr int kGroup = D * 16;                         // bytes of a group
     // offset of 16 bytes (8 elements, unit u) of row r
     static __device__ __forceinline__ int at(int r, int u) { return (r >> 3) * kGroup + (u >> 3) * 1024 + (r & 7) * 128 + (((u & 7) ^ (r & 7)) << 4); }
 };
 
+// What a piece of the share is to every role; begin == end behind the last one.
+struct Job {
+    int L, n, first_token;  // length, nodes, row of the first node
+    int row0, kvh, tiles, begin, end, paired;
+};
+
 template <int D>
 struct Smem {
-    unsigned char q[2][Tile<D>::kOperand];
+    unsigned char q[2][Tile<D>::kOperand];  // row tiles, used in turn: of a split piece one, of a pair both
     unsigned char kv[Tile<D>::kBuffers][Tile<D>::kOperand];
+    float2 state[2][kTile];                // at the end of a split piece: both streams' m and l (sign bit: there is a note)
     int place[Tile<D>::kRing][8];          // a tile's blocks: their first group of eight rows
     unsigned masked[Tile<D>::kRing];       // which have an id outside the pool; bit 31: the tile's V is cleaned
-    float2 state[2][kTile];                // at the end of a split piece: both streams' m and l (sign bit: there is a note)
-    unsigned special[kCleanRing];          // whether a cleaned tile had infinities or NaN
-    uint64_t side_full[Tile<D>::kRing], copied[Tile<D>::kRing], q_full[2], kv_full[Tile<D>::kBuffers], kv_empty[Tile<D>::kBuffers];
-    uint64_t dirty_full[kCleanRing], clean_full[kCleanRing];
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
+    unsigned special[Tile<D>::kCleanRing]; // whether a cleaned tile had infinities or NaN
+    Job jobs[kPieces];
+    uint64_t job_full[kPieces], job_free[kPieces], side_full[Tile<D>::kRing], copied[Tile<D>::kRing];
+    uint64_t q_full[2], q_free[2], kv_full[Tile<D>::kBuffers], kv_empty[Tile<D>::kBuffers];
+    uint64_t dirty_full[Tile<D>::kCleanRing], clean_full[Tile<D>::kCleanRing];
+    uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -82,7 +91,7 @@ static_assert(sizeof(Smem<128>) <= 227 * 1024, "fits an SM");
 // -inf or NaN.  at: per cleaned tile and position; row: per row of a stream, the elements of its output that they reach.
 template <int D>
 struct Notes {
-    uint8_t at[kCleanRing][2][kTile][D / 8];
+    uint8_t at[Tile<D>::kCleanRing][2][kTile][D / 8];
     uint32_t row[2][2][kTile][D / 32];
 };
 
@@ -104,7 +113,24 @@ __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
 }
 
 // The first key tile whose V is cleaned: the one with the request's first node (or the context's end).
-__device__ __forceinline__ int first_cleaned(const Item& it) { return max(0, it.L - it.n) / kTile; }
+__device__ __forceinline__ int first_cleaned(const Job& j) { return max(0, j.L - j.n) / kTile; }
+
+// Tensor memory: per stream 64 columns of scores (of one half), then twice 32 of weights P; behind both streams', D of output each.
+__device__ __forceinline__ uint32_t scores_at(uint32_t tmem, int t) { return tmem + t * 128; }
+__device__ __forceinline__ uint32_t weights_at(uint32_t tmem, int t, int half) { return tmem + t * 128 + 64 + 32 * half; }
+template <int D>
+__device__ __forceinline__ uint32_t output_at(uint32_t tmem, int t) { return tmem + 256 + t * D; }
+
+// Piece i of the share, for a warp of any role but the look-ahead's, which writes them; false if a wait gave up.
+constexpr int kReaders = kThreads / 32 - 1;
+template <int D>
+__device__ __forceinline__ bool read_job(Smem<D>& sm, unsigned i, Job* job, unsigned* err) {
+    if (!warp_wait(&sm.job_full[i % kPieces], (i / kPieces) & 1, err, &sm.abort)) return false;
+    *job = sm.jobs[i % kPieces];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.job_free[i % kPieces]);
+    return true;
+}
 
 // The look-ahead warp: the places of block after block into the side ring, up to kAhead tiles before they are copied and across the ends
 // of pieces, so that the tables' latency is not waited for.
@@ -119,11 +145,23 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, const Worksp
     const int lane = threadIdx.x & 31;
     const int behind = a.num_blocks * a.num_kv_heads * (BS / 8);  // the first group behind the pool: copied as zeros
     Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
-    Piece p;
     unsigned tiles = 0;
-    while (walk.next(&p)) {
-        const Item it = item_of(a, p);
-        const int used = (it.L + BS - 1) / BS, cleaned = first_cleaned(it);
+#pragma unroll 1
+    for (unsigned i = 0;; ++i) {
+        Piece p{};
+        Job j{};
+        const bool have = walk.next(&p);
+        if (have) {
+            const Item it = item_of(a, p);
+            j = Job{it.L, it.n, it.first_token, p.row0, p.kvh, p.tiles, p.begin, p.end, p.paired};
+        }
+        if (i >= kPieces && !warp_wait(&sm.job_free[i % kPieces], (i / kPieces - 1) & 1, a.err, &sm.abort)) return;
+        if (lane == 0) {
+            sm.jobs[i % kPieces] = j;
+            mbar_arrive(&sm.job_full[i % kPieces]);
+        }
+        if (!have) return;
+        const int used = (j.L + BS - 1) / BS, cleaned = first_cleaned(j);
         const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
         // lane j < BLOCKS has block j of a tile
         auto wanted = [&](int tile) { return lane < BLOCKS && tile < p.end && tile * BLOCKS + lane < used; };
@@ -159,19 +197,20 @@ __device__ __forceinline__ void copy_block(void* dst, const CUtensorMap* map, in
 
 // The copy warp.  V that is cleaned arrives on a barrier of the cleaning warp's, which then says that the buffer is full.
 template <int D, int BS>
-__device__ __forceinline__ void copy_tiles(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, const CUtensorMap* kmap,
-                                           const CUtensorMap* vmap) {
-    constexpr int BLOCKS = kTile / BS, N = Tile<D>::kBuffers, RING = Tile<D>::kRing;
+__device__ __forceinline__ void copy_tiles(const TreeAttendArgs& a, Smem<D>& sm, const CUtensorMap* kmap, const CUtensorMap* vmap) {
+    constexpr int BLOCKS = kTile / BS, N = Tile<D>::kBuffers, RING = Tile<D>::kRing, kCleanRing = Tile<D>::kCleanRing;
     const int lane = threadIdx.x & 31;
-    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
-    Piece p;
     unsigned fills = 0, tiles = 0, cleaned = 0, dirty = 0;  // dirty: buffers whose last fill is one that is cleaned
     bool ok = true;
-    while (ok && walk.next(&p)) {
-        const int n = p.end - p.begin;
+#pragma unroll 1
+    for (unsigned piece = 0; ok; ++piece) {
+        Job job;
+        ok = read_job(sm, piece, &job, a.err);
+        if (ok && job.begin == job.end) return;
+        const int n = ok ? job.end - job.begin : 0;
 #pragma unroll 1
         for (int i = 0; i < 2 * n; ++i, ++fills) {
-            const Fill f = fill_of(p.paired, n, i);
+            const Fill f = fill_of(job.paired, n, i);
             const int buf = fills % N;
             const unsigned tile = tiles + f.tile, side = tile % RING;
             ok = f.value || warp_wait(&sm.side_full[side], (tile / RING) & 1, a.err, &sm.abort);
@@ -218,23 +257,23 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 // The cleaning warp: V tiles from the first one with a node (or the context's end) on.  Rows between the context's end and its block's
 // become zeros (what lies there may be anything); infinities and NaN of nodes too, with notes.
 // Slots of dirty_full, clean_full, special and the notes are used in turn by cleaned tiles.  Slot c % kCleanRing is free when V of cleaned
-// tile c arrives: its buffer, and those of all fills kBuffers <= 10 or more before it, were released, so the softmax of tiles
-// c - 6 and older is done.  A softmax warp waits for clean_full only of its own tiles; the phase before the one that is meant is over when it
-// does: K of the tile has arrived then, so fills kBuffers or more before that one were released, among them V of cleaned tile
-// c - kCleanRing, at least 2 kCleanRing - 3 >= 10 before.
+// tile c arrives: its buffer, and those of all fills kBuffers or more before it, were released, so the softmax of tiles
+// c - kCleanRing and older is done (V's fills are two apart, or one at a piece's end).  A softmax warp waits for clean_full only of its own
+// tiles; the phase before the one that is meant is over when it does: K of the tile has arrived then, so fills kBuffers or more before that
+// one were released, among them V of cleaned tile c - kCleanRing, at least 2 kCleanRing - 3 before.
 template <typename T, int D, int BS>
-__device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, Notes<D>& notes) {
-    constexpr int N = Tile<D>::kBuffers, UNITS = D / 8, RPP = 32 / UNITS;  // rows per pass
-    static_assert(2 * kCleanRing - 3 >= N && kCleanRing >= 7, "see above");
+__device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, Smem<D>& sm, Notes<D>& notes) {
+    constexpr int N = Tile<D>::kBuffers, kCleanRing = Tile<D>::kCleanRing, UNITS = D / 8, RPP = 32 / UNITS;  // rows per pass
+    static_assert(2 * kCleanRing - 3 >= N, "see above");
     const int lane = threadIdx.x & 31, u = lane % UNITS, sub = lane / UNITS;
-    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
-    Piece p;
     unsigned fills = 0, cleaned = 0;
-    while (walk.next(&p)) {
-        const Item it = item_of(a, p);
-        const int n = p.end - p.begin, base = it.L - it.n;
-        for (int tile = max(p.begin, first_cleaned(it)); tile < p.end; ++tile, ++cleaned) {
-            const unsigned fill = fills + value_fill(p.paired, n, tile - p.begin), slot = cleaned % kCleanRing;
+#pragma unroll 1
+    for (unsigned piece = 0;; ++piece) {
+        Job it;
+        if (!read_job(sm, piece, &it, a.err) || it.begin == it.end) return;
+        const int n = it.end - it.begin, base = it.L - it.n;
+        for (int tile = max(it.begin, first_cleaned(it)); tile < it.end; ++tile, ++cleaned) {
+            const unsigned fill = fills + value_fill(it.paired, n, tile - it.begin), slot = cleaned % kCleanRing;
             unsigned char* v = sm.kv[fill % N];
             if (!warp_wait(&sm.dirty_full[slot], (cleaned / kCleanRing) & 1, a.err, &sm.abort)) return;
             const int p0 = tile * kTile, end = min(kTile, it.L - p0), first = max(0, base - p0);
@@ -278,96 +317,125 @@ __device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, const Works
     }
 }
 
-// One warp per stream issues its products; while one waits, the other's keep the tensor cores busy.  Job j of a piece is a
-// score tile of stream j % 2, in two halves of 64 columns (64 positions): a half's scores are issued right behind the output of the
-// same half of the stream's previous job, which has then read the P that they overwrite, and are ready while the softmax warps are
-// still at the other half.
+// One warp per stream issues its products.  Job j of a piece is a score tile of stream j % 2, in two halves of 64 columns (64 positions).
+// The scores of a half go out as soon as those of the half before are in registers, and the output of a half when its weights
+// are there: the softmax warps find the next half's scores ready, and the tensor cores work while they do.  (With weights in the scores'
+// place, 64 columns more each, a half's scores had to wait for the output of the half before the last: 163 us for wide trees.)
 // A buffer is free after two arrivals, one from either stream: by its products' commit, or, of a tile that is the other stream's, when it is
-// passed.  A wait tells a phase of a barrier from the one before it alone: so every stream takes the fills in order and waits for each.
+// passed.  A wait tells a phase of a barrier from the one before it alone: so every stream takes the fills in order and waits for each.  A
+// query tile too is free after two arrivals; a stream that skips one (a pair's other) waits for the next in its place, or for one
+// that was staged behind that.
 template <typename T, int D>
-__device__ __forceinline__ void issue_products(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, int t) {
+__device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>& sm, int t) {
     constexpr int N = Tile<D>::kBuffers;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     volatile int* abort = &sm.abort;
-    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * D;
-    const uint64_t qd = desc_of(smem_addr(sm.q[t]), 16, 1024), k0 = desc_of(smem_addr(sm.kv[0]), 16, Tile<D>::kGroup),
+    const bool one = (threadIdx.x & 31) == 0;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = scores_at(tmem, t), o_at = output_at<D>(tmem, t);
+    const uint64_t q0 = desc_of(smem_addr(sm.q[0]), 16, 1024), k0 = desc_of(smem_addr(sm.kv[0]), 16, Tile<D>::kGroup),
                    v0 = desc_of(smem_addr(sm.kv[0]), 1024, Tile<D>::kGroup);
-    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
-    Piece p;
-    unsigned fill = 0, pieces = 0, steps = 0;  // fill: the next one that this stream has to take
-    while (walk.next(&p)) {
-        const int n = p.end - p.begin, jobs = n * (p.paired ? 2 : 1);
-        const unsigned fills = fill;
+    // scores: the query rows are negated instead of the scale
+    const uint32_t s_desc = idesc_of(kTile / 2, false, kBf16) | (a.scale < 0.f ? 1u << 13 : 0u);
+    unsigned fill = 0, queries = 0, done = 0;  // next fill and query tile that this stream has to take; halves before this piece
+#pragma unroll 1
+    for (unsigned piece = 0;; ++piece) {
+        Job job;
+        if (!read_job(sm, piece, &job, a.err) || job.begin == job.end) return;
+        const int n = job.end - job.begin, jobs = n * (job.paired ? 2 : 1), halves = 2 * ((jobs + 1 - t) / 2);
+        const unsigned fills = fill, query = queries + (job.paired ? t : 0), qbuf = query & 1;
+        queries += job.paired ? 2 : 1;
         auto pass = [&](unsigned to) {
             for (; fill < to; ++fill) {
                 if (!warp_wait(&sm.kv_full[fill % N], (fill / N) & 1, a.err, abort)) return false;
-                if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.kv_empty[fill % N]);
+                if (one) mbar_arrive(&sm.kv_empty[fill % N]);
             }
             return true;
         };
-        // unit u: half u % 2 of the stream's job u / 2
-        const int units = 2 * ((jobs + 1 - t) / 2);
+        if (!warp_wait(&sm.q_full[qbuf], (query >> 1) & 1, a.err, abort)) return;
+        if (halves == 0 && one) mbar_arrive(&sm.q_free[qbuf]);
+        const uint64_t qd = q0 + (qbuf * Tile<D>::kOperand >> 4);
 #pragma unroll 1
-        for (int u = -2; u < units; ++u) {
-            const int half = u & 1;
-            if (u >= 0) {
-                const int tile = p.paired ? u >> 1 : u - half + t;
-                const unsigned f = fills + value_fill(p.paired, n, tile), buf = f % N;
-                if (half == 0 && !(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
-                if (!warp_wait(&sm.p_full[t][half], steps & 1, a.err, abort)) return;
-                tc_fence_after();
-                const uint64_t vd = v0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    mma_ts(o_at, s_at + 64 * half + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), u > 0 || k > 0);
-                tc_commit(&sm.pv_done[t][half]);
-                if (half == 0) fill = f + 1;  // (released behind the other half)
-                if (half == 1) {
-                    tc_commit(&sm.kv_empty[buf]);
-                    ++steps;
+        for (int h = -1; h < halves; ++h) {
+            const int next = h + 1;
+            if (next < halves) {
+                const int tile = job.paired ? next >> 1 : (next & ~1) + t, half = next & 1;
+                const unsigned f = fills + key_fill(job.paired, tile), buf = f % N;
+                if (half == 0) {
+                    if (!(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
+                    fill = f + 1;  // (released behind the other half)
                 }
-                if (u == units - 1) tc_commit(&sm.o_full[t]);
-            }
-            const int next = u + 2;
-            if (next < units) {
-                const int tile = p.paired ? next >> 1 : next - half + t;
-                const unsigned f = fills + key_fill(p.paired, tile), buf = f % N;
-                if (half == 0 && !(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
-                if (next == 0 && !warp_wait(&sm.q_full[t], pieces++ & 1, a.err, abort)) return;
+                const unsigned at = done + next;
+                if (at > 0 && !warp_wait(&sm.s_free[t], (at - 1) & 1, a.err, abort)) return;
                 tc_fence_after();
                 const uint64_t kd = k0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_ss(s_at + 64 * half, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4),
-                           idesc_of(kTile / 2, false, kBf16), k > 0);
-                if (half == 0) fill = f + 1;
+                    mma_ss(s_at, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4), s_desc, k > 0);
+                tc_commit(&sm.s_full[t]);
                 if (half == 1) tc_commit(&sm.kv_empty[buf]);
-                tc_commit(&sm.s_full[t][half]);
+                if (next == halves - 1) {
+                    tc_commit(&sm.q_free[qbuf]);
+                    if (job.paired) tc_commit(&sm.q_free[qbuf]);
+                }
+            }
+            if (h >= 0) {
+                const int tile = job.paired ? h >> 1 : (h & ~1) + t, half = h & 1;
+                const unsigned f = fills + value_fill(job.paired, n, tile), buf = f % N;
+                if (half == 0) {
+                    if (!(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
+                    fill = f + 1;
+                }
+                if (!warp_wait(&sm.p_full[t][half], ((done + h) >> 1) & 1, a.err, abort)) return;
+                tc_fence_after();
+                const uint64_t vd = v0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ts(o_at, weights_at(tmem, t, half) + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), h > 0 || k > 0);
+                tc_commit(&sm.pv_done[t][half]);
+                if (half == 1) tc_commit(&sm.kv_empty[buf]);
+                if (h == halves - 1) tc_commit(&sm.o_full[t]);
             }
         }
+        done += halves;
         if (!pass(fills + 2 * n)) return;
     }
 }
 
-// A warp's 32 query rows into the swizzled tile; row_at: where this lane's row begins (live: if it exists).  D / 8 lanes load a row together.
+// The query warp: row tile after row tile, up to one piece ahead.  D / 8 lanes copy a row together; rows of a live softmax warp that do not
+// exist become zeros.
 template <typename T, int D>
-__device__ __forceinline__ void stage_query(const T* query, size_t row_at, bool live, bool negate, unsigned char* tile, int row0) {
-    constexpr int LPR = D / 8, RPS = 32 / LPR, BATCH = 8;
-    const int lane = threadIdx.x & 31, sub = lane / LPR, i = lane % LPR;
-    const unsigned alive = __ballot_sync(0xffffffffu, live);
-    const uint32_t flip = negate ? 0x80008000u : 0u;
+__device__ __forceinline__ void stage_queries(const TreeAttendArgs& a, Smem<D>& sm) {
+    constexpr int LPR = D / 8, RPS = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, i = lane % LPR, group = a.num_heads / a.num_kv_heads;
+    const T* query = static_cast<const T*>(a.query);
+    unsigned tile = 0;
 #pragma unroll 1
-    for (int b = 0; b < 32; b += BATCH * RPS) {
-        uint4 raw[BATCH];
+    for (unsigned piece = 0;; ++piece) {
+        Job job;
+        if (!read_job(sm, piece, &job, a.err) || job.begin == job.end) return;
+#pragma unroll 1
+        for (int k = 0; k < (job.paired ? 2 : 1); ++k, ++tile) {
+            const int buf = tile & 1, first = job.row0 + k * kTile, rows = min(kTile, job.n * group - first);
+            if (!warp_wait(&sm.q_free[buf], ((tile >> 1) & 1) ^ 1, a.err, &sm.abort)) return;
+#pragma unroll 1
+            for (int b = 0; b < rows; b += 32) {
+                const int v = first + b + lane, node = v / group;  // this lane's row; its address goes to the lanes that copy it
+                const bool live = b + lane < rows;
+                const long long row_at =
+                    live ? ((long long)(job.first_token + node) * a.num_heads + job.kvh * group + (v - node * group)) * D : 0;
+                const unsigned alive = __ballot_sync(0xffffffffu, live);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)  // (rows that do not exist read the first one: a branch would wait for each load)
-            raw[k] = *reinterpret_cast<const uint4*>(query + __shfl_sync(0xffffffffu, row_at, b + k * RPS + sub) + 8 * i);
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int r = b + k * RPS + sub, row = row0 + r;
-            const bool there = alive >> r & 1;
-            *reinterpret_cast<uint4*>(tile + row * 128 + (i / 8) * kPanel + (((i & 7) ^ (row & 7)) << 4)) =
-                there ? make_uint4(raw[k].x ^ flip, raw[k].y ^ flip, raw[k].z ^ flip, raw[k].w ^ flip) : make_uint4(0u, 0u, 0u, 0u);
+                for (int r = 0; r < 32; r += RPS) {
+                    const int row = b + r + sub;
+                    const T* src = query + __shfl_sync(0xffffffffu, row_at, r + sub) + 8 * i;
+                    cp_async_16_or_zero(sm.q[buf] + row * 128 + (i / 8) * kPanel + (((i & 7) ^ (row & 7)) << 4), src, alive >> (r + sub) & 1);
+                }
+            }
+            cp_async_commit();
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full[buf]);
         }
     }
 }
@@ -437,238 +505,247 @@ __device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, float
     return sum.x + sum.y;
 }
 
+// Eight 16-byte units of a row per lane become, in groups of eight lanes, one unit of each of the group's rows: x[r] is unit lane % 8 of
+// row r.  Stores of x[r] then write whole 128-byte lines; a row to a lane, each store of a warp touched 32 of them, and the results of
+// a piece took 4000 cycles.
+__device__ __forceinline__ void transpose8(uint4 (&x)[8]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int step = 4; step > 0; step >>= 1) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j & step) continue;
+            const uint4 give = up ? x[j] : x[j + step];
+            const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, step), __shfl_xor_sync(0xffffffffu, give.y, step),
+                                         __shfl_xor_sync(0xffffffffu, give.z, step), __shfl_xor_sync(0xffffffffu, give.w, step));
+            if (up) x[j] = got;
+            else x[j + step] = got;
+        }
+    }
+}
+
 // A softmax warp: 32 rows of a stream's row tile, one per lane.
 template <typename T, int D, int BS>
 __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, Notes<D>& notes) {
-    constexpr int RING = Tile<D>::kRing;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane;
+    constexpr int RING = Tile<D>::kRing, kCleanRing = Tile<D>::kCleanRing;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane, group = a.num_heads / a.num_kv_heads;
     volatile int* abort = &sm.abort;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = sm.tmem + lanes + t * kTile, o_at = sm.tmem + lanes + 2 * kTile + t * D;
-    const uint32_t other_o_at = sm.tmem + lanes + 2 * kTile + (t ^ 1) * D;
+    const uint32_t s_at = scores_at(sm.tmem, t) + lanes, o_at = output_at<D>(sm.tmem, t) + lanes, other_o_at = output_at<D>(sm.tmem, t ^ 1) + lanes;
     // (kept above zero, so that masked scores stay -inf)
     const float factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-38f);
-    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
-    unsigned pieces = 0, steps = 0, joins = 0, tiles_before = 0, cleaned_before = 0;  // so far
-    // what the result of a piece needs; it is written after the next piece's queries are staged, which waits for nothing
-    struct Result {
-        size_t row_at;
-        float* rec;
-        bool live, warp_live, cut, join;
-    } res{};
-    float m = -INFINITY, l = 0.f;  // the row's reference of exponents, the sum of its exponentials
-    bool noted = false, pending = false;
+    unsigned pieces = 0, done = 0, joins = 0, tiles_before = 0, cleaned_before = 0;  // so far: of this stream, halves; of all, tiles
 #pragma unroll 1
-    for (;;) {
-        Piece p;
-        Item it{};
-        int n = 0, my_jobs = 0, base = 0, first_clean = 0;
-        const uint64_t* words = nullptr;
-        Result now{};
-        const bool have = walk.next(&p);
-        if (have) {
-            it = item_of(a, p);
-            n = p.end - p.begin;
-            my_jobs = (it.jobs + 1 - t) / 2;
-            base = it.L - it.n;
-            first_clean = max(p.begin, first_cleaned(it));
-            if (my_jobs == 0 && !pending) {  // a single tile in a split piece is stream 0's
-                tiles_before += n;
-                cleaned_before += max(0, p.end - first_clean);
+    for (unsigned piece = 0;; ++piece) {
+        Job job;
+        if (!read_job(sm, piece, &job, a.err) || job.begin == job.end) return;
+        const int n = job.end - job.begin, jobs = n * (job.paired ? 2 : 1), halves = 2 * ((jobs + 1 - t) / 2);
+        const int base = job.L - job.n, first_clean = max(job.begin, first_cleaned(job));
+        const unsigned tiles_now = tiles_before, cleaned_now = cleaned_before;
+        tiles_before += n;
+        cleaned_before += max(0, job.end - first_clean);
+        if (halves == 0) continue;  // a single tile in a split piece is stream 0's
+        const int first = job.row0 + (job.paired ? t * kTile : 0), v = first + r, node = v / group;  // row of the request
+        const bool live = v < job.n * group, warp_live = first + (warp & 3) * 32 < job.n * group;
+        const uint64_t* words = reinterpret_cast<const uint64_t*>(a.tree_mask) + (live ? (size_t)(job.first_token + node) * a.mask_words : 0);
+        float m = -INFINITY, l = 0.f;  // the row's reference of exponents, the sum of its exponentials
+        bool noted = false;
+        uint64_t seen[2] = {~0ull, ~0ull};
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h, ++done) {
+            const int half = h & 1, local = job.paired ? h >> 1 : (h & ~1) + t, tile = job.begin + local;
+            const int p0 = tile * kTile, slot = (tiles_now + local) % RING;
+            if (!warp_wait(&sm.s_full[t], done & 1, a.err, abort)) return;
+            tc_fence_after();
+            if (!warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
+                if (lane == 0) {
+                    mbar_arrive(&sm.s_free[t]);
+                    mbar_arrive(&sm.p_full[t][half]);
+                }
                 continue;
             }
-            const int first = p.row0 + (p.paired ? t * kTile : 0), v = first + r;  // row of the request
-            const int token = v / it.group;
-            now.live = v < it.rows;
-            now.warp_live = first + (warp & 3) * 32 < it.rows;
-            now.cut = p.begin > 0 || p.end < p.tiles;
-            now.join = !p.paired && it.jobs > 1;
-            now.rec = ws.records + ((size_t)blockIdx.x * 4 + (p.begin > 0 ? 0 : 2) + (p.paired ? t : 0)) * record_floats(D);
-            now.row_at = now.live ? ((size_t)(it.first_token + token) * a.num_heads + p.kvh * it.group + (v - token * it.group)) * D : 0;
-            words = reinterpret_cast<const uint64_t*>(a.tree_mask) + (now.live ? (size_t)(it.first_token + token) * a.mask_words : 0);
-            if (my_jobs > 0) {
-                // the stream's last scores were waited for, so its query tile is free
-                stage_query<T, D>(static_cast<const T*>(a.query), now.row_at, now.live, a.scale < 0.f, sm.q[t], (warp & 3) * 32);
-                fence_proxy_async_smem();
-                mbar_arrive(&sm.q_full[t]);
+            uint32_t s[64];
+            tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            const unsigned masked = sm.masked[slot];
+            tc_wait_ld(s);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_free[t]);
+            if (masked) {  // a block that is not there, or (bit 31) a tile with nodes or the context's end
+                const uint64_t mine =
+                    live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
+                if (half == 0) seen[0] = mine;
+                else seen[1] = mine;
+                const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (!(lo >> i & 1)) s[i] = 0xff800000u;
+                    if (!(hi >> i & 1)) s[32 + i] = 0xff800000u;
+                }
             }
+            const float top = row_max(s) * factor;
+            if (h == 0) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                // The output so far has to be there.  (The phase before the one that is meant is over, for the reason below.)
+                if (!warp_wait(&sm.pv_done[t][half ^ 1], ((done - 1) >> 1) & 1, a.err, abort)) return;
+                tc_fence_after();
+                const float mn = fmaxf(m, top);
+                const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                l *= f;
+                m = mn;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_at + c, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st16(o_at + c, o);
+                }
+            }
+            // (The weights of the half before the last lie where these go.  They have been read: the output that reads them was issued before
+            // this half's scores, whose commit waits for all products before it.)
+            l += row_exp<T>(s, weights_at(sm.tmem, t, half) + lanes, factor, m == -INFINITY ? 0.f : m);
+            if (half == 1 && (masked >> 31)) {  // a tile whose V was cleaned
+                const unsigned c = cleaned_now + (tile - first_clean), note = c % kCleanRing;
+                if (!warp_wait(&sm.clean_full[note], (c / kCleanRing) & 1, a.err, abort)) return;
+                if (sm.special[note]) {
+                    const int from = max(0, base - p0);
+#pragma unroll 1
+                    for (int sign = 0; sign < 2; ++sign) {
+#pragma unroll 1
+                        for (int i = 0; i < D / 32; ++i) {
+                            uint32_t bits = noted ? notes.row[t][sign][r][i] : 0u;
+#pragma unroll 1
+                            for (int k = from; k < kTile; ++k)
+                                if (seen[k >> 6] >> (k & 63) & 1) bits |= *reinterpret_cast<const uint32_t*>(&notes.at[note][sign][k][4 * i]);
+                            notes.row[t][sign][r][i] = bits;
+                        }
+                    }
+                    noted = true;
+                }
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
         }
 
-        if (pending) {  // the previous piece's result
-            if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+        // the piece's result
+        const bool cut = job.begin > 0 || job.end < job.tiles, join = !job.paired && jobs > 1;
+        if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+        tc_fence_after();
+        ++pieces;
+        float f0 = 1.f, f1 = 0.f;  // factors of this stream's output and of the other's
+        uint32_t notes_from = noted ? 1u << t : 0u;
+        if (join) {  // both streams have a part of the same rows, in the same lanes of tensor memory
+            sm.state[t][r] = make_float2(m, __uint_as_float((__float_as_uint(l) & 0x7fffffffu) | (noted ? 0x80000000u : 0u)));
+            tc_fence_before();
+            mbar_arrive(&sm.join_full);
+            if (!warp_wait(&sm.join_full, joins & 1, a.err, abort)) return;
             tc_fence_after();
-            ++pieces;
-            float f0 = 1.f, f1 = 0.f;  // factors of this stream's output and of the other's
-            uint32_t notes_from = noted ? 1u << t : 0u;
-            if (res.join) {  // both streams have a part of the same rows, in the same lanes of tensor memory
-                sm.state[t][r] = make_float2(m, __uint_as_float((__float_as_uint(l) & 0x7fffffffu) | (noted ? 0x80000000u : 0u)));
-                tc_fence_before();
-                mbar_arrive(&sm.join_full);
-                if (!warp_wait(&sm.join_full, joins & 1, a.err, abort)) return;
-                tc_fence_after();
-                const float2 o = sm.state[t ^ 1][r];
-                const float ol = __uint_as_float(__float_as_uint(o.y) & 0x7fffffffu);
-                const float mn = fmaxf(m, o.x);
-                // a state without a maximum is empty, unless its sum is NaN
-                f0 = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2_approx(m - mn);
-                f1 = o.x == -INFINITY ? (ol != ol ? 1.f : 0.f) : exp2_approx(o.x - mn);
-                l = l * f0 + ol * f1;
-                m = mn;
-                if (__float_as_uint(o.y) >> 31) notes_from |= 2u >> t;
-            }
-            if (res.warp_live) {
-                const float inv = res.cut ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-                const int c0 = res.join ? t * (D / 2) : 0, c1 = res.join ? c0 + D / 2 : D;
+            const float2 o = sm.state[t ^ 1][r];
+            const float ol = __uint_as_float(__float_as_uint(o.y) & 0x7fffffffu);
+            const float mn = fmaxf(m, o.x);
+            // a state without a maximum is empty, unless its sum is NaN
+            f0 = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2_approx(m - mn);
+            f1 = o.x == -INFINITY ? (ol != ol ? 1.f : 0.f) : exp2_approx(o.x - mn);
+            l = l * f0 + ol * f1;
+            m = mn;
+            if (__float_as_uint(o.y) >> 31) notes_from |= 2u >> t;
+        }
+        if (warp_live) {
+            float* rec = ws.records + ((size_t)blockIdx.x * 4 + (job.begin > 0 ? 0 : 2) + (job.paired ? t : 0)) * record_floats(D);
+            const long long row_at = live ? ((long long)(job.first_token + node) * a.num_heads + job.kvh * group + (v - node * group)) * D : 0;
+            if (!cut) f0 *= l == 0.f ? 0.f : 1.f / l, f1 *= l == 0.f ? 0.f : 1.f / l;
+            if (l != l) notes_from = 0;  // (NaN everywhere)
+            const unsigned alive = __ballot_sync(0xffffffffu, live);
+            const int c0 = join ? t * (D / 2) : 0, c1 = join ? c0 + D / 2 : D;
+            // 32 columns from c on, in float32
+            auto columns = [&](int c, uint32_t (&s)[32]) {
+                tmem_ld32(o_at + c, s);
+                tc_wait_ld(s);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
+                if (join) {
+                    uint32_t o[32];
+                    tmem_ld32(other_o_at + c, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k])));
+                }
+                if (notes_from) {
+                    uint32_t plus = 0, minus = 0;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (notes_from >> k & 1) {
+                            plus |= notes.row[k][0][r][c / 32];
+                            minus |= notes.row[k][1][r][c / 32];
+                        }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if ((plus | minus) >> k & 1) s[k] = !(minus >> k & 1) ? 0x7f800000u : !(plus >> k & 1) ? 0xff800000u : 0x7fc00000u;
+                }
+            };
+            if (cut) {
 #pragma unroll 1
                 for (int c = c0; c < c1; c += 32) {
                     uint32_t s[32];
-                    tmem_ld32(o_at + c, s);
-                    tc_wait_ld(s);
+                    columns(c, s);
+                    uint4 x[8];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
-                    if (res.join) {
-                        uint32_t o[32];
-                        tmem_ld32(other_o_at + c, o);
-                        tc_wait_ld(o);
+                    for (int k = 0; k < 8; ++k) x[k] = make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
+                    transpose8(x);
+                    float* to = rec + 2 * kTile + (size_t)((warp & 3) * 32 + (lane & 24)) * D + c + 4 * (lane & 7);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k])));
-                    }
-                    if (notes_from) {
-                        uint32_t plus = 0, minus = 0;
+                    for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(to + k * D) = x[k];
+                }
+                if (c0 == 0) {
+                    rec[r] = m;
+                    rec[kTile + r] = l;
+                }
+            } else {
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 64) {
+                    uint4 x[8];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (notes_from >> k & 1) {
-                                plus |= notes.row[k][0][r][c / 32];
-                                minus |= notes.row[k][1][r][c / 32];
-                            }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if ((plus | minus) >> k & 1) s[k] = !(minus >> k & 1) ? 0x7f800000u : !(plus >> k & 1) ? 0xff800000u : 0x7fc00000u;
-                    }
-                    if (res.live && res.cut) {
-                        uint4* d = reinterpret_cast<uint4*>(res.rec + 2 * kTile + (size_t)r * D + c);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) d[k] = make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]);
-                    } else if (res.live) {
-                        uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + res.row_at + c);
+                    for (int part = 0; part < 2; ++part) {
+                        if (join && D == 64 && part == 1) {  // (a stream has 32 columns)
+                            x[4] = x[5] = x[6] = x[7] = make_uint4(0u, 0u, 0u, 0u);
+                            break;
+                        }
+                        uint32_t s[32];
+                        columns(c + 32 * part, s);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t y[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                y[i] = round2<T>(make_float2(__uint_as_float(s[8 * k + 2 * i]) * inv, __uint_as_float(s[8 * k + 2 * i + 1]) * inv));
-                            d[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                                y[i] = round2<T>(make_float2(__uint_as_float(s[8 * k + 2 * i]), __uint_as_float(s[8 * k + 2 * i + 1])));
+                            x[4 * part + k] = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
-                }
-                if (res.cut && res.live && c0 == 0) {
-                    res.rec[r] = m;
-                    res.rec[kTile + r] = l;
-                }
-            }
-            tc_fence_before();
-            if (res.join) {  // neither stream's output is written again before both have read it
-                mbar_arrive(&sm.join_done);
-                if (!warp_wait(&sm.join_done, joins & 1, a.err, abort)) return;
-                ++joins;
-            }
-            pending = false;
-        }
-        if (!have) return;
-        if (my_jobs == 0) {
-            tiles_before += n;
-            cleaned_before += max(0, p.end - first_clean);
-            continue;
-        }
-
-        res = now;
-        pending = true;
-        m = -INFINITY;
-        l = 0.f;
-        noted = false;
-#pragma unroll 1
-        for (int step = 0; step < my_jobs; ++step, ++steps) {
-            const int local = p.paired ? step : 2 * step + t, tile = p.begin + local;
-            const int p0 = tile * kTile, slot = (tiles_before + local) % RING;
-            uint64_t seen[2] = {~0ull, ~0ull};
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (!warp_wait(&sm.s_full[t][half], steps & 1, a.err, abort)) return;
-                tc_fence_after();
-                if (!now.warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
-                    if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
-                    continue;
-                }
-                const uint32_t at = s_at + 64 * half;
-                uint32_t s[64];
-                tmem_ld32(at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                tmem_ld32(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                const unsigned masked = sm.masked[slot];
-                tc_wait_ld(s);
-                if (masked) {  // a block that is not there, or (bit 31) a tile with nodes or the context's end
-                    const uint64_t mine = now.live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, it.n,
-                                                                  (masked & 0xffu) >> (half * (64 / BS)))
-                                                   : 0ull;
-                    if (half == 0) seen[0] = mine;
-                    else seen[1] = mine;
-                    const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
+                    const bool mine = !(join && D == 64) || (lane & 7) < 4;
+                    transpose8(x);
+                    T* out = static_cast<T*>(a.out) + c + 8 * (lane & 7);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (!(lo >> i & 1)) s[i] = 0xff800000u;
-                        if (!(hi >> i & 1)) s[32 + i] = 0xff800000u;
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = (lane & 24) + k;
+                        const long long at = __shfl_sync(0xffffffffu, row_at, row);
+                        if (mine && (alive >> row & 1)) *reinterpret_cast<uint4*>(out + at) = x[k];
                     }
                 }
-                const float top = row_max(s) * factor;
-                if (step == 0 && half == 0) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                    // The output so far has to be there.  (Its barrier is waited for only here: the phase before the one that is
-                    // meant is over, because this half's scores were issued after the output of the half before the last.)
-                    const unsigned last = half ? steps : steps - 1;
-                    if (!warp_wait(&sm.pv_done[t][half ^ 1], last & 1, a.err, abort)) return;
-                    tc_fence_after();
-                    const float mn = fmaxf(m, top);
-                    const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-                    l *= f;
-                    m = mn;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_at + c, o);
-                        tc_wait_ld(o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st16(o_at + c, o);
-                    }
-                }
-                l += row_exp<T>(s, at, factor, m == -INFINITY ? 0.f : m);
-                if (half == 1 && (masked >> 31)) {  // a tile whose V was cleaned
-                    const unsigned c = cleaned_before + (tile - first_clean), note = c % kCleanRing;
-                    if (!warp_wait(&sm.clean_full[note], (c / kCleanRing) & 1, a.err, abort)) return;
-                    if (sm.special[note]) {
-                        const int from = max(0, base - p0);
-#pragma unroll 1
-                        for (int sign = 0; sign < 2; ++sign) {
-#pragma unroll 1
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t bits = noted ? notes.row[t][sign][r][i] : 0u;
-#pragma unroll 1
-                                for (int k = from; k < kTile; ++k)
-                                    if (seen[k >> 6] >> (k & 63) & 1) bits |= *reinterpret_cast<const uint32_t*>(&notes.at[note][sign][k][4 * i]);
-                                notes.row[t][sign][r][i] = bits;
-                            }
-                        }
-                        noted = true;
-                    }
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
             }
         }
-        tiles_before += n;
-        cleaned_before += max(0, p.end - first_clean);
+        tc_fence_before();
+        if (join) {  // neither stream's output is written again before both have read it
+            mbar_arrive(&sm.join_done);
+            if (!warp_wait(&sm.join_done, joins & 1, a.err, abort)) return;
+            ++joins;
+        }
     }
 }
 
@@ -681,13 +758,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 128);
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_free[i], 2);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4);
             for (int h = 0; h < 2; ++h) {
-                mbar_init(&sm.s_full[i][h], 1);
                 mbar_init(&sm.p_full[i][h], 4);
                 mbar_init(&sm.pv_done[i][h], 1);
             }
             mbar_init(&sm.o_full[i], 1);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&sm.job_full[i], 1);
+            mbar_init(&sm.job_free[i], kReaders);
         }
         for (int i = 0; i < Tile<D>::kRing; ++i) {
             mbar_init(&sm.side_full[i], 1);
@@ -697,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 2);
         }
-        for (int i = 0; i < kCleanRing; ++i) {
+        for (int i = 0; i < Tile<D>::kCleanRing; ++i) {
             mbar_init(&sm.dirty_full[i], 1);
             mbar_init(&sm.clean_full[i], 1);
         }
@@ -718,14 +801,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
     if (warp < kSoftmaxWarps) {
         softmax_rows<T, D, BS>(a, ws, sm, notes);
     } else if (warp == kCopyWarp) {
-        copy_tiles<D, BS>(a, ws, sm, &kmap, &vmap);
+        copy_tiles<D, BS>(a, sm, &kmap, &vmap);
     } else if (warp == kLookWarp) {
         look_ahead<D, BS>(a, ws, sm);
     } else if (warp == kCleanWarp) {
-        clean_tiles<T, D, BS>(a, ws, sm, notes);
+        clean_tiles<T, D, BS>(a, sm, notes);
+    } else if (warp == kQueryWarp) {
+        stage_queries<T, D>(a, sm);
     } else {
         const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
-        issue_products<T, D>(a, ws, sm, t);
+        issue_products<T, D>(a, sm, t);
         if (__any_sync(0xffffffffu, sm.abort)) {  // products still in flight read shared and tensor memory
             int never = 0;
             tc_commit(&sm.drain[t]);
