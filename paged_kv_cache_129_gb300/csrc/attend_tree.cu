@@ -5,11 +5,10 @@
 //     out = sum softmax(scale q k_j) v_j over what it sees; zeros where that is nothing.
 //
 // Rows.  The g query heads of a kv head and the request's nodes form n_b * g rows (row v: node v / g, head v % g), cut into tiles of 128,
-// the M of the products; keys come in tiles of 128 positions, whose scores are made and used in halves of 64 columns: while the softmax
-// warps work on one half, the other half's products run.  A CTA has two streams of softmax warps:
-//   paired  two row tiles share every key tile;
-//   split   a single row tile (small trees, single tokens, the rest of a wide tree): the streams take alternate key tiles, and join their
-//           results at the end.
+// the M of the products; keys come in tiles of 128 positions.  A CTA has two streams of softmax warps:
+//   paired  two row tiles share every key tile, a stream each;
+//   split   a single row tile (small trees, single tokens, the rest of a wide tree): each stream takes one half, 64 positions, of every key
+//           tile, and they join their results at the end.
 // Work.  Equal shares of all units' key tiles per SM, see attend_units.cuh.
 // Operands.  K and V go from the cache's blocks straight into operand tiles, one bulk tensor copy per block: a block's rows as groups of
 // eight by panels of 64 elements, which is the order that both products read (K by rows, V by columns) with uniform strides.  A block
@@ -96,7 +95,7 @@ struct Notes {
 };
 
 // The order in which a piece's n key tiles go through the buffers.  Paired: K0 V0 K1 V1 ...  Split: K one tile ahead, K0 K1 V0 K2
-// V1 ... V(n-2) V(n-1), because the scores of a tile are issued before the output of the tile before it.
+// V1 ... V(n-2) V(n-1), because the scores of a tile are made before the output of the tile before it.
 struct Fill {
     int tile;
     bool value;
@@ -107,7 +106,6 @@ __device__ __forceinline__ Fill fill_of(bool paired, int n, int i) {
     if (i == 0) return {0, false};
     return (i & 1) ? Fill{(i + 1) >> 1, false} : Fill{(i >> 1) - 1, true};
 }
-__device__ __forceinline__ int key_fill(bool paired, int tile) { return paired ? 2 * tile : tile == 0 ? 0 : 2 * tile - 1; }
 __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
     return paired ? 2 * tile + 1 : tile == n - 1 ? 2 * n - 1 : 2 * tile + 2;
 }
@@ -115,11 +113,16 @@ __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
 // The first key tile whose V is cleaned: the one with the request's first node (or the context's end).
 __device__ __forceinline__ int first_cleaned(const Job& j) { return max(0, j.L - j.n) / kTile; }
 
-// Tensor memory: per stream 64 columns of scores (of one half), then twice 32 of weights P; behind both streams', D of output each.
-__device__ __forceinline__ uint32_t scores_at(uint32_t tmem, int t) { return tmem + t * 128; }
-__device__ __forceinline__ uint32_t weights_at(uint32_t tmem, int t, int half) { return tmem + t * 128 + 64 + 32 * half; }
+// Tensor memory: 128 columns per stream for scores and the weights P made of them (32 columns for 64 positions), and behind both streams'
+// D columns of output each.
+//   paired  scores of the whole tile; P of a half goes where its first half's scores were.  While one stream is at its softmax the other's
+//           products run: a product of 128 columns of scores takes 66 cycles where two of 64 take 100, since it reads the query rows once.
+//   split   64 columns of scores, and twice 32 of P, in turn by key tiles: the next tile's scores can be made as soon as these are in
+//           registers, and are ready when their turn comes.
+__device__ __forceinline__ uint32_t scores_at(bool paired, int half) { return paired ? 64 * half : 0; }
+__device__ __forceinline__ uint32_t weights_at(bool paired, int buffer) { return 32 * buffer + (paired ? 0 : 64); }
 template <int D>
-__device__ __forceinline__ uint32_t output_at(uint32_t tmem, int t) { return tmem + 256 + t * D; }
+__device__ __forceinline__ uint32_t output_at(int t) { return 256 + t * D; }
 
 // Piece i of the share, for a warp of any role but the look-ahead's, which writes them; false if a wait gave up.
 constexpr int kReaders = kThreads / 32 - 1;
@@ -258,13 +261,11 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 // become zeros (what lies there may be anything); infinities and NaN of nodes too, with notes.
 // Slots of dirty_full, clean_full, special and the notes are used in turn by cleaned tiles.  Slot c % kCleanRing is free when V of cleaned
 // tile c arrives: its buffer, and those of all fills kBuffers or more before it, were released, so the softmax of tiles
-// c - kCleanRing and older is done (V's fills are two apart, or one at a piece's end).  A softmax warp waits for clean_full only of its own
-// tiles; the phase before the one that is meant is over when it does: K of the tile has arrived then, so fills kBuffers or more before that
-// one were released, among them V of cleaned tile c - kCleanRing, at least 2 kCleanRing - 3 before.
+// c - kCleanRing and older is done (V's fills are two apart, or one at a piece's end).
 template <typename T, int D, int BS>
 __device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, Smem<D>& sm, Notes<D>& notes) {
     constexpr int N = Tile<D>::kBuffers, kCleanRing = Tile<D>::kCleanRing, UNITS = D / 8, RPP = 32 / UNITS;  // rows per pass
-    static_assert(2 * kCleanRing - 3 >= N, "see above");
+    static_assert(2 * kCleanRing - 1 >= N, "see above");
     const int lane = threadIdx.x & 31, u = lane % UNITS, sub = lane / UNITS;
     unsigned fills = 0, cleaned = 0;
 #pragma unroll 1
@@ -317,87 +318,94 @@ __device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, Smem<D>& sm
     }
 }
 
-// One warp per stream issues its products.  Job j of a piece is a score tile of stream j % 2, in two halves of 64 columns (64 positions).
-// The scores of a half go out as soon as those of the half before are in registers, and the output of a half when its weights
-// are there: the softmax warps find the next half's scores ready, and the tensor cores work while they do.  (With weights in the scores'
-// place, 64 columns more each, a half's scores had to wait for the output of the half before the last: 163 us for wide trees.)
-// A buffer is free after two arrivals, one from either stream: by its products' commit, or, of a tile that is the other stream's, when it is
-// passed.  A wait tells a phase of a barrier from the one before it alone: so every stream takes the fills in order and waits for each.  A
-// query tile too is free after two arrivals; a stream that skips one (a pair's other) waits for the next in its place, or for one
-// that was staged behind that.
+// One warp per stream issues its products.  Both streams read every K and V tile, in the order in which they come; a buffer is free when
+// both have committed what reads it, a query tile too (a pair's tile, read by one stream, is committed twice).
 template <typename T, int D>
 __device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>& sm, int t) {
     constexpr int N = Tile<D>::kBuffers;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     volatile int* abort = &sm.abort;
-    const bool one = (threadIdx.x & 31) == 0;
-    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = scores_at(tmem, t), o_at = output_at<D>(tmem, t);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), s_at = tmem + t * 128, o_at = tmem + output_at<D>(t);
     const uint64_t q0 = desc_of(smem_addr(sm.q[0]), 16, 1024), k0 = desc_of(smem_addr(sm.kv[0]), 16, Tile<D>::kGroup),
                    v0 = desc_of(smem_addr(sm.kv[0]), 1024, Tile<D>::kGroup);
-    // scores: the query rows are negated instead of the scale
-    const uint32_t s_desc = idesc_of(kTile / 2, false, kBf16) | (a.scale < 0.f ? 1u << 13 : 0u);
-    unsigned fill = 0, queries = 0, done = 0;  // next fill and query tile that this stream has to take; halves before this piece
+    constexpr uint32_t kHalf = Tile<D>::kOperand / 2 >> 4;
+    const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // the query rows are negated instead of the scale
+    unsigned buf = 0, phase = 0, query = 0;  // the next fill's buffer and the parity of its phase; the piece's first query tile
+    unsigned p_phase = 0, free_phase = 0;    // parities of the next phases: bit b of P buffer b's
+    // waits for the next fill; its buffer, or -1
+    auto take = [&] {
+        if (!warp_wait(&sm.kv_full[buf], phase, a.err, abort)) return -1;
+        tc_fence_after();
+        const int got = (int)buf;
+        if (++buf == N) buf = 0, phase ^= 1;
+        return got;
+    };
+    auto scores = [&](uint64_t qd, uint64_t kd, uint32_t desc) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            mma_ss(s_at, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4), desc, k > 0);
+        tc_commit(&sm.s_full[t]);
+    };
+    // output of P buffer b times 64 rows of V
+    auto output = [&](int b, bool paired, uint64_t vd, bool add) {
+        if (!warp_wait(&sm.p_full[t][b], p_phase >> b & 1, a.err, abort)) return false;
+        p_phase ^= 1u << b;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+            mma_ts(o_at, s_at + weights_at(paired, b) + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), add || k > 0);
+        tc_commit(&sm.pv_done[t][b]);
+        return true;
+    };
 #pragma unroll 1
     for (unsigned piece = 0;; ++piece) {
         Job job;
         if (!read_job(sm, piece, &job, a.err) || job.begin == job.end) return;
-        const int n = job.end - job.begin, jobs = n * (job.paired ? 2 : 1), halves = 2 * ((jobs + 1 - t) / 2);
-        const unsigned fills = fill, query = queries + (job.paired ? t : 0), qbuf = query & 1;
-        queries += job.paired ? 2 : 1;
-        auto pass = [&](unsigned to) {
-            for (; fill < to; ++fill) {
-                if (!warp_wait(&sm.kv_full[fill % N], (fill / N) & 1, a.err, abort)) return false;
-                if (one) mbar_arrive(&sm.kv_empty[fill % N]);
-            }
-            return true;
-        };
-        if (!warp_wait(&sm.q_full[qbuf], (query >> 1) & 1, a.err, abort)) return;
-        if (halves == 0 && one) mbar_arrive(&sm.q_free[qbuf]);
+        const int n = job.end - job.begin;
+        const unsigned mine = query + (job.paired ? t : 0), qbuf = mine & 1;
+        query += job.paired ? 2 : 1;
+        // (a stream that skips a pair's other tile: the phase before the one that it waits for is over, staged before one that it has seen)
+        if (!warp_wait(&sm.q_full[qbuf], mine >> 1 & 1, a.err, abort)) return;
         const uint64_t qd = q0 + (qbuf * Tile<D>::kOperand >> 4);
+        int at = take();
+        if (at < 0) return;
+        // (the scores before are in registers: their weights, which came later, were waited for)
+        if (job.paired) {
+            const uint32_t desc = idesc_of(kTile, false, kBf16) | negate;
+            scores(qd, k0 + (at * Tile<D>::kOperand >> 4), desc);
+            tc_commit(&sm.kv_empty[at]);
 #pragma unroll 1
-        for (int h = -1; h < halves; ++h) {
-            const int next = h + 1;
-            if (next < halves) {
-                const int tile = job.paired ? next >> 1 : (next & ~1) + t, half = next & 1;
-                const unsigned f = fills + key_fill(job.paired, tile), buf = f % N;
-                if (half == 0) {
-                    if (!(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
-                    fill = f + 1;  // (released behind the other half)
-                }
-                const unsigned at = done + next;
-                if (at > 0 && !warp_wait(&sm.s_free[t], (at - 1) & 1, a.err, abort)) return;
-                tc_fence_after();
-                const uint64_t kd = k0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(s_at, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4), s_desc, k > 0);
-                tc_commit(&sm.s_full[t]);
-                if (half == 1) tc_commit(&sm.kv_empty[buf]);
-                if (next == halves - 1) {
-                    tc_commit(&sm.q_free[qbuf]);
-                    if (job.paired) tc_commit(&sm.q_free[qbuf]);
+            for (int i = 0; i < n; ++i) {
+                if ((at = take()) < 0) return;
+                const uint64_t vd = v0 + (at * Tile<D>::kOperand >> 4);
+                if (!output(0, true, vd, i > 0) || !output(1, true, vd + kHalf, true)) return;
+                tc_commit(&sm.kv_empty[at]);
+                if (i + 1 < n) {
+                    if ((at = take()) < 0) return;
+                    scores(qd, k0 + (at * Tile<D>::kOperand >> 4), desc);
+                    tc_commit(&sm.kv_empty[at]);
                 }
             }
-            if (h >= 0) {
-                const int tile = job.paired ? h >> 1 : (h & ~1) + t, half = h & 1;
-                const unsigned f = fills + value_fill(job.paired, n, tile), buf = f % N;
-                if (half == 0) {
-                    if (!(pass(f) && warp_wait(&sm.kv_full[buf], (f / N) & 1, a.err, abort))) return;
-                    fill = f + 1;
+            tc_commit(&sm.q_free[qbuf]);
+        } else {
+            const uint32_t desc = idesc_of(kTile / 2, false, kBf16) | negate;
+            scores(qd, k0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, desc);
+            tc_commit(&sm.kv_empty[at]);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                if (i + 1 < n) {
+                    if ((at = take()) < 0 || !warp_wait(&sm.s_free[t], free_phase, a.err, abort)) return;
+                    free_phase ^= 1;
+                    tc_fence_after();
+                    scores(qd, k0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, desc);
+                    tc_commit(&sm.kv_empty[at]);
                 }
-                if (!warp_wait(&sm.p_full[t][half], ((done + h) >> 1) & 1, a.err, abort)) return;
-                tc_fence_after();
-                const uint64_t vd = v0 + ((buf * Tile<D>::kOperand + half * (Tile<D>::kOperand / 2)) >> 4);
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    mma_ts(o_at, weights_at(tmem, t, half) + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), h > 0 || k > 0);
-                tc_commit(&sm.pv_done[t][half]);
-                if (half == 1) tc_commit(&sm.kv_empty[buf]);
-                if (h == halves - 1) tc_commit(&sm.o_full[t]);
+                if ((at = take()) < 0 || !output(i & 1, false, v0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, i > 0)) return;
+                tc_commit(&sm.kv_empty[at]);
             }
         }
-        done += halves;
-        if (!pass(fills + 2 * n)) return;
+        tc_commit(&sm.q_free[qbuf]);
+        tc_commit(&sm.o_full[t]);
     }
 }
 
@@ -531,48 +539,58 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
     constexpr int RING = Tile<D>::kRing, kCleanRing = Tile<D>::kCleanRing;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane, group = a.num_heads / a.num_kv_heads;
     volatile int* abort = &sm.abort;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = scores_at(sm.tmem, t) + lanes, o_at = output_at<D>(sm.tmem, t) + lanes, other_o_at = output_at<D>(sm.tmem, t ^ 1) + lanes;
+    const uint32_t lanes = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lanes + t * 128, o_at = lanes + output_at<D>(t), other_o_at = lanes + output_at<D>(t ^ 1);
     // (kept above zero, so that masked scores stay -inf)
     const float factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-38f);
-    unsigned pieces = 0, done = 0, joins = 0, tiles_before = 0, cleaned_before = 0;  // so far: of this stream, halves; of all, tiles
+    unsigned pieces = 0, joins = 0, tiles_before = 0, cleaned = 0;  // so far
+    unsigned s_phase = 0, pv_phase = 3;  // parity of the next phase of s_full; of the last one of pv_done: bit b of P buffer b's
 #pragma unroll 1
     for (unsigned piece = 0;; ++piece) {
         Job job;
         if (!read_job(sm, piece, &job, a.err) || job.begin == job.end) return;
-        const int n = job.end - job.begin, jobs = n * (job.paired ? 2 : 1), halves = 2 * ((jobs + 1 - t) / 2);
-        const int base = job.L - job.n, first_clean = max(job.begin, first_cleaned(job));
-        const unsigned tiles_now = tiles_before, cleaned_now = cleaned_before;
-        tiles_before += n;
-        cleaned_before += max(0, job.end - first_clean);
-        if (halves == 0) continue;  // a single tile in a split piece is stream 0's
-        const int first = job.row0 + (job.paired ? t * kTile : 0), v = first + r, node = v / group;  // row of the request
+        const bool paired = job.paired;
+        const int n = job.end - job.begin, base = job.L - job.n;
+        const int first = job.row0 + (paired ? t * kTile : 0), v = first + r, node = v / group;  // row of the request
         const bool live = v < job.n * group, warp_live = first + (warp & 3) * 32 < job.n * group;
         const uint64_t* words = reinterpret_cast<const uint64_t*>(a.tree_mask) + (live ? (size_t)(job.first_token + node) * a.mask_words : 0);
         float m = -INFINITY, l = 0.f;  // the row's reference of exponents, the sum of its exponentials
         bool noted = false;
-        uint64_t seen[2] = {~0ull, ~0ull};
+        uint64_t seen[2] = {0, 0};     // of the tile's halves, where V is cleaned
+        const int steps = paired ? 2 * n : n;
 #pragma unroll 1
-        for (int h = 0; h < halves; ++h, ++done) {
-            const int half = h & 1, local = job.paired ? h >> 1 : (h & ~1) + t, tile = job.begin + local;
-            const int p0 = tile * kTile, slot = (tiles_now + local) % RING;
-            if (!warp_wait(&sm.s_full[t], done & 1, a.err, abort)) return;
-            tc_fence_after();
+        for (int step = 0; step < steps; ++step) {
+            const int half = paired ? step & 1 : t, local = paired ? step >> 1 : step, b = step & 1;
+            const int p0 = (job.begin + local) * kTile;
+            if (!paired || half == 0) {
+                if (!warp_wait(&sm.s_full[t], s_phase, a.err, abort)) return;
+                s_phase ^= 1;
+                tc_fence_after();
+            }
+            const bool last = !paired && step + 1 == steps;
+            const unsigned masked = sm.masked[(tiles_before + local) % RING];
+            const bool clean = (masked >> 31) && (!paired || half == 1);  // V of this tile is cleaned
             if (!warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
-                if (lane == 0) {
-                    mbar_arrive(&sm.s_free[t]);
-                    mbar_arrive(&sm.p_full[t][half]);
+                if (clean) {
+                    if (!warp_wait(&sm.clean_full[cleaned % kCleanRing], (cleaned / kCleanRing) & 1, a.err, abort)) return;
+                    ++cleaned;
                 }
+                if (lane == 0) {
+                    if (!paired && !last) mbar_arrive(&sm.s_free[t]);
+                    mbar_arrive(&sm.p_full[t][b]);
+                }
+                pv_phase ^= 1u << b;
                 continue;
             }
             uint32_t s[64];
-            tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-            const unsigned masked = sm.masked[slot];
+            tmem_ld32(s_at + scores_at(paired, half), *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(s_at + scores_at(paired, half) + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tc_wait_ld(s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_free[t]);
+            if (!paired && !last) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.s_free[t]);
+            }
             if (masked) {  // a block that is not there, or (bit 31) a tile with nodes or the context's end
                 const uint64_t mine =
                     live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
@@ -586,11 +604,13 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                 }
             }
             const float top = row_max(s) * factor;
-            if (h == 0) {
+            if (step == 0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                // The output so far has to be there.  (The phase before the one that is meant is over, for the reason below.)
-                if (!warp_wait(&sm.pv_done[t][half ^ 1], ((done - 1) >> 1) & 1, a.err, abort)) return;
+                // The output so far has to be there.  (The phase before the one that is meant is over: these scores were issued behind the
+                // output before the last, or in a pair behind all of the tile before, and a commit waits for all products before it.  So
+                // P's place is free too.)
+                if (!warp_wait(&sm.pv_done[t][b ^ 1], pv_phase >> (b ^ 1) & 1, a.err, abort)) return;
                 tc_fence_after();
                 const float mn = fmaxf(m, top);
                 const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
@@ -606,14 +626,15 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                     tmem_st16(o_at + c, o);
                 }
             }
-            // (The weights of the half before the last lie where these go.  They have been read: the output that reads them was issued before
-            // this half's scores, whose commit waits for all products before it.)
-            l += row_exp<T>(s, weights_at(sm.tmem, t, half) + lanes, factor, m == -INFINITY ? 0.f : m);
-            if (half == 1 && (masked >> 31)) {  // a tile whose V was cleaned
-                const unsigned c = cleaned_now + (tile - first_clean), note = c % kCleanRing;
-                if (!warp_wait(&sm.clean_full[note], (c / kCleanRing) & 1, a.err, abort)) return;
+            l += row_exp<T>(s, s_at + weights_at(paired, b), factor, m == -INFINITY ? 0.f : m);
+            pv_phase ^= 1u << b;
+            if (clean) {
+                const unsigned note = cleaned % kCleanRing;
+                if (!warp_wait(&sm.clean_full[note], (cleaned / kCleanRing) & 1, a.err, abort)) return;
+                ++cleaned;
                 if (sm.special[note]) {
                     const int from = max(0, base - p0);
+                    if (!paired) seen[t ^ 1] = 0;
 #pragma unroll 1
                     for (int sign = 0; sign < 2; ++sign) {
 #pragma unroll 1
@@ -621,7 +642,8 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                             uint32_t bits = noted ? notes.row[t][sign][r][i] : 0u;
 #pragma unroll 1
                             for (int k = from; k < kTile; ++k)
-                                if (seen[k >> 6] >> (k & 63) & 1) bits |= *reinterpret_cast<const uint32_t*>(&notes.at[note][sign][k][4 * i]);
+                                if ((k < 64 ? seen[0] : seen[1]) >> (k & 63) & 1)
+                                    bits |= *reinterpret_cast<const uint32_t*>(&notes.at[note][sign][k][4 * i]);
                             notes.row[t][sign][r][i] = bits;
                         }
                     }
@@ -631,11 +653,12 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
+            if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
         }
+        tiles_before += n;
 
         // the piece's result
-        const bool cut = job.begin > 0 || job.end < job.tiles, join = !job.paired && jobs > 1;
+        const bool cut = job.begin > 0 || job.end < job.tiles, join = !paired;
         if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
         tc_fence_after();
         ++pieces;
@@ -658,7 +681,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
             if (__float_as_uint(o.y) >> 31) notes_from |= 2u >> t;
         }
         if (warp_live) {
-            float* rec = ws.records + ((size_t)blockIdx.x * 4 + (job.begin > 0 ? 0 : 2) + (job.paired ? t : 0)) * record_floats(D);
+            float* rec = ws.records + ((size_t)blockIdx.x * 4 + (job.begin > 0 ? 0 : 2) + (paired ? t : 0)) * record_floats(D);
             const long long row_at = live ? ((long long)(job.first_token + node) * a.num_heads + job.kvh * group + (v - node * group)) * D : 0;
             if (!cut) f0 *= l == 0.f ? 0.f : 1.f / l, f1 *= l == 0.f ? 0.f : 1.f / l;
             if (l != l) notes_from = 0;  // (NaN everywhere)
