@@ -38,7 +38,7 @@ constexpr int kSoftmaxWarps = 8;  // four per stream
 constexpr int kIssueWarp = kSoftmaxWarps;  // two, one per stream
 constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1, kQueryWarp = kCleanWarp + 1;
 constexpr int kThreads = (kQueryWarp + 1) * 32;
-constexpr int kPieces = 4;  // pieces of the share that the roles may be apart
+constexpr int kPieces = 4;  // pieces of the share that the look-ahead warp may be ahead of the others
 
 struct TreeRule {
     static constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 16;
@@ -113,14 +113,11 @@ __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
 // The first key tile whose V is cleaned: the one with the request's first node (or the context's end).
 __device__ __forceinline__ int first_cleaned(const Job& j) { return max(0, j.L - j.n) / kTile; }
 
-// Tensor memory: 128 columns per stream for scores and the weights P made of them (32 columns for 64 positions), and behind both streams'
-// D columns of output each.
-//   paired  scores of the whole tile; P of a half goes where its first half's scores were.  While one stream is at its softmax the other's
-//           products run: a product of 128 columns of scores takes 66 cycles where two of 64 take 100, since it reads the query rows once.
-//   split   64 columns of scores, and twice 32 of P, in turn by key tiles: the next tile's scores can be made as soon as these are in
-//           registers, and are ready when their turn comes.
-__device__ __forceinline__ uint32_t scores_at(bool paired, int half) { return paired ? 64 * half : 0; }
-__device__ __forceinline__ uint32_t weights_at(bool paired, int buffer) { return 32 * buffer + (paired ? 0 : 64); }
+// Tensor memory: per stream 64 columns of scores, then twice 32 of the weights P made of them, in turn; behind both streams' D columns of
+// output each.  The next scores can be made as soon as these are in registers, and are ready when their turn comes.  (P in the scores'
+// place, scores of a pair in products of 128 columns, 66 cycles where two of 64 take 100: every tile waited for its products,
+// 4570 cycles a tile, and as long with the streams taking turns.)
+constexpr int kWeightsAt = 64;
 template <int D>
 __device__ __forceinline__ uint32_t output_at(int t) { return 256 + t * D; }
 
@@ -340,20 +337,28 @@ __device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>&
         if (++buf == N) buf = 0, phase ^= 1;
         return got;
     };
-    auto scores = [&](uint64_t qd, uint64_t kd, uint32_t desc) {
+    // scores of 64 rows of K, once those before are in registers
+    const uint32_t desc = idesc_of(kTile / 2, false, kBf16) | negate;
+    auto scores = [&](uint64_t qd, uint64_t kd, bool first) {
+        if (!first) {
+            if (!warp_wait(&sm.s_free[t], free_phase, a.err, abort)) return false;
+            free_phase ^= 1;
+            tc_fence_after();
+        }
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
             mma_ss(s_at, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4), desc, k > 0);
         tc_commit(&sm.s_full[t]);
+        return true;
     };
     // output of P buffer b times 64 rows of V
-    auto output = [&](int b, bool paired, uint64_t vd, bool add) {
+    auto output = [&](int b, uint64_t vd, bool add) {
         if (!warp_wait(&sm.p_full[t][b], p_phase >> b & 1, a.err, abort)) return false;
         p_phase ^= 1u << b;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
-            mma_ts(o_at, s_at + weights_at(paired, b) + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), add || k > 0);
+            mma_ts(o_at, s_at + kWeightsAt + 32 * b + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), add || k > 0);
         tc_commit(&sm.pv_done[t][b]);
         return true;
     };
@@ -369,39 +374,39 @@ __device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>&
         const uint64_t qd = q0 + (qbuf * Tile<D>::kOperand >> 4);
         int at = take();
         if (at < 0) return;
-        // (the scores before are in registers: their weights, which came later, were waited for)
+        // (the last scores of the piece before are in registers: their weights, which came later, were waited for)
+        uint64_t kd = k0 + (at * Tile<D>::kOperand >> 4);
         if (job.paired) {
-            const uint32_t desc = idesc_of(kTile, false, kBf16) | negate;
-            scores(qd, k0 + (at * Tile<D>::kOperand >> 4), desc);
-            tc_commit(&sm.kv_empty[at]);
+            scores(qd, kd, true);
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                if ((at = take()) < 0) return;
-                const uint64_t vd = v0 + (at * Tile<D>::kOperand >> 4);
-                if (!output(0, true, vd, i > 0) || !output(1, true, vd + kHalf, true)) return;
+                if (!scores(qd, kd + kHalf, false)) return;
                 tc_commit(&sm.kv_empty[at]);
+                const int v = take();
+                if (v < 0) return;
+                const uint64_t vd = v0 + (v * Tile<D>::kOperand >> 4);
+                if (!output(0, vd, i > 0)) return;
                 if (i + 1 < n) {
                     if ((at = take()) < 0) return;
-                    scores(qd, k0 + (at * Tile<D>::kOperand >> 4), desc);
-                    tc_commit(&sm.kv_empty[at]);
+                    kd = k0 + (at * Tile<D>::kOperand >> 4);
+                    if (!scores(qd, kd, false)) return;
                 }
+                if (!output(1, vd + kHalf, true)) return;
+                tc_commit(&sm.kv_empty[v]);
             }
             tc_commit(&sm.q_free[qbuf]);
         } else {
-            const uint32_t desc = idesc_of(kTile / 2, false, kBf16) | negate;
-            scores(qd, k0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, desc);
+            scores(qd, kd + t * kHalf, true);
             tc_commit(&sm.kv_empty[at]);
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 if (i + 1 < n) {
-                    if ((at = take()) < 0 || !warp_wait(&sm.s_free[t], free_phase, a.err, abort)) return;
-                    free_phase ^= 1;
-                    tc_fence_after();
-                    scores(qd, k0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, desc);
+                    if ((at = take()) < 0 || !scores(qd, k0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, false)) return;
                     tc_commit(&sm.kv_empty[at]);
                 }
-                if ((at = take()) < 0 || !output(i & 1, false, v0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, i > 0)) return;
-                tc_commit(&sm.kv_empty[at]);
+                const int v = take();
+                if (v < 0 || !output(i & 1, v0 + (v * Tile<D>::kOperand >> 4) + t * kHalf, i > 0)) return;
+                tc_commit(&sm.kv_empty[v]);
             }
         }
         tc_commit(&sm.q_free[qbuf]);
@@ -472,12 +477,17 @@ __device__ __forceinline__ uint64_t seen_from(const uint64_t* words, int num_wor
     return seen;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
+}
 __device__ __forceinline__ float row_max(const uint32_t (&s)[64]) {
     float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
 #pragma unroll
     for (int i = 0; i < 64; i += 8)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = fmaxf(x[j], fmaxf(__uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1])));
+        for (int j = 0; j < 4; ++j) x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
     return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 }
 
@@ -562,12 +572,10 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
         for (int step = 0; step < steps; ++step) {
             const int half = paired ? step & 1 : t, local = paired ? step >> 1 : step, b = step & 1;
             const int p0 = (job.begin + local) * kTile;
-            if (!paired || half == 0) {
-                if (!warp_wait(&sm.s_full[t], s_phase, a.err, abort)) return;
-                s_phase ^= 1;
-                tc_fence_after();
-            }
-            const bool last = !paired && step + 1 == steps;
+            if (!warp_wait(&sm.s_full[t], s_phase, a.err, abort)) return;
+            s_phase ^= 1;
+            tc_fence_after();
+            const bool last = step + 1 == steps;
             const unsigned masked = sm.masked[(tiles_before + local) % RING];
             const bool clean = (masked >> 31) && (!paired || half == 1);  // V of this tile is cleaned
             if (!warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
@@ -576,21 +584,19 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                     ++cleaned;
                 }
                 if (lane == 0) {
-                    if (!paired && !last) mbar_arrive(&sm.s_free[t]);
+                    if (!last) mbar_arrive(&sm.s_free[t]);
                     mbar_arrive(&sm.p_full[t][b]);
                 }
                 pv_phase ^= 1u << b;
                 continue;
             }
             uint32_t s[64];
-            tmem_ld32(s_at + scores_at(paired, half), *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld32(s_at + scores_at(paired, half) + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
             tc_wait_ld(s);
-            if (!paired && !last) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.s_free[t]);
-            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && !last) mbar_arrive(&sm.s_free[t]);
             if (masked) {  // a block that is not there, or (bit 31) a tile with nodes or the context's end
                 const uint64_t mine =
                     live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
@@ -608,8 +614,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                 m = top;
             } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
                 // The output so far has to be there.  (The phase before the one that is meant is over: these scores were issued behind the
-                // output before the last, or in a pair behind all of the tile before, and a commit waits for all products before it.  So
-                // P's place is free too.)
+                // output before the last, and a commit waits for all products before it.  So P's place is free too.)
                 if (!warp_wait(&sm.pv_done[t][b ^ 1], pv_phase >> (b ^ 1) & 1, a.err, abort)) return;
                 tc_fence_after();
                 const float mn = fmaxf(m, top);
@@ -626,7 +631,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                     tmem_st16(o_at + c, o);
                 }
             }
-            l += row_exp<T>(s, s_at + weights_at(paired, b), factor, m == -INFINITY ? 0.f : m);
+            l += row_exp<T>(s, s_at + kWeightsAt + 32 * b, factor, m == -INFINITY ? 0.f : m);
             pv_phase ^= 1u << b;
             if (clean) {
                 const unsigned note = cleaned % kCleanRing;
