@@ -37,7 +37,7 @@ namespace {
 constexpr int kSoftmaxWarps = 8;  // four per stream
 constexpr int kIssueWarp = kSoftmaxWarps;  // two, one per stream
 constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1, kQueryWarp = kCleanWarp + 1;
-constexpr int kThreads = (kQueryWarp + 1) * 32;
+constexpr int kThreads = 512;  // four warpgroups, so that registers can go from the others' to the softmax's
 constexpr int kPieces = 4;  // pieces of the share that the look-ahead warp may be ahead of the others
 
 struct TreeRule {
@@ -122,7 +122,7 @@ template <int D>
 __device__ __forceinline__ uint32_t output_at(int t) { return 256 + t * D; }
 
 // Piece i of the share, for a warp of any role but the look-ahead's, which writes them; false if a wait gave up.
-constexpr int kReaders = kThreads / 32 - 1;
+constexpr int kReaders = kQueryWarp;  // (all roles' warps but one)
 template <int D>
 __device__ __forceinline__ bool read_job(Smem<D>& sm, unsigned i, Job* job, unsigned* err) {
     if (!warp_wait(&sm.job_full[i % kPieces], (i / kPieces) & 1, err, &sm.abort)) return false;
@@ -566,7 +566,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
         const uint64_t* words = reinterpret_cast<const uint64_t*>(a.tree_mask) + (live ? (size_t)(job.first_token + node) * a.mask_words : 0);
         float m = -INFINITY, l = 0.f;  // the row's reference of exponents, the sum of its exponentials
         bool noted = false;
-        uint64_t seen[2] = {0, 0};     // of the tile's halves, where V is cleaned
+        uint64_t seen0 = 0, seen1 = 0;  // of the tile's halves, where V is cleaned (of a split piece this stream's)
         const int steps = paired ? 2 * n : n;
 #pragma unroll 1
         for (int step = 0; step < steps; ++step) {
@@ -590,48 +590,55 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                 pv_phase ^= 1u << b;
                 continue;
             }
-            uint32_t s[64];
-            tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-            tc_wait_ld(s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0 && !last) mbar_arrive(&sm.s_free[t]);
-            if (masked) {  // a block that is not there, or (bit 31) a tile with nodes or the context's end
-                const uint64_t mine =
-                    live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
-                if (half == 0) seen[0] = mine;
-                else seen[1] = mine;
-                const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
+            // The half's weights, from its scores.  (A body for either case: where only the masking is conditional, the 64 scores are moved to
+            // other registers on the way around it, 135 instructions of 456.)
+            auto weigh = [&](auto edge) {
+                uint32_t s[64];
+                tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                tc_wait_ld(s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && !last) mbar_arrive(&sm.s_free[t]);
+                if constexpr (decltype(edge)::value) {
+                    const uint64_t mine =
+                        live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
+                    if (half == 0) seen0 = mine;
+                    else seen1 = mine;
+                    const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (!(lo >> i & 1)) s[i] = 0xff800000u;
-                    if (!(hi >> i & 1)) s[32 + i] = 0xff800000u;
+                    for (int i = 0; i < 32; ++i) {
+                        if (!(lo >> i & 1)) s[i] = 0xff800000u;
+                        if (!(hi >> i & 1)) s[32 + i] = 0xff800000u;
+                    }
                 }
-            }
-            const float top = row_max(s) * factor;
-            if (step == 0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                // The output so far has to be there.  (The phase before the one that is meant is over: these scores were issued behind the
-                // output before the last, and a commit waits for all products before it.  So P's place is free too.)
-                if (!warp_wait(&sm.pv_done[t][b ^ 1], pv_phase >> (b ^ 1) & 1, a.err, abort)) return;
-                tc_fence_after();
-                const float mn = fmaxf(m, top);
-                const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-                l *= f;
-                m = mn;
+                const float top = row_max(s) * factor;
+                if (step == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                    // The output so far has to be there.  (The phase before the one that is meant is over: these scores were issued behind the
+                    // output before the last, and a commit waits for all products before it.  So P's place is free too.)
+                    if (!warp_wait(&sm.pv_done[t][b ^ 1], pv_phase >> (b ^ 1) & 1, a.err, abort)) return false;
+                    tc_fence_after();
+                    const float mn = fmaxf(m, top);
+                    const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                    l *= f;
+                    m = mn;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_at + c, o);
-                    tc_wait_ld(o);
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + c, o);
+                        tc_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st16(o_at + c, o);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st16(o_at + c, o);
+                    }
                 }
-            }
-            l += row_exp<T>(s, s_at + kWeightsAt + 32 * b, factor, m == -INFINITY ? 0.f : m);
+                l += row_exp<T>(s, s_at + kWeightsAt + 32 * b, factor, m == -INFINITY ? 0.f : m);
+                return true;
+            };
+            // edge: a block that is not there, or (bit 31) a tile with nodes or the context's end
+            if (!(masked ? weigh(std::true_type{}) : weigh(std::false_type{}))) return;
             pv_phase ^= 1u << b;
             if (clean) {
                 const unsigned note = cleaned % kCleanRing;
@@ -639,7 +646,6 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                 ++cleaned;
                 if (sm.special[note]) {
                     const int from = max(0, base - p0);
-                    if (!paired) seen[t ^ 1] = 0;
 #pragma unroll 1
                     for (int sign = 0; sign < 2; ++sign) {
 #pragma unroll 1
@@ -647,7 +653,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                             uint32_t bits = noted ? notes.row[t][sign][r][i] : 0u;
 #pragma unroll 1
                             for (int k = from; k < kTile; ++k)
-                                if ((k < 64 ? seen[0] : seen[1]) >> (k & 63) & 1)
+                                if ((k < 64 ? seen0 : seen1) >> (k & 63) & 1)
                                     bits |= *reinterpret_cast<const uint32_t*>(&notes.at[note][sign][k][4 * i]);
                             notes.row[t][sign][r][i] = bits;
                         }
@@ -826,6 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
     griddep_wait();
     griddep_launch_dependents();
     Notes<D>& notes = all_notes[blockIdx.x];
+    // 512 threads may have 128 registers each.  Of 16 warps' 2048, the softmax's eight take 168, with which they spill none (wide trees 176
+    // to 161 us), and the others 80.
+    if (warp < kSoftmaxWarps)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp < kSoftmaxWarps) {
         softmax_rows<T, D, BS>(a, ws, sm, notes);
     } else if (warp == kCopyWarp) {
@@ -836,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
         clean_tiles<T, D, BS>(a, sm, notes);
     } else if (warp == kQueryWarp) {
         stage_queries<T, D>(a, sm);
-    } else {
+    } else if (warp < kCopyWarp) {
         const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
         issue_products<T, D>(a, sm, t);
         if (__any_sync(0xffffffffu, sm.abort)) {  // products still in flight read shared and tensor memory
