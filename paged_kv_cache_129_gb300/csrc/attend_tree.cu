@@ -9,7 +9,9 @@
 //   paired  two row tiles share every key tile, a stream each;
 //   split   a single row tile (small trees, single tokens, the rest of a wide tree): each stream takes one half, 64 positions, of every key
 //           tile, and they join their results at the end.
-// Work.  Equal shares of all units' key tiles per SM, see attend_units.cuh.
+// Work.  A unit is (request, kv head, pair of row tiles).  All units' key tiles are laid end to end, weighted by their cost, and cut into one
+// equal contiguous share per CTA, of which there is one per SM; every CTA adds up the requests' costs for itself and finds its own.  Units
+// cut by a share boundary leave float32 partial results (two slots per CTA), joined by a second kernel.
 // Operands.  K and V go from the cache's blocks straight into operand tiles, one bulk tensor copy per block: a block's rows as groups of
 // eight by panels of 64 elements, which is the order that both products read (K by rows, V by columns) with uniform strides.  A block
 // that is not there is copied from behind the pool, as zeros.
@@ -24,9 +26,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "attend_units.cuh"
 #include "pa_common.cuh"
-#include "pa_internal.h"
 #include "tcgen05.cuh"
 #include "tree_ops.h"
 
@@ -34,19 +34,128 @@ namespace pa {
 
 namespace {
 
+constexpr int kJoinThreads = 256;
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+__host__ __device__ inline size_t record_floats(int D) { return (size_t)kTile * (D + 2); }
+
 constexpr int kSoftmaxWarps = 8;  // four per stream
 constexpr int kIssueWarp = kSoftmaxWarps;  // two, one per stream
 constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1, kQueryWarp = kCleanWarp + 1;
 constexpr int kThreads = 512;  // four warpgroups, so that registers can go from the others' to the softmax's
 constexpr int kPieces = 4;  // pieces of the share that the look-ahead warp may be ahead of the others
 
-struct TreeRule {
-    static constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 16;
-    static constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
-    static __device__ __forceinline__ int tiles(int L, int, int, int) { return max(1, (L + kTile - 1) / kTile); }
-    static __device__ __forceinline__ bool refuses(const TreeAttendArgs& a, int L, int n) { return L < n || n > 64 * a.mask_words; }
+// Cost of work in shares: of a key tile of a pair and of a split piece, and of a unit besides its tiles.
+constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 16;
+constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
+
+// A request as the shares see it: n nodes on L positions.
+struct Request {
+    int L, n, first_token, rows, tiles;
+    bool bad;  // its lengths or offsets are none
+    Request() = default;
+    __device__ __forceinline__ Request(const TreeAttendArgs& a, int b) {
+        const int given = a.context_lens[b], lo = a.q_offsets[b], hi = a.q_offsets[b + 1], most = a.max_blocks * a.block_size;
+        const bool run = is_run(lo, hi, a.num_tokens);
+        L = max(0, min(given, most));
+        n = run ? hi - lo : 0;
+        bad = !run || given < n || given > most;
+        first_token = lo;
+        rows = n * a.group;
+        tiles = max(1, (L + kTile - 1) / kTile);
+    }
+    __device__ __forceinline__ int entries() const { return (rows + 2 * kTile - 1) / (2 * kTile); }  // pairs of row tiles
+    __device__ __forceinline__ bool paired(int e) const { return rows - e * 2 * kTile > kTile; }
+    __device__ __forceinline__ long long cost(bool pair) const { return kUnitCost + (long long)tiles * (pair ? kPairedCost : kSplitCost); }
+    __device__ __forceinline__ long long head_cost() const {  // of a kv head's units
+        const int full = rows / (2 * kTile), rest = rows % (2 * kTile);
+        return full * cost(true) + (rest ? cost(rest > kTile) : 0);
+    }
 };
-using Walk = UnitWalk<TreeRule>;
+
+// Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).
+__device__ __forceinline__ int tiles_in(long long x, int tiles, bool paired) {  // (a unit's tiles: below 2^24)
+    const unsigned cost = (unsigned)max(0ll, min(x - kUnitCost, (long long)tiles * (paired ? kPairedCost : kSplitCost)));
+    return (int)(paired ? (cost + kPairedCost - 1) / kPairedCost : (cost + kSplitCost - 1) / kSplitCost);
+}
+
+// x / y; of what fits 32 bits, which is nearly all, in a fifth of the time.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return ((unsigned long long)(x | y) >> 32) == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+
+// Where a CTA's share [pos, stop) of the total cost begins: a unit that starts at `unit`.
+struct Start {
+    long long pos, stop, unit, share;
+    int seq, kvh, entry;
+    Request r;
+};
+
+// A boundary that cuts a unit: what the joining kernel needs.  CTAs first .. last have parts of it; last 0: nothing to join.
+struct Seam {
+    long long unit, share;
+    int seq, kvh, row0, rows, tiles, paired, first, last;
+};
+
+struct Scratch {
+    long long cost[kThreads / 32], rows[kThreads / 32];
+    Start start;
+};
+
+// The share of this CTA; all its threads.  A run of requests per thread, their costs summed over the CTA; whoever's run the share begins
+// in finds the unit.
+__device__ __forceinline__ Start find_share(const TreeAttendArgs& a, Scratch& sc) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.num_seqs, H = a.num_kv_heads;
+    const int per = (B + kThreads - 1) / kThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    long long cost = 0, rows = 0, head = 0;
+    Request r{};
+    for (int b = b0; b < b1; ++b) {
+        r = Request(a, b);
+        head = r.head_cost();
+        cost += head * H;
+        rows += r.n;
+        if (blockIdx.x == 0 && (r.bad || r.n > 64 * a.mask_words)) atomicOr(a.err, kErrBadContext);
+    }
+    long long sum = cost;  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, o), y = __shfl_xor_sync(0xffffffffu, rows, o);
+        if (lane >= o) sum += x;
+        rows += y;
+    }
+    if (lane == 31) sc.cost[warp] = sum, sc.rows[warp] = rows;
+    if (tid == 0) sc.start.seq = -1;
+    __syncthreads();
+    long long total = 0, before = 0, all_rows = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) before = total;
+        total += sc.cost[w];
+        all_rows += sc.rows[w];
+    }
+    if (all_rows > a.num_tokens) {  // runs that overlap
+        if (blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrBadContext);
+        total = 0;
+    }
+    const long long even = quotient(total + gridDim.x - 1, gridDim.x), share = even > kMinShare ? even : kMinShare, pos = share * blockIdx.x;
+    long long at = before + sum - cost;
+    if (pos < total && at <= pos && pos < at + cost) {
+        int b = b1 - 1;
+        if (per > 1)  // (else the only request is at hand)
+            for (b = b0;; ++b) {
+                r = Request(a, b);
+                head = r.head_cost();
+                if (pos < at + head * H) break;
+                at += head * H;
+            }
+        const int kvh = (int)quotient(pos - at, head);
+        at += kvh * head;
+        const long long pair = r.cost(true);
+        const int e = min((int)quotient(pos - at, pair), r.rows / (2 * kTile));
+        sc.start = Start{pos, min(pos + share, total), at + e * pair, share, b, kvh, e, r};
+    }
+    __syncthreads();
+    return sc.start;
+}
 
 // Sizes and places of the operand tiles.  A key tile is 16 groups of 8 positions; a group is D / 64 panels of 8 rows by 128 bytes,
 // swizzled (16-byte unit u of row r at u ^ r), which is how a block's copy leaves it.
@@ -64,7 +173,7 @@ struct Tile {
 
 // What a piece of the share is to every role; begin == end behind the last one.
 struct Job {
-    int L, n, first_token;  // length, nodes, row of the first node
+    int L, n, first_token, seq;  // length, nodes, row of the first node
     int row0, kvh, tiles, begin, end, paired;
 };
 
@@ -139,22 +248,46 @@ __device__ __forceinline__ bool read_job(Smem<D>& sm, unsigned i, Job* job, unsi
 // streams, which release in order; V of tile g is fill 2g + 2 at most.  Tile i is looked at once K of tile i - kAhead is copied: with g = i - kRing,
 // 2 (i - kRing) + 2 <= 2 (i - kAhead) - 1 - kBuffers.
 template <int D, int BS>
-__device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm) {
+__device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, Seam* seams, Smem<D>& sm, const Start& start) {
     constexpr int BLOCKS = kTile / BS, RING = Tile<D>::kRing, AHEAD = Tile<D>::kAhead;
     static_assert(2 * (RING - AHEAD) >= Tile<D>::kBuffers + 3 && AHEAD > 1, "a slot's tile is done with when it is written again");
     const int lane = threadIdx.x & 31;
     const int behind = a.num_blocks * a.num_kv_heads * (BS / 8);  // the first group behind the pool: copied as zeros
-    Walk walk(ws, a.num_kv_heads, blockIdx.x, gridDim.x);
+    int seq = start.seq, kvh = start.kvh, e = start.entry;
+    long long unit = start.unit;  // where the unit begins
+    bool more = seq >= 0;
+    Request r = start.r;
+    // the boundary at this share's start is the first inside the unit if the share before begins at the unit, or before it
+    if (lane == 0) {
+        Seam seam{};
+        if (more && start.pos > unit && start.pos - start.share <= unit)
+            seam = Seam{unit, start.share, seq, kvh, e * 2 * kTile, min(2 * kTile, r.rows - e * 2 * kTile), r.tiles, r.paired(e), (int)blockIdx.x - 1,
+                        (int)quotient(unit + r.cost(r.paired(e)) - 1, start.share)};
+        seams[blockIdx.x] = seam;
+    }
     unsigned tiles = 0;
 #pragma unroll 1
     for (unsigned i = 0;; ++i) {
-        Piece p{};
         Job j{};
-        const bool have = walk.next(&p);
-        if (have) {
-            const Item it = item_of(a, p);
-            j = Job{it.L, it.n, it.first_token, p.row0, p.kvh, p.tiles, p.begin, p.end, p.paired};
+        while (more && j.begin == j.end) {  // the next unit with tiles in the share
+            const bool pair = r.paired(e);
+            const long long cost = r.cost(pair);
+            j = Job{r.L, r.n, r.first_token, seq, e * 2 * kTile, kvh, r.tiles, tiles_in(start.pos - unit, r.tiles, pair),
+                    tiles_in(start.stop - unit, r.tiles, pair), pair};
+            unit += cost;
+            if (++e == r.entries()) {
+                e = 0;
+                if (++kvh == a.num_kv_heads) {
+                    kvh = 0;
+                    do {
+                        if (++seq == a.num_seqs) break;
+                        r = Request(a, seq);
+                    } while (r.rows == 0);
+                }
+            }
+            more = unit < start.stop && seq < a.num_seqs;
         }
+        const bool have = j.begin < j.end;
         if (i >= kPieces && !warp_wait(&sm.job_free[i % kPieces], (i / kPieces - 1) & 1, a.err, &sm.abort)) return;
         if (lane == 0) {
             sm.jobs[i % kPieces] = j;
@@ -162,14 +295,14 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, const Worksp
         }
         if (!have) return;
         const int used = (j.L + BS - 1) / BS, cleaned = first_cleaned(j);
-        const int32_t* table = a.block_tables + (size_t)p.seq * a.max_blocks;
-        // lane j < BLOCKS has block j of a tile
-        auto wanted = [&](int tile) { return lane < BLOCKS && tile < p.end && tile * BLOCKS + lane < used; };
-        int id = wanted(p.begin) ? table[p.begin * BLOCKS + lane] : -1;
-        for (int tile = p.begin; tile < p.end; ++tile, ++tiles) {
+        const int32_t* table = a.block_tables + (size_t)j.seq * a.max_blocks;
+        // lane l < BLOCKS has block l of a tile
+        auto wanted = [&](int tile) { return lane < BLOCKS && tile < j.end && tile * BLOCKS + lane < used; };
+        int id = wanted(j.begin) ? table[j.begin * BLOCKS + lane] : -1;
+        for (int tile = j.begin; tile < j.end; ++tile, ++tiles) {
             const bool mine = wanted(tile), in = mine && id >= 0 && id < a.num_blocks;
             if (mine && !in) atomicOr(a.err, kErrBadTable);
-            const int place = in ? (id * a.num_kv_heads + p.kvh) * (BS / 8) : behind;
+            const int place = in ? (id * a.num_kv_heads + j.kvh) * (BS / 8) : behind;
             id = wanted(tile + 1) ? table[(tile + 1) * BLOCKS + lane] : -1;
             const unsigned masked = __ballot_sync(0xffffffffu, mine && !in) | (tile >= cleaned ? 1u << 31 : 0u);
             if (tiles >= AHEAD) {
@@ -419,7 +552,7 @@ __device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>&
 template <typename T, int D>
 __device__ __forceinline__ void stage_queries(const TreeAttendArgs& a, Smem<D>& sm) {
     constexpr int LPR = D / 8, RPS = 32 / LPR;
-    const int lane = threadIdx.x & 31, sub = lane / LPR, i = lane % LPR, group = a.num_heads / a.num_kv_heads;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, i = lane % LPR, group = a.group;
     const T* query = static_cast<const T*>(a.query);
     unsigned tile = 0;
 #pragma unroll 1
@@ -454,11 +587,12 @@ __device__ __forceinline__ void stage_queries(const TreeAttendArgs& a, Smem<D>& 
 }
 
 // Which of the 64 positions from `at` on a row sees: those before the nodes (base), and its nodes; less the blocks in masked.
+// word0: the row's first word, read ahead.
 template <int BS>
-__device__ __forceinline__ uint64_t seen_from(const uint64_t* words, int num_words, int at, int base, int n, unsigned masked) {
+__device__ __forceinline__ uint64_t seen_from(const uint64_t* words, uint64_t word0, int num_words, int at, int base, int n, unsigned masked) {
     auto word = [&](int w) {
         const int left = n - 64 * w;
-        return w >= num_words || left <= 0 ? 0ull : words[w] & (left >= 64 ? ~0ull : (1ull << left) - 1);
+        return w >= num_words || left <= 0 ? 0ull : (w == 0 ? word0 : words[w]) & (left >= 64 ? ~0ull : (1ull << left) - 1);
     };
     const int node = at - base;
     uint64_t seen;
@@ -545,9 +679,9 @@ __device__ __forceinline__ void transpose8(uint4 (&x)[8]) {
 
 // A softmax warp: 32 rows of a stream's row tile, one per lane.
 template <typename T, int D, int BS>
-__device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Workspace& ws, Smem<D>& sm, Notes<D>& notes) {
+__device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* records, Smem<D>& sm, Notes<D>& notes) {
     constexpr int RING = Tile<D>::kRing, kCleanRing = Tile<D>::kCleanRing;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane, group = a.num_heads / a.num_kv_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, r = (warp & 3) * 32 + lane, group = a.group;
     volatile int* abort = &sm.abort;
     const uint32_t lanes = sm.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lanes + t * 128, o_at = lanes + output_at<D>(t), other_o_at = lanes + output_at<D>(t ^ 1);
@@ -564,6 +698,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
         const int first = job.row0 + (paired ? t * kTile : 0), v = first + r, node = v / group;  // row of the request
         const bool live = v < job.n * group, warp_live = first + (warp & 3) * 32 < job.n * group;
         const uint64_t* words = reinterpret_cast<const uint64_t*>(a.tree_mask) + (live ? (size_t)(job.first_token + node) * a.mask_words : 0);
+        const uint64_t word0 = words[0];
         float m = -INFINITY, l = 0.f;  // the row's reference of exponents, the sum of its exponentials
         bool noted = false;
         uint64_t seen0 = 0, seen1 = 0;  // of the tile's halves, where V is cleaned (of a split piece this stream's)
@@ -602,7 +737,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
                 if (lane == 0 && !last) mbar_arrive(&sm.s_free[t]);
                 if constexpr (decltype(edge)::value) {
                     const uint64_t mine =
-                        live ? seen_from<BS>(words, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
+                        live ? seen_from<BS>(words, word0, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
                     if (half == 0) seen0 = mine;
                     else seen1 = mine;
                     const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
@@ -692,7 +827,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
             if (__float_as_uint(o.y) >> 31) notes_from |= 2u >> t;
         }
         if (warp_live) {
-            float* rec = ws.records + ((size_t)blockIdx.x * 4 + (job.begin > 0 ? 0 : 2) + (paired ? t : 0)) * record_floats(D);
+            float* rec = records + ((size_t)blockIdx.x * 4 + (job.begin > 0 ? 0 : 2) + (paired ? t : 0)) * record_floats(D);
             const long long row_at = live ? ((long long)(job.first_token + node) * a.num_heads + job.kvh * group + (v - node * group)) * D : 0;
             if (!cut) f0 *= l == 0.f ? 0.f : 1.f / l, f1 *= l == 0.f ? 0.f : 1.f / l;
             if (l != l) notes_from = 0;  // (NaN everywhere)
@@ -784,12 +919,16 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, const Work
 }
 
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAttendArgs a, const Workspace ws, Notes<D>* all_notes,
+__global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAttendArgs a, Seam* seams, float* records, Notes<D>* all_notes,
                                                                   const __grid_constant__ CUtensorMap kmap,
                                                                   const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char raw_smem[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw_smem);
     const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
@@ -826,11 +965,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
         fence_barrier_init();
     }
     if (warp == kIssueWarp) tmem_alloc(&sm.tmem, 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     griddep_wait();
     griddep_launch_dependents();
+    static_assert(sizeof(Scratch) <= sizeof(sm.state), "the sums lie where the states will");
+    tc_fence_before();
+    const Start start = find_share(a, *reinterpret_cast<Scratch*>(&sm.state));  // (synchronises the CTA)
+    tc_fence_after();
     Notes<D>& notes = all_notes[blockIdx.x];
     // 512 threads may have 128 registers each.  Of 16 warps' 2048, the softmax's eight take 168, with which they spill none (wide trees 176
     // to 161 us), and the others 80.
@@ -839,11 +979,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp < kSoftmaxWarps) {
-        softmax_rows<T, D, BS>(a, ws, sm, notes);
+        softmax_rows<T, D, BS>(a, records, sm, notes);
     } else if (warp == kCopyWarp) {
         copy_tiles<D, BS>(a, sm, &kmap, &vmap);
     } else if (warp == kLookWarp) {
-        look_ahead<D, BS>(a, ws, sm);
+        look_ahead<D, BS>(a, seams, sm, start);
     } else if (warp == kCleanWarp) {
         clean_tiles<T, D, BS>(a, sm, notes);
     } else if (warp == kQueryWarp) {
@@ -864,43 +1004,108 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
     if (warp == kIssueWarp) tmem_free(sm.tmem, 512);
 }
 
-// Places in the workspace of a call.
-template <int D>
-size_t lay_out(int num_sms, size_t cap, char* base, Workspace* ws, Notes<D>** notes) {
-    const size_t records = 256 + align256((cap + 1) * sizeof(Entry)), at = records + (size_t)num_sms * 4 * record_floats(D) * sizeof(float);
-    if (ws) {
-        ws->head = reinterpret_cast<PlanHead*>(base);
-        ws->entries = reinterpret_cast<Entry*>(base + 256);
-        ws->records = reinterpret_cast<float*>(base + records);
-        *notes = reinterpret_cast<Notes<D>*>(base + at);
+// Joins the partial results of the units that share boundaries cut: CTA (boundary, rows), a warp per row, D / 32 elements per lane.  The
+// parts' maxima and sums are read by a lane each.
+constexpr int kJoinRows = kJoinThreads / 32, kJoinSplit = 16;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeAttendArgs a, const Seam* seams, const float* records) {
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int E = D / 32;
+    using Vec = typename std::conditional<E == 4, float4, float2>::type;
+    const Seam s = seams[blockIdx.x + 1];
+    if (s.last == 0) return;
+    const int lane = threadIdx.x & 31, group = a.group, first_token = a.q_offsets[s.seq];
+    auto cut = [&](int c) { return tiles_in(s.share * c - s.unit, s.tiles, s.paired); };  // CTA c has tiles [cut(c), cut(c + 1))
+    bool parts = false;  // (a boundary inside the cost may still fall before the first tile or behind the last)
+    for (int c = s.first + 1; c <= s.last; ++c) parts |= cut(c) > 0 && cut(c) < s.tiles;
+    if (!parts) return;
+    for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < s.rows; r += gridDim.y * kJoinRows) {
+        const int tile = r / kTile, rr = r % kTile;
+        float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = 0.f;
+        for (int c0 = s.first; c0 <= s.last; c0 += 32) {
+            const int c = c0 + lane, from = cut(c);
+            const bool has = c <= s.last && from < cut(c + 1);
+            const size_t at = ((size_t)c * 4 + (from > 0 ? 0 : 2) + tile) * record_floats(D);
+            const float mc = has ? records[at + rr] : -INFINITY, lc = has ? records[at + kTile + rr] : 0.f;
+            float mn = mc;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+            mn = fmaxf(mn, m);
+            // a part without a maximum is empty, unless its sum is NaN
+            const float weight = lc != lc ? 1.f : mc == -INFINITY ? 0.f : exp2_approx(mc - mn), f = l != l ? 1.f : m == -INFINITY ? 0.f : exp2_approx(m - mn);
+            float sum = lc * weight;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            l = l * f + sum;
+            m = mn;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] *= f;
+            unsigned left = __ballot_sync(0xffffffffu, has);
+            while (left) {
+                constexpr int kAtOnce = 4;
+                alignas(16) float x[kAtOnce][E], wj[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int j = left ? __ffs(left) - 1 : 0;
+                    wj[k] = left ? __shfl_sync(0xffffffffu, weight, j) : 0.f;
+                    const size_t part = __shfl_sync(0xffffffffu, at, j);
+                    if (left) *reinterpret_cast<Vec*>(x[k]) = *reinterpret_cast<const Vec*>(records + part + 2 * kTile + (size_t)rr * D + lane * E);
+                    else
+#pragma unroll
+                        for (int i = 0; i < E; ++i) x[k][i] = 0.f;
+                    left &= left - 1;
+                }
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) o[i] = fmaf(x[k][i], wj[k], o[i]);
+            }
+        }
+        const int v = s.row0 + r, node = v / group;
+        T* dst = static_cast<T*>(a.out) + ((size_t)(first_token + node) * a.num_heads + s.kvh * group + (v - node * group)) * D + lane * E;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint32_t y[E / 2];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) y[i] = round2<T>(make_float2(o[2 * i] * inv, o[2 * i + 1] * inv));
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = y[0];
     }
-    return at + (size_t)num_sms * sizeof(Notes<D>);
+}
+
+// Places in the workspace of a call: seams, then records [CTAs][2 slots][2 tiles][m 128 | l 128 | o 128 x D], then notes.
+template <int D>
+size_t lay_out(int num_sms, char* base, Seam** seams, float** records, Notes<D>** notes) {
+    const size_t first = align256((size_t)num_sms * sizeof(Seam)), second = first + (size_t)num_sms * 4 * record_floats(D) * sizeof(float);
+    if (base) {
+        *seams = reinterpret_cast<Seam*>(base);
+        *records = reinterpret_cast<float*>(base + first);
+        *notes = reinterpret_cast<Notes<D>*>(base + second);
+    }
+    return second + (size_t)num_sms * sizeof(Notes<D>);
 }
 
 template <typename T, int D, int BS>
 cudaError_t attend_typed(const TreeAttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
-    const int group = a.num_heads / a.num_kv_heads, ctas = a.num_sms;
-    const size_t cap = max_entries(a.num_seqs, a.num_tokens, group);
-    Workspace ws;
+    const int ctas = a.num_sms;
+    Seam* seams;
+    float* records;
     Notes<D>* notes;
-    lay_out<D>(a.num_sms, cap, static_cast<char*>(a.workspace), &ws, &notes);
-    cudaError_t e = launch_pdl(attend_plan_kernel<TreeAttendArgs, TreeRule>, dim3(1), dim3(kPlanThreads),
-                               (size_t)(a.num_seqs + 1) * sizeof(int), stream, a, ws, (int)cap);
-    if (e != cudaSuccess) return e;
+    lay_out<D>(ctas, static_cast<char*>(a.workspace), &seams, &records, &notes);
     const size_t smem = sizeof(Smem<D>);
-    e = cudaFuncSetAttribute(attend_tree_kernel<T, D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(attend_tree_kernel<T, D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_tree_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, ws, notes, kmap, vmap);
+    e = launch_pdl(attend_tree_kernel<T, D, BS>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, a, seams, records, notes, kmap, vmap);
     if (e != cudaSuccess || ctas < 2) return e;
-    return launch_pdl(attend_join_kernel<T, D, TreeAttendArgs, TreeRule>, dim3((unsigned)(ctas - 1), 8), dim3(kJoinThreads), 0, stream, a, ws,
-                      ctas);
+    return launch_pdl(join_tree_kernel<T, D>, dim3((unsigned)(ctas - 1), kJoinSplit), dim3(kJoinThreads), 0, stream, a, seams, records);
 }
 
 }  // namespace
 
-size_t attend_tree_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim) {
-    const size_t cap = max_entries(num_seqs, num_tokens, num_heads / num_kv_heads);
-    return head_dim == 64 ? lay_out<64>(num_sms, cap, nullptr, nullptr, nullptr) : lay_out<128>(num_sms, cap, nullptr, nullptr, nullptr);
+size_t attend_tree_workspace_bytes(int num_sms, int head_dim) {
+    return head_dim == 64 ? lay_out<64>(num_sms, nullptr, nullptr, nullptr, nullptr) : lay_out<128>(num_sms, nullptr, nullptr, nullptr, nullptr);
 }
 
 cudaError_t attend_tree_launch(const TreeAttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {

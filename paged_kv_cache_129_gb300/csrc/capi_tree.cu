@@ -177,10 +177,11 @@ int pa_attend_tree(void* out, const void* query, const void* key_cache, const vo
                     {q_offsets, 4ll * (num_seqs + 1), 4}});
     if (st != PA_OK) return st;
     TreeAttendArgs a{out, query, key_cache, value_cache, tree_mask, block_tables, context_lens, q_offsets, num_seqs, num_tokens, num_heads,
-                     num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, mask_words, dtype, scale, workspace, 0, nullptr};
+                     num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, mask_words, dtype, num_heads / num_kv_heads, scale,
+                     workspace, 0, nullptr};
     st = device_state(&a.err, &a.num_sms);
     if (st != PA_OK) return st;
-    const size_t need = attend_tree_workspace_bytes(a.num_sms, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim);
+    const size_t need = attend_tree_workspace_bytes(a.num_sms, head_dim);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return fail(PA_ERR_INVALID_ARG, "pa_attend_tree: needs a 256-byte aligned workspace of %zu bytes (%zu given)", need,
                     workspace ? workspace_bytes : (size_t)0);
@@ -202,7 +203,7 @@ size_t pa_attend_tree_workspace_size(int num_tokens, int num_seqs, int num_heads
     unsigned* err = nullptr;
     int sms = 0;
     if (device_state(&err, &sms) != PA_OK) return 0;
-    return attend_tree_workspace_bytes(sms, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim);
+    return attend_tree_workspace_bytes(sms, head_dim);
 }
 
 }  // extern "C"

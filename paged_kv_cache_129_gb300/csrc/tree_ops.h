@@ -83,6 +83,7 @@ struct TreeAttendArgs {
     const int32_t* context_lens;
     const int32_t* q_offsets;
     int num_seqs, num_tokens, num_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, mask_words, dtype;
+    int group;  // query heads of a kv head
     float scale;
     void* workspace;
     int num_sms;
@@ -94,7 +95,7 @@ cudaError_t accept_tree_launch(const AcceptArgs& a, cudaStream_t stream);
 cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, cudaStream_t stream);
 cudaError_t norm_rope_write_kv_launch(const NormRopeArgs& a, cudaStream_t stream);
 // Scratch of one attend_tree call.
-size_t attend_tree_workspace_bytes(int num_sms, int num_seqs, int num_tokens, int num_heads, int num_kv_heads, int head_dim);
+size_t attend_tree_workspace_bytes(int num_sms, int head_dim);
 // kmap, vmap: group_map()s of K and V.
 cudaError_t attend_tree_launch(const TreeAttendArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream);
 
