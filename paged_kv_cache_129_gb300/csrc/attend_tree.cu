@@ -72,10 +72,13 @@ struct Request {
     }
 };
 
-// Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).
+// Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).  A cut so near to
+// an end of the unit that the piece would cost more than its tiles goes to the end.
+constexpr int kSnap = 3;
 __device__ __forceinline__ int tiles_in(long long x, int tiles, bool paired) {  // (a unit's tiles: below 2^24)
     const unsigned cost = (unsigned)max(0ll, min(x - kUnitCost, (long long)tiles * (paired ? kPairedCost : kSplitCost)));
-    return (int)(paired ? (cost + kPairedCost - 1) / kPairedCost : (cost + kSplitCost - 1) / kSplitCost);
+    const int cut = (int)(paired ? (cost + kPairedCost - 1) / kPairedCost : (cost + kSplitCost - 1) / kSplitCost);
+    return cut == tiles ? tiles : cut < kSnap ? 0 : cut > tiles - kSnap ? tiles : cut;
 }
 
 // x / y; of what fits 32 bits, which is nearly all, in a fifth of the time.
@@ -241,6 +244,14 @@ __device__ __forceinline__ bool read_job(Smem<D>& sm, unsigned i, Job* job, unsi
     return true;
 }
 
+// The boundary at a share's start, if it is the first inside its unit: the share before begins at the unit, or before it.
+__device__ __forceinline__ Seam seam_of(const Start& s) {
+    if (s.seq < 0 || s.pos <= s.unit || s.pos - s.share > s.unit) return Seam{};
+    const bool pair = s.r.paired(s.entry);
+    return Seam{s.unit, s.share, s.seq, s.kvh, s.entry * 2 * kTile, min(2 * kTile, s.r.rows - s.entry * 2 * kTile), s.r.tiles, pair,
+                (int)blockIdx.x - 1, (int)quotient(s.unit + s.r.cost(pair) - 1, s.share)};
+}
+
 // The look-ahead warp: the places of block after block into the side ring, up to kAhead tiles before they are copied and across the ends
 // of pieces, so that the tables' latency is not waited for.
 // Side data of tile i sits in slot i % kRing, which was tile i - kRing's, last looked at by the softmax before P of that tile is there, so before
@@ -257,14 +268,6 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, Seam* seams,
     long long unit = start.unit;  // where the unit begins
     bool more = seq >= 0;
     Request r = start.r;
-    // the boundary at this share's start is the first inside the unit if the share before begins at the unit, or before it
-    if (lane == 0) {
-        Seam seam{};
-        if (more && start.pos > unit && start.pos - start.share <= unit)
-            seam = Seam{unit, start.share, seq, kvh, e * 2 * kTile, min(2 * kTile, r.rows - e * 2 * kTile), r.tiles, r.paired(e), (int)blockIdx.x - 1,
-                        (int)quotient(unit + r.cost(r.paired(e)) - 1, start.share)};
-        seams[blockIdx.x] = seam;
-    }
     unsigned tiles = 0;
 #pragma unroll 1
     for (unsigned i = 0;; ++i) {
@@ -293,6 +296,7 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, Seam* seams,
             sm.jobs[i % kPieces] = j;
             mbar_arrive(&sm.job_full[i % kPieces]);
         }
+        if (i == 0 && lane == 0) seams[blockIdx.x] = seam_of(start);
         if (!have) return;
         const int used = (j.L + BS - 1) / BS, cleaned = first_cleaned(j);
         const int32_t* table = a.block_tables + (size_t)j.seq * a.max_blocks;
@@ -813,7 +817,8 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
         if (join) {  // both streams have a part of the same rows, in the same lanes of tensor memory
             sm.state[t][r] = make_float2(m, __uint_as_float((__float_as_uint(l) & 0x7fffffffu) | (noted ? 0x80000000u : 0u)));
             tc_fence_before();
-            mbar_arrive(&sm.join_full);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.join_full);
             if (!warp_wait(&sm.join_full, joins & 1, a.err, abort)) return;
             tc_fence_after();
             const float2 o = sm.state[t ^ 1][r];
@@ -836,15 +841,17 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
             // 32 columns from c on, in float32
             auto columns = [&](int c, uint32_t (&s)[32]) {
                 tmem_ld32(o_at + c, s);
-                tc_wait_ld(s);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
                 if (join) {
                     uint32_t o[32];
                     tmem_ld32(other_o_at + c, o);
+                    tc_wait_ld(s);
                     tc_wait_ld(o);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k])));
+                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f1, __uint_as_float(s[k]) * f0));
+                } else {
+                    tc_wait_ld(s);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f0);
                 }
                 if (notes_from) {
                     uint32_t plus = 0, minus = 0;
@@ -911,7 +918,8 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
         }
         tc_fence_before();
         if (join) {  // neither stream's output is written again before both have read it
-            mbar_arrive(&sm.join_done);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.join_done);
             if (!warp_wait(&sm.join_done, joins & 1, a.err, abort)) return;
             ++joins;
         }
@@ -957,8 +965,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
             mbar_init(&sm.dirty_full[i], 1);
             mbar_init(&sm.clean_full[i], 1);
         }
-        mbar_init(&sm.join_full, kSoftmaxWarps * 32);
-        mbar_init(&sm.join_done, kSoftmaxWarps * 32);
+        mbar_init(&sm.join_full, kSoftmaxWarps);
+        mbar_init(&sm.join_done, kSoftmaxWarps);
         mbar_init(&sm.drain[0], 1);
         mbar_init(&sm.drain[1], 1);
         sm.abort = 0;
