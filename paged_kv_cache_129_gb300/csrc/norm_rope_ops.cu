@@ -15,7 +15,9 @@ namespace pa {
 namespace {
 
 constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
-constexpr int kNormTokens = 4;  // tokens of a CTA, at most
+constexpr int kNormTokens = 4;  // tokens whose turns are in shared memory at a time
+constexpr int kNormCtasPerSm = 4;
+constexpr int kNormBatch = 2;   // rows that a group of lanes has in flight
 
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int i) {
     return dtype == 0   ? static_cast<const float*>(w)[i]
@@ -23,96 +25,216 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int i) {
                         : to_float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 
-// A row is ns = d / 2V slots of two chunks of V elements (as in rope_ops.cu); LPR lanes, a power of two, share it, S slots each.
-template <typename T, int VB, int S>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const NormRopeArgs a, int tokens_per_cta, int LPR) {
+// Turns of a pair with its weights: (x, y) -> (x a + y b, x c + y d), a = cos w_x, b = -sin w_y, c = sin w_x, d = cos w_y.  Of a slot of V pairs
+// two go together, as four packed operands (two 16-byte units); those of neighbouring slots lie next to each other, so that the lanes
+// of a row read without bank conflicts.
+template <int V>
+__device__ __forceinline__ void put_turn(float* table, int pair, int slots, float4 t) {
+    if constexpr (V == 1) {
+        reinterpret_cast<float4*>(table)[pair] = t;
+    } else {
+        const int slot = pair / V, i = pair % V;
+        float* at = table + (((i / 2) * 2) * slots + slot) * 4 + i % 2;
+        at[0] = t.x;
+        at[2] = t.y;
+        at += slots * 4;
+        at[0] = t.z;
+        at[2] = t.w;
+    }
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return d;
+}
+
+// The pairs of one slot, normed, weighted and turned.
+template <typename T, int VB, bool INTERLEAVED>
+__device__ __forceinline__ void turn_pairs(Chunk<T, VB>& x0, Chunk<T, VB>& x1, const float* table, int slot, int slots, float norm) {
     constexpr int V = Chunk<T, VB>::V;
-    extern __shared__ float2 cs[];  // [tokens][rotary_dim / 2]; then the pairs' steps; then query and key weights, [d] each
+    const float4* t = reinterpret_cast<const float4*>(table);
+    if constexpr (V == 1) {
+        const float4 w = t[slot];
+        const float x = x0.one() * norm, y = x1.one() * norm;
+        x0.put_one(fmaf(x, w.x, y * w.y));
+        x1.put_one(fmaf(x, w.z, y * w.w));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {  // pairs 2i and 2i + 1
+            const float4 p = t[2 * i * slots + slot], q = t[(2 * i + 1) * slots + slot];
+            const float2 n = make_float2(norm, norm);
+            if (INTERLEAVED) {  // a pair is neighbours: four elements of one chunk
+                Chunk<T, VB>& c = 2 * i < V / 2 ? x0 : x1;
+                const int at = 2 * i % (V / 2);
+                const float2 u = mul2(c.pair(at), n), v = mul2(c.pair(at + 1), n);
+                c.put(at, make_float2(fmaf(u.x, p.x, u.y * p.z), fmaf(u.x, q.x, u.y * q.z)));
+                c.put(at + 1, make_float2(fmaf(v.x, p.y, v.y * p.w), fmaf(v.x, q.y, v.y * q.w)));
+            } else {
+                const float2 x = mul2(x0.pair(i), n), y = mul2(x1.pair(i), n);
+                x0.put(i, fma2(x, make_float2(p.x, p.y), mul2(y, make_float2(p.z, p.w))));
+                x1.put(i, fma2(x, make_float2(q.x, q.y), mul2(y, make_float2(q.z, q.w))));
+            }
+        }
+    }
+}
+
+// Elements that do not turn: the pairs' own weights are the table's a and d.
+template <typename T, int VB>
+__device__ __forceinline__ void scale_pairs(Chunk<T, VB>& x0, Chunk<T, VB>& x1, const float* table, int slot, int slots, float norm) {
+    constexpr int V = Chunk<T, VB>::V;
+    const float4* t = reinterpret_cast<const float4*>(table);
+    if constexpr (V == 1) {
+        const float4 w = t[slot];
+        x0.put_one(x0.one() * norm * w.x);
+        x1.put_one(x1.one() * norm * w.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float4 p = t[2 * i * slots + slot], q = t[(2 * i + 1) * slots + slot];
+            const float2 n = make_float2(norm, norm);
+            x0.put(i, mul2(mul2(x0.pair(i), n), make_float2(p.x, p.y)));
+            x1.put(i, mul2(mul2(x1.pair(i), n), make_float2(q.z, q.w)));
+        }
+    }
+}
+
+// A row (a query, key or value head of a token) is slots = d / 2V slots of two chunks of V elements, as in rope_ops.cu; LPR lanes, a power
+// of two, share it, S slots each.  A CTA takes runs of kNormTokens tokens: their turns, with the weights, are made once and not once per head,
+// and the steps of the pairs, in float64, once per CTA.  Rows are moved once: HBM bounds it for prompts, latency for steps.
+template <typename T, int VB, int S, bool INTERLEAVED>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const NormRopeArgs a, int LPR) {
+    constexpr int V = Chunk<T, VB>::V;
+    extern __shared__ float4 tables[];  // [tokens][queries, keys][d / 2], see put_turn; then the pairs' steps
     __shared__ long long dest[kNormTokens];
     griddep_wait();
     griddep_launch_dependents();
     const RopeArgs& r = a.r;
-    const int half = r.rotary_dim / 2, d = r.head_dim, tid = threadIdx.x, lane = tid & 31;
-    uint64_t* steps = reinterpret_cast<uint64_t*>(cs + tokens_per_cta * half);
-    float* weights = reinterpret_cast<float*>(steps + half);
-    const int tok0 = blockIdx.x * tokens_per_cta, ntok = min(tokens_per_cta, r.num_tokens - tok0);
+    const int half = r.rotary_dim / 2, d = r.head_dim, pairs = d / 2, tid = threadIdx.x, lane = tid & 31;
+    uint64_t* steps = reinterpret_cast<uint64_t*>(tables + kNormTokens * 2 * pairs);
+    const int slots = d / (2 * V), RPW = 32 / LPR, sub = lane / LPR, in_row = lane % LPR;
+    const int per_token = r.num_heads + 2 * r.num_kv_heads, step = kNormWarps * RPW;
+    // where the lane's chunks are in a row
+    int e0[S], e1[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int sl = in_row + s * LPR;
+        const bool split = sl < half / V && !INTERLEAVED;
+        e0[s] = split ? V * sl : 2 * V * sl;
+        e1[s] = split ? V * sl + half : 2 * V * sl + V;
+    }
     for (int i = tid; i < half; i += kNormThreads) steps[i] = turn_step(r.inv_freq[i]);
-    for (int i = tid; i < d; i += kNormThreads) {
-        weights[i] = (a.q_weight ? weight_at(a.q_weight, a.weight_dtype, i) : 1.f) + (a.q_weight ? a.weight_offset : 0.f);
-        weights[d + i] = (a.k_weight ? weight_at(a.k_weight, a.weight_dtype, i) : 1.f) + (a.k_weight ? a.weight_offset : 0.f);
-    }
-    if (tid < ntok) {
-        const long long slot = a.slot_mapping[tok0 + tid];
-        long long to = -1;  // in rows of the cache, without the head
-        if (slot >= (long long)r.num_blocks * r.block_size) {
-            atomicOr(r.err, kErrBadSlot);
-        } else if (slot >= 0) {
-            const long long blk = slot / r.block_size;
-            to = blk * r.num_kv_heads * r.block_size + (slot - blk * r.block_size);
-        }
-        dest[tid] = to;
-    }
-    __syncthreads();
-    for (int i = tid; i < ntok * half; i += kNormThreads) {
-        const int t = i / half;
-        cs[i] = turn(steps[i - t * half], a.positions[tok0 + t], r.factor);
-    }
-    __syncthreads();
-    const int ns = d / (2 * V), RPW = 32 / LPR, sub = lane / LPR, in_row = lane % LPR;
-    const int per_token = r.num_heads + 2 * r.num_kv_heads, rows = ntok * per_token;
-    for (int base = (tid >> 5) * RPW; base < rows; base += kNormWarps * RPW) {
-        const int row = base + sub;
-        const bool live = row < rows;
-        const int t = live ? row / per_token : 0;
-        int h = live ? row - t * per_token : 0;
-        const bool is_query = h < r.num_heads;
-        if (!is_query) h -= r.num_heads;
-        const bool is_value = !is_query && h >= r.num_kv_heads;
-        if (is_value) h -= r.num_kv_heads;
-        const T* src = is_query   ? static_cast<const T*>(r.query) + (tok0 + t) * r.q_stride
-                       : is_value ? static_cast<const T*>(r.value) + (tok0 + t) * r.v_stride
-                                  : static_cast<const T*>(r.key) + (tok0 + t) * r.k_stride;
-        src += (long long)h * d;
-        Chunk<T, VB> x0[S], x1[S];
-        int e0[S], e1[S];
-        float sum = 0.f;
+    for (long long tok = (long long)blockIdx.x * kNormTokens; tok < r.num_tokens; tok += (long long)gridDim.x * kNormTokens) {
+        const int tok0 = (int)tok, ntok = min(kNormTokens, r.num_tokens - tok0), rows = ntok * per_token;
+        Chunk<T, VB> x0[kNormBatch][S], x1[kNormBatch][S];
+        auto load = [&](int base) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int sl = in_row + s * LPR;
-            const bool turns = sl < half / V, split = turns && !r.interleaved;
-            e0[s] = split ? V * sl : 2 * V * sl;
-            e1[s] = split ? V * sl + half : 2 * V * sl + V;
-            if (!live || sl >= ns) continue;
-            x0[s].load(src + e0[s]);
-            x1[s].load(src + e1[s]);
-            float y0[V], y1[V];
-            widen_slot<T, VB>(x0[s], x1[s], y0, y1);
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum = fmaf(y0[i], y0[i], fmaf(y1[i], y1[i], sum));
-        }
-        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float norm = 1.f / sqrtf(sum / (float)d + a.eps);
-        if (!live || (!is_query && dest[t] < 0)) continue;
-        T* dst = is_query ? static_cast<T*>(r.query_out) + ((long long)(tok0 + t) * r.num_heads + h) * d
-                          : static_cast<T*>(is_value ? a.value_cache : a.key_cache) + (dest[t] + (long long)h * r.block_size) * d;
-        const float* w = weights + (is_query ? 0 : d);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int sl = in_row + s * LPR;
-            if (sl >= ns) continue;
-            if (!is_value) {
-                float y0[V], y1[V];
-                widen_slot<T, VB>(x0[s], x1[s], y0, y1);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    y0[i] *= norm * w[e0[s] + i];
-                    y1[i] *= norm * w[e1[s] + i];
+            for (int u = 0; u < kNormBatch; ++u) {
+                const int row = base + u * step + sub;
+                if (row >= rows) break;
+                const int t = row / per_token;
+                int h = row - t * per_token;
+                const T* src;
+                if (h < r.num_heads) {
+                    src = static_cast<const T*>(r.query) + (tok0 + t) * r.q_stride;
+                } else if ((h -= r.num_heads) < r.num_kv_heads) {
+                    src = static_cast<const T*>(r.key) + (tok0 + t) * r.k_stride;
+                } else {
+                    h -= r.num_kv_heads;
+                    src = static_cast<const T*>(r.value) + (tok0 + t) * r.v_stride;
                 }
-                if (sl < half / V) turn_slot<V>(y0, y1, cs + t * half + sl * V, r.interleaved != 0);
-                pack_slot<T, VB>(y0, y1, x0[s], x1[s]);
+                src += (long long)h * d;
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (in_row + s * LPR < slots) {
+                        x0[u][s].load(src + e0[s]);
+                        x1[u][s].load(src + e1[s]);
+                    }
             }
-            x0[s].store(dst + e0[s]);
-            x1[s].store(dst + e1[s]);
+        };
+        const int base0 = (tid >> 5) * RPW;
+        load(base0);  // (the first rows are on their way while the turns are made)
+        __syncthreads();
+        if (tid < ntok) {
+            const long long slot = a.slot_mapping[tok0 + tid];
+            long long to = -1;  // in rows of the cache, without the head
+            if (slot >= (long long)r.num_blocks * r.block_size) {
+                atomicOr(r.err, kErrBadSlot);
+            } else if (slot >= 0) {
+                const long long blk = slot / r.block_size;
+                to = blk * r.num_kv_heads * r.block_size + (slot - blk * r.block_size);
+            }
+            dest[tid] = to;
+        }
+        for (int i = tid; i < ntok * pairs; i += kNormThreads) {
+            const int t = i / pairs, p = i - t * pairs, sl = p / V, k = p - sl * V;
+            const float2 cs = p < half ? turn(steps[p], a.positions[tok0 + t], r.factor) : make_float2(1.f, 0.f);
+            // the pair's elements
+            const bool turns = p < half;
+            const int ex = turns ? (INTERLEAVED ? 2 * p : p) : 2 * V * sl + k, ey = turns ? (INTERLEAVED ? 2 * p + 1 : p + half) : ex + V;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const void* w = q ? a.k_weight : a.q_weight;
+                const float wx = w ? weight_at(w, a.weight_dtype, ex) + a.weight_offset : 1.f;
+                const float wy = w ? weight_at(w, a.weight_dtype, ey) + a.weight_offset : 1.f;
+                put_turn<V>(reinterpret_cast<float*>(tables + (t * 2 + q) * pairs), p, slots, make_float4(cs.x * wx, -cs.y * wy, cs.y * wx, cs.x * wy));
+            }
+        }
+        __syncthreads();
+        for (int base = base0; base < rows; base += step * kNormBatch) {
+            if (base != base0) load(base);
+#pragma unroll
+            for (int u = 0; u < kNormBatch; ++u) {
+                const int row = base + u * step + sub;
+                const bool live = row < rows;
+                float2 sums = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    if (!live || in_row + s * LPR >= slots) continue;
+                    if constexpr (V == 1) {
+                        sums.x = fmaf(x0[u][s].one(), x0[u][s].one(), sums.x);
+                        sums.y = fmaf(x1[u][s].one(), x1[u][s].one(), sums.y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const float2 x = x0[u][s].pair(i), y = x1[u][s].pair(i);
+                            sums = fma2(x, x, fma2(y, y, sums));
+                        }
+                    }
+                }
+                float sum = sums.x + sums.y;
+                for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (!live) continue;
+                const float norm = 1.f / sqrtf(sum / (float)d + a.eps);
+                const int t = row / per_token;
+                int h = row - t * per_token;
+                const bool is_query = h < r.num_heads;
+                if (!is_query) h -= r.num_heads;
+                const bool is_value = !is_query && h >= r.num_kv_heads;
+                if (is_value) h -= r.num_kv_heads;
+                if (!is_query && dest[t] < 0) continue;
+                T* dst = is_query ? static_cast<T*>(r.query_out) + ((long long)(tok0 + t) * r.num_heads + h) * d
+                                  : static_cast<T*>(is_value ? a.value_cache : a.key_cache) + (dest[t] + (long long)h * r.block_size) * d;
+                const float* table = reinterpret_cast<const float*>(tables + (t * 2 + (is_query ? 0 : 1)) * pairs);
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int sl = in_row + s * LPR;
+                    if (sl >= slots) continue;
+                    if (!is_value) {
+                        if (sl < half / V)
+                            turn_pairs<T, VB, INTERLEAVED>(x0[u][s], x1[u][s], table, sl, slots, norm);
+                        else
+                            scale_pairs<T, VB>(x0[u][s], x1[u][s], table, sl, slots, norm);
+                    }
+                    x0[u][s].store(dst + e0[s]);
+                    x1[u][s].store(dst + e1[s]);
+                }
+            }
         }
     }
 }
@@ -121,14 +243,15 @@ bool multiple(const void* p, long long bytes) { return reinterpret_cast<uintptr_
 
 template <typename T, int VB, int S>
 cudaError_t norm_typed(const NormRopeArgs& a, cudaStream_t stream) {
-    const int ns = a.r.head_dim / (2 * (VB / (int)sizeof(T)));
+    const int slots = a.r.head_dim / (2 * (VB / (int)sizeof(T)));
     int lpr = 1;
-    while (lpr < ns && lpr < 32) lpr *= 2;
-    if ((ns + lpr - 1) / lpr > S) return cudaErrorInvalidValue;
-    const int per = a.r.num_tokens >= kNormTokens * a.num_sms ? kNormTokens : 1;
-    const unsigned grid = (unsigned)((a.r.num_tokens + per - 1) / per);
-    const size_t smem = (size_t)(per + 1) * (a.r.rotary_dim / 2) * sizeof(float2) + (size_t)2 * a.r.head_dim * sizeof(float);
-    return launch_pdl(norm_rope_write_kv_kernel<T, VB, S>, dim3(grid), dim3(kNormThreads), smem, stream, a, per, lpr);
+    while (lpr < slots && lpr < 32) lpr *= 2;
+    if ((slots + lpr - 1) / lpr > S) return cudaErrorInvalidValue;
+    const long long runs = (a.r.num_tokens + kNormTokens - 1) / kNormTokens;
+    const unsigned grid = (unsigned)std::min(runs, (long long)kNormCtasPerSm * a.num_sms);
+    const size_t smem = (size_t)kNormTokens * a.r.head_dim * sizeof(float4) + (size_t)(a.r.rotary_dim / 2) * sizeof(uint64_t);
+    auto* kernel = a.r.interleaved ? norm_rope_write_kv_kernel<T, VB, S, true> : norm_rope_write_kv_kernel<T, VB, S, false>;
+    return launch_pdl(kernel, dim3(grid), dim3(kNormThreads), smem, stream, a, lpr);
 }
 
 // Whether a row splits into chunks of 16 bytes: aligned bases and strides, slots of two chunks that do not straddle the end of the pairs.

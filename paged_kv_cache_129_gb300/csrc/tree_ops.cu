@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_tree_kernel(const Accep
 
 // ---- compaction ----------------------------------------------------------------------------------------
 
-constexpr int kCompactThreads = 256;
+constexpr int kCompactThreads = 256, kCompactCtasPerSm = 16;
 
 // Whether request b's accepted nodes are some of its n nodes in ascending order.  Any number of threads, each for itself.
 __device__ __forceinline__ bool is_path(const CompactArgs& a, int b, int n, int count) {
@@ -171,40 +171,69 @@ __device__ __forceinline__ void trim(const CompactArgs& a) {
     if (bits) atomicOr(a.err, bits);
 }
 
-// Row (node a_j, layer, K or V, kv head) goes to the place of node j.  A thread has a column of VB bytes and takes the nodes in order: a
-// node's place is written behind every read of it, since a_j >= j.
+// Row (node a_j, layer, K or V, kv head) goes to the place of node j, for the nodes that are not there already: those behind the first that is
+// not.  CTA (request, part of its rows); a thread has columns of sizeof(Vec) bytes and takes the nodes in order, kCompactBatch at a time:
+// a node's place is written behind every read of it, since a_j >= j.  CTA 0 has the lengths and the blocks.
+// The rows are 64 - 512 bytes here and there, each read and written once: HBM bounds many requests, latency few.
+constexpr int kCompactBatch = 8;
 template <typename Vec>
-__global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const CompactArgs a, const __grid_constant__ CachePtrs caches) {
+__global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const CompactArgs a, const __grid_constant__ CachePtrs caches, int parts) {
+    __shared__ long long from[kMaxTreeNodes], to[kMaxTreeNodes];  // bytes, of kv head 0
+    __shared__ int moving[kCompactThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
-    if (blockIdx.x == (unsigned)a.num_seqs) {
+    if (blockIdx.x == 0) {
         trim(a);
         return;
     }
-    const int b = blockIdx.x, H = a.num_kv_heads, bs = a.block_size;
+    const int b = (blockIdx.x - 1) / parts, part = (blockIdx.x - 1) - b * parts, H = a.num_kv_heads, bs = a.block_size, tid = threadIdx.x;
     int first;
     bool bad;
     const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), count = a.num_accepted[b];
-    if (bad || !is_path(a, b, n, count)) return;
-    const int columns = a.row_bytes / (int)sizeof(Vec);
-    const long long slots = (long long)a.num_blocks * bs, items = 2ll * a.num_layers * H * columns;
-    for (long long x = threadIdx.x; x < items; x += kCompactThreads) {
-        const int unit = (int)(x / columns), column = (int)(x - (long long)unit * columns);
-        const int layer = unit / (2 * H), h = unit % H;
-        char* cache = (unit / H & 1 ? caches.value[layer] : caches.key[layer]);
-        for (int j = 0; j < count; ++j) {
-            const int node = a.accepted[(long long)b * a.max_accepted + j];
-            if (node == j) continue;
-            const long long from = a.slot_mapping[first + node], to = a.slot_mapping[first + j];
-            if (from < 0 || from >= slots || to < 0 || to >= slots) {
-                atomicOr(a.err, kErrBadSlot);
-                continue;
-            }
-            auto place = [&](long long slot) {
-                const long long row = (slot / bs * H + h) * bs + slot % bs;
-                return reinterpret_cast<Vec*>(cache + row * a.row_bytes) + column;
-            };
-            *place(to) = *place(from);
+    if (bad || count <= 0 || count > n || count > a.max_accepted) return;
+    const long long slots = (long long)a.num_blocks * bs;
+    const int32_t* path = a.accepted + (long long)b * a.max_accepted;
+    bool wrong = false;
+    int still = 0;  // nodes that are in their place
+    for (int j = tid; j < count; j += kCompactThreads) {
+        const int node = path[j], before = j > 0 ? path[j - 1] : -1;
+        wrong |= node <= before || node >= n;
+        if (wrong) break;
+        still += node == j;
+        long long at[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const long long slot = a.slot_mapping[first + (k ? j : node)];
+            const long long blk = slot >= 0 ? slot / bs : 0;
+            at[k] = slot < 0 || slot >= slots ? -1 : (blk * H * bs + (slot - blk * bs)) * a.row_bytes;
+        }
+        if (at[0] < 0 || at[1] < 0) {
+            if (node != j) atomicOr(a.err, kErrBadSlot);
+            at[0] = -1;
+        }
+        from[j] = at[0];
+        to[j] = at[1];
+    }
+    if (__syncthreads_or(wrong)) return;
+    still = __reduce_add_sync(0xffffffffu, still);
+    if ((tid & 31) == 0) moving[tid >> 5] = still;
+    __syncthreads();
+    still = 0;
+#pragma unroll
+    for (int w = 0; w < kCompactThreads / 32; ++w) still += moving[w];
+    if (still == count) return;
+    const int columns = a.row_bytes / (int)sizeof(Vec), items = 2 * a.num_layers * H * columns;
+    for (int x = part * kCompactThreads + tid; x < items; x += parts * kCompactThreads) {
+        const int unit = x / columns, column = x - unit * columns, cache = unit / H, h = unit - cache * H;
+        char* base = (cache & 1 ? caches.value[cache >> 1] : caches.key[cache >> 1]) + (long long)h * bs * a.row_bytes + column * (int)sizeof(Vec);
+        for (int j0 = still; j0 < count; j0 += kCompactBatch) {
+            Vec v[kCompactBatch];
+#pragma unroll
+            for (int k = 0; k < kCompactBatch; ++k)
+                if (j0 + k < count && from[j0 + k] >= 0) v[k] = *reinterpret_cast<const Vec*>(base + from[j0 + k]);
+#pragma unroll
+            for (int k = 0; k < kCompactBatch; ++k)
+                if (j0 + k < count && from[j0 + k] >= 0) *reinterpret_cast<Vec*>(base + to[j0 + k]) = v[k];
         }
     }
 }
@@ -222,10 +251,15 @@ cudaError_t accept_tree_launch(const AcceptArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, cudaStream_t stream) {
-    const dim3 grid((unsigned)a.num_seqs + 1), block(kCompactThreads);
-    if (a.vector) return launch_pdl(compact_tree_kernel<uint4>, grid, block, 0, stream, a, caches);
-    if (a.elem_bytes == 4) return launch_pdl(compact_tree_kernel<uint32_t>, grid, block, 0, stream, a, caches);
-    return launch_pdl(compact_tree_kernel<uint16_t>, grid, block, 0, stream, a, caches);
+    const int vec = a.vector ? 16 : a.elem_bytes;
+    // Parts of a request's rows: as many CTAs as kCompactCtasPerSm to an SM, but a column of every thread at least.
+    const long long items = 2ll * a.num_layers * a.num_kv_heads * (a.row_bytes / vec), most = (items + kCompactThreads - 1) / kCompactThreads;
+    const long long wanted = a.num_seqs ? ((long long)kCompactCtasPerSm * a.num_sms + a.num_seqs - 1) / a.num_seqs : 1;
+    const int parts = (int)std::max(1ll, std::min(most, wanted));
+    const dim3 grid((unsigned)(1 + (long long)a.num_seqs * parts)), block(kCompactThreads);
+    if (a.vector) return launch_pdl(compact_tree_kernel<uint4>, grid, block, 0, stream, a, caches, parts);
+    if (a.elem_bytes == 4) return launch_pdl(compact_tree_kernel<uint32_t>, grid, block, 0, stream, a, caches, parts);
+    return launch_pdl(compact_tree_kernel<uint16_t>, grid, block, 0, stream, a, caches, parts);
 }
 
 }  // namespace pa
