@@ -15,9 +15,8 @@ namespace pa {
 namespace {
 
 constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
-constexpr int kNormTokens = 4;  // tokens whose turns are in shared memory at a time
+constexpr int kNormTokens = 8;  // tokens whose turns are in shared memory at a time
 constexpr int kNormCtasPerSm = 4;
-constexpr int kNormBatch = 2;   // rows that a group of lanes has in flight
 
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int i) {
     return dtype == 0   ? static_cast<const float*>(w)[i]
@@ -105,20 +104,23 @@ __device__ __forceinline__ void scale_pairs(Chunk<T, VB>& x0, Chunk<T, VB>& x1, 
 }
 
 // A row (a query, key or value head of a token) is slots = d / 2V slots of two chunks of V elements, as in rope_ops.cu; LPR lanes, a power
-// of two, share it, S slots each.  A CTA takes runs of kNormTokens tokens: their turns, with the weights, are made once and not once per head,
-// and the steps of the pairs, in float64, once per CTA.  Rows are moved once: HBM bounds it for prompts, latency for steps.
+// of two, share it, S slots each.  A CTA takes consecutive tokens, kNormTokens at a time: their turns, with the weights, are made once and not
+// once per head, and the steps of the pairs, in float64, once per CTA.  A group of lanes has two rows in flight, the next ones while it works on
+// these.  Rows are moved once: HBM bounds it for prompts, latency for steps.
 template <typename T, int VB, int S, bool INTERLEAVED>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const NormRopeArgs a, int LPR) {
+__global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const NormRopeArgs a, int LPR, int tokens_per_cta) {
     constexpr int V = Chunk<T, VB>::V;
-    extern __shared__ float4 tables[];  // [tokens][queries, keys][d / 2], see put_turn; then the pairs' steps
+    extern __shared__ float4 tables[];  // [tokens][queries, keys][d / 2], see put_turn; then the pairs' steps; then weights [2][d]
     __shared__ long long dest[kNormTokens];
     griddep_wait();
     griddep_launch_dependents();
     const RopeArgs& r = a.r;
     const int half = r.rotary_dim / 2, d = r.head_dim, pairs = d / 2, tid = threadIdx.x, lane = tid & 31;
+    const int Hq = r.num_heads, Hk = r.num_kv_heads, per_token = Hq + 2 * Hk;
     uint64_t* steps = reinterpret_cast<uint64_t*>(tables + kNormTokens * 2 * pairs);
-    const int slots = d / (2 * V), RPW = 32 / LPR, sub = lane / LPR, in_row = lane % LPR;
-    const int per_token = r.num_heads + 2 * r.num_kv_heads, step = kNormWarps * RPW;
+    float* weights = reinterpret_cast<float*>(steps + half);
+    const int slots = d / (2 * V), RPW = 32 / LPR, sub = lane / LPR, in_row = lane % LPR, step = kNormWarps * RPW;
+    const float per_element = 1.f / (float)d;
     // where the lane's chunks are in a row
     int e0[S], e1[S];
 #pragma unroll
@@ -128,37 +130,93 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const 
         e0[s] = split ? V * sl : 2 * V * sl;
         e1[s] = split ? V * sl + half : 2 * V * sl + V;
     }
-    for (int i = tid; i < half; i += kNormThreads) steps[i] = turn_step(r.inv_freq[i]);
-    for (long long tok = (long long)blockIdx.x * kNormTokens; tok < r.num_tokens; tok += (long long)gridDim.x * kNormTokens) {
-        const int tok0 = (int)tok, ntok = min(kNormTokens, r.num_tokens - tok0), rows = ntok * per_token;
-        Chunk<T, VB> x0[kNormBatch][S], x1[kNormBatch][S];
-        auto load = [&](int base) {
-#pragma unroll
-            for (int u = 0; u < kNormBatch; ++u) {
-                const int row = base + u * step + sub;
-                if (row >= rows) break;
-                const int t = row / per_token;
-                int h = row - t * per_token;
-                const T* src;
-                if (h < r.num_heads) {
-                    src = static_cast<const T*>(r.query) + (tok0 + t) * r.q_stride;
-                } else if ((h -= r.num_heads) < r.num_kv_heads) {
-                    src = static_cast<const T*>(r.key) + (tok0 + t) * r.k_stride;
-                } else {
-                    h -= r.num_kv_heads;
-                    src = static_cast<const T*>(r.value) + (tok0 + t) * r.v_stride;
-                }
-                src += (long long)h * d;
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (in_row + s * LPR < slots) {
-                        x0[u][s].load(src + e0[s]);
-                        x1[u][s].load(src + e1[s]);
-                    }
-            }
+    const long long tok_begin = (long long)blockIdx.x * tokens_per_cta, tok_end = min(tok_begin + tokens_per_cta, (long long)r.num_tokens);
+    for (long long tok0 = tok_begin; tok0 < tok_end; tok0 += kNormTokens) {
+        const int ntok = (int)min((long long)kNormTokens, tok_end - tok0);
+        // a lane's row: head h (queries, keys, values) of token t; t >= ntok: none
+        struct Row {
+            int t, h;
         };
-        const int base0 = (tid >> 5) * RPW;
-        load(base0);  // (the first rows are on their way while the turns are made)
+        auto next = [&](Row x) {
+            x.h += step;
+            while (x.h >= per_token) x.h -= per_token, ++x.t;
+            return x;
+        };
+        Chunk<T, VB> x0[2][S], x1[2][S];
+        auto load = [&](int u, Row x) {
+            if (x.t >= ntok) return;
+            const bool is_query = x.h < Hq, is_value = x.h >= Hq + Hk;
+            const T* src = static_cast<const T*>(is_query ? r.query : is_value ? r.value : r.key);
+            src += (tok0 + x.t) * (is_query ? r.q_stride : is_value ? r.v_stride : r.k_stride);
+            src += (x.h - (is_query ? 0 : is_value ? Hq + Hk : Hq)) * d;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (in_row + s * LPR < slots) {
+                    x0[u][s].load(src + e0[s]);
+                    x1[u][s].load(src + e1[s]);
+                }
+        };
+        auto work = [&](int u, Row x) {
+            const bool live = x.t < ntok;
+            float2 sums = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                if (!live || in_row + s * LPR >= slots) continue;
+                if constexpr (V == 1) {
+                    sums.x = fmaf(x0[u][s].one(), x0[u][s].one(), sums.x);
+                    sums.y = fmaf(x1[u][s].one(), x1[u][s].one(), sums.y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float2 y = x0[u][s].pair(i), z = x1[u][s].pair(i);
+                        sums = fma2(y, y, fma2(z, z, sums));
+                    }
+                }
+            }
+            float sum = sums.x + sums.y;
+            for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (!live) return;
+            const bool is_query = x.h < Hq, is_value = x.h >= Hq + Hk;
+            T* dst;
+            if (is_query) {
+                dst = static_cast<T*>(r.query_out) + ((tok0 + x.t) * Hq + x.h) * d;
+            } else {
+                const long long to = dest[x.t];
+                if (to < 0) return;
+                dst = static_cast<T*>(is_value ? a.value_cache : a.key_cache) + (to + (long long)(x.h - (is_value ? Hq + Hk : Hq)) * r.block_size) * d;
+            }
+            if (!is_value) {
+                const float norm = __frsqrt_rn(fmaf(sum, per_element, a.eps));
+                const float* table = reinterpret_cast<const float*>(tables + (x.t * 2 + (is_query ? 0 : 1)) * pairs);
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int sl = in_row + s * LPR;
+                    if (sl >= slots) continue;
+                    if (sl < half / V)
+                        turn_pairs<T, VB, INTERLEAVED>(x0[u][s], x1[u][s], table, sl, slots, norm);
+                    else
+                        scale_pairs<T, VB>(x0[u][s], x1[u][s], table, sl, slots, norm);
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (in_row + s * LPR < slots) {
+                    x0[u][s].store(dst + e0[s]);
+                    x1[u][s].store(dst + e1[s]);
+                }
+        };
+        Row p{0, (tid >> 5) * RPW + sub};
+        while (p.h >= per_token) p.h -= per_token, ++p.t;
+        Row q = next(p);
+        load(0, p);  // (the first rows are on their way while the turns are made)
+        load(1, q);
+        if (tok0 == tok_begin) {
+            for (int i = tid; i < half; i += kNormThreads) steps[i] = turn_step(r.inv_freq[i]);
+            for (int i = tid; i < 2 * d; i += kNormThreads) {
+                const void* w = i < d ? a.q_weight : a.k_weight;
+                weights[i] = w ? weight_at(w, a.weight_dtype, i < d ? i : i - d) + a.weight_offset : 1.f;
+            }
+        }
         __syncthreads();
         if (tid < ntok) {
             const long long slot = a.slot_mapping[tok0 + tid];
@@ -167,74 +225,32 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const 
                 atomicOr(r.err, kErrBadSlot);
             } else if (slot >= 0) {
                 const long long blk = slot / r.block_size;
-                to = blk * r.num_kv_heads * r.block_size + (slot - blk * r.block_size);
+                to = blk * Hk * r.block_size + (slot - blk * r.block_size);
             }
             dest[tid] = to;
         }
         for (int i = tid; i < ntok * pairs; i += kNormThreads) {
-            const int t = i / pairs, p = i - t * pairs, sl = p / V, k = p - sl * V;
-            const float2 cs = p < half ? turn(steps[p], a.positions[tok0 + t], r.factor) : make_float2(1.f, 0.f);
+            const int t = i / pairs, pair = i - t * pairs;
+            const bool turns = pair < half;
+            const float2 cs = turns ? turn(steps[pair], a.positions[tok0 + t], r.factor) : make_float2(1.f, 0.f);
             // the pair's elements
-            const bool turns = p < half;
-            const int ex = turns ? (INTERLEAVED ? 2 * p : p) : 2 * V * sl + k, ey = turns ? (INTERLEAVED ? 2 * p + 1 : p + half) : ex + V;
+            const int still = 2 * V * (pair / V) + pair % V;
+            const int ex = !turns ? still : INTERLEAVED ? 2 * pair : pair, ey = !turns ? still + V : INTERLEAVED ? 2 * pair + 1 : pair + half;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const void* w = q ? a.k_weight : a.q_weight;
-                const float wx = w ? weight_at(w, a.weight_dtype, ex) + a.weight_offset : 1.f;
-                const float wy = w ? weight_at(w, a.weight_dtype, ey) + a.weight_offset : 1.f;
-                put_turn<V>(reinterpret_cast<float*>(tables + (t * 2 + q) * pairs), p, slots, make_float4(cs.x * wx, -cs.y * wy, cs.y * wx, cs.x * wy));
+            for (int k = 0; k < 2; ++k) {
+                const float wx = weights[k * d + ex], wy = weights[k * d + ey];
+                put_turn<V>(reinterpret_cast<float*>(tables + (t * 2 + k) * pairs), pair, slots, make_float4(cs.x * wx, -cs.y * wy, cs.y * wx, cs.x * wy));
             }
         }
         __syncthreads();
-        for (int base = base0; base < rows; base += step * kNormBatch) {
-            if (base != base0) load(base);
-#pragma unroll
-            for (int u = 0; u < kNormBatch; ++u) {
-                const int row = base + u * step + sub;
-                const bool live = row < rows;
-                float2 sums = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    if (!live || in_row + s * LPR >= slots) continue;
-                    if constexpr (V == 1) {
-                        sums.x = fmaf(x0[u][s].one(), x0[u][s].one(), sums.x);
-                        sums.y = fmaf(x1[u][s].one(), x1[u][s].one(), sums.y);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V / 2; ++i) {
-                            const float2 x = x0[u][s].pair(i), y = x1[u][s].pair(i);
-                            sums = fma2(x, x, fma2(y, y, sums));
-                        }
-                    }
-                }
-                float sum = sums.x + sums.y;
-                for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (!live) continue;
-                const float norm = 1.f / sqrtf(sum / (float)d + a.eps);
-                const int t = row / per_token;
-                int h = row - t * per_token;
-                const bool is_query = h < r.num_heads;
-                if (!is_query) h -= r.num_heads;
-                const bool is_value = !is_query && h >= r.num_kv_heads;
-                if (is_value) h -= r.num_kv_heads;
-                if (!is_query && dest[t] < 0) continue;
-                T* dst = is_query ? static_cast<T*>(r.query_out) + ((long long)(tok0 + t) * r.num_heads + h) * d
-                                  : static_cast<T*>(is_value ? a.value_cache : a.key_cache) + (dest[t] + (long long)h * r.block_size) * d;
-                const float* table = reinterpret_cast<const float*>(tables + (t * 2 + (is_query ? 0 : 1)) * pairs);
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const int sl = in_row + s * LPR;
-                    if (sl >= slots) continue;
-                    if (!is_value) {
-                        if (sl < half / V)
-                            turn_pairs<T, VB, INTERLEAVED>(x0[u][s], x1[u][s], table, sl, slots, norm);
-                        else
-                            scale_pairs<T, VB>(x0[u][s], x1[u][s], table, sl, slots, norm);
-                    }
-                    x0[u][s].store(dst + e0[s]);
-                    x1[u][s].store(dst + e1[s]);
-                }
-            }
+        // (a warp's lanes go on together: the first one's row is the first)
+        while (__any_sync(0xffffffffu, p.t < ntok)) {
+            work(0, p);
+            p = next(q);
+            load(0, p);
+            work(1, q);
+            q = next(p);
+            load(1, q);
         }
     }
 }
@@ -247,11 +263,11 @@ cudaError_t norm_typed(const NormRopeArgs& a, cudaStream_t stream) {
     int lpr = 1;
     while (lpr < slots && lpr < 32) lpr *= 2;
     if ((slots + lpr - 1) / lpr > S) return cudaErrorInvalidValue;
-    const long long runs = (a.r.num_tokens + kNormTokens - 1) / kNormTokens;
-    const unsigned grid = (unsigned)std::min(runs, (long long)kNormCtasPerSm * a.num_sms);
-    const size_t smem = (size_t)kNormTokens * a.r.head_dim * sizeof(float4) + (size_t)(a.r.rotary_dim / 2) * sizeof(uint64_t);
+    const int ctas = kNormCtasPerSm * a.num_sms, per = (int)(((long long)a.r.num_tokens + ctas - 1) / ctas);
+    const unsigned grid = (unsigned)((a.r.num_tokens + per - 1) / per);
+    const size_t smem = (size_t)kNormTokens * a.r.head_dim * sizeof(float4) + (size_t)(a.r.rotary_dim / 2) * sizeof(uint64_t) + (size_t)2 * a.r.head_dim * sizeof(float);
     auto* kernel = a.r.interleaved ? norm_rope_write_kv_kernel<T, VB, S, true> : norm_rope_write_kv_kernel<T, VB, S, false>;
-    return launch_pdl(kernel, dim3(grid), dim3(kNormThreads), smem, stream, a, lpr);
+    return launch_pdl(kernel, dim3(grid), dim3(kNormThreads), smem, stream, a, lpr, per);
 }
 
 // Whether a row splits into chunks of 16 bytes: aligned bases and strides, slots of two chunks that do not straddle the end of the pairs.
