@@ -14,9 +14,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
-constexpr int kNormTokens = 8;  // tokens whose turns are in shared memory at a time
-constexpr int kNormCtasPerSm = 4;
+constexpr int kNormThreads = 256, kNormCtasPerSm = 3;
+constexpr int kNormSlots = 2;  // slots of a lane, where a row has as many
 
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int i) {
     return dtype == 0   ? static_cast<const float*>(w)[i]
@@ -104,22 +103,22 @@ __device__ __forceinline__ void scale_pairs(Chunk<T, VB>& x0, Chunk<T, VB>& x1, 
 }
 
 // A row (a query, key or value head of a token) is slots = d / 2V slots of two chunks of V elements, as in rope_ops.cu; LPR lanes, a power
-// of two, share it, S slots each.  A CTA takes consecutive tokens, kNormTokens at a time: their turns, with the weights, are made once and not
-// once per head, and the steps of the pairs, in float64, once per CTA.  A group of lanes has two rows in flight, the next ones while it works on
-// these.  Rows are moved once: HBM bounds it for prompts, latency for steps.
+// of two, share it, S slots each.  A warp takes a token at a time: its turns, with the weights, are made once and not once per head, in shared
+// memory of the warp's own, so that no warp waits for another; the steps of the pairs, in float64, and the weights are the CTA's.  A lane has two
+// rows in flight, the next ones while it works on these.  Rows are moved once: HBM bounds it for prompts, latency for steps.
 template <typename T, int VB, int S, bool INTERLEAVED>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const NormRopeArgs a, int LPR, int tokens_per_cta) {
+__global__ void __launch_bounds__(kNormThreads, kNormCtasPerSm) norm_rope_write_kv_kernel(const NormRopeArgs a, int LPR) {
     constexpr int V = Chunk<T, VB>::V;
-    extern __shared__ float4 tables[];  // [tokens][queries, keys][d / 2], see put_turn; then the pairs' steps; then weights [2][d]
-    __shared__ long long dest[kNormTokens];
+    extern __shared__ float4 tables[];  // [warps][queries, keys][d / 2], see put_turn; then the pairs' steps; then weights [2][d]
     griddep_wait();
     griddep_launch_dependents();
     const RopeArgs& r = a.r;
-    const int half = r.rotary_dim / 2, d = r.head_dim, pairs = d / 2, tid = threadIdx.x, lane = tid & 31;
-    const int Hq = r.num_heads, Hk = r.num_kv_heads, per_token = Hq + 2 * Hk;
-    uint64_t* steps = reinterpret_cast<uint64_t*>(tables + kNormTokens * 2 * pairs);
+    const int half = r.rotary_dim / 2, d = r.head_dim, pairs = d / 2, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int Hq = r.num_heads, Hk = r.num_kv_heads, rows = Hq + 2 * Hk;
+    float4* table = tables + warp * 2 * pairs;
+    uint64_t* steps = reinterpret_cast<uint64_t*>(tables + warps * 2 * pairs);
     float* weights = reinterpret_cast<float*>(steps + half);
-    const int slots = d / (2 * V), RPW = 32 / LPR, sub = lane / LPR, in_row = lane % LPR, step = kNormWarps * RPW;
+    const int slots = d / (2 * V), RPW = 32 / LPR, sub = lane / LPR, in_row = lane % LPR;
     const float per_element = 1.f / (float)d;
     // where the lane's chunks are in a row
     int e0[S], e1[S];
@@ -130,25 +129,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const 
         e0[s] = split ? V * sl : 2 * V * sl;
         e1[s] = split ? V * sl + half : 2 * V * sl + V;
     }
-    const long long tok_begin = (long long)blockIdx.x * tokens_per_cta, tok_end = min(tok_begin + tokens_per_cta, (long long)r.num_tokens);
-    for (long long tok0 = tok_begin; tok0 < tok_end; tok0 += kNormTokens) {
-        const int ntok = (int)min((long long)kNormTokens, tok_end - tok0);
-        // a lane's row: head h (queries, keys, values) of token t; t >= ntok: none
-        struct Row {
-            int t, h;
-        };
-        auto next = [&](Row x) {
-            x.h += step;
-            while (x.h >= per_token) x.h -= per_token, ++x.t;
-            return x;
-        };
+    bool first = true;
+    const long long stride = (long long)gridDim.x * warps;
+    for (long long tok = (long long)blockIdx.x * warps + warp; first || tok < r.num_tokens; tok += stride) {
+        const bool there = tok < r.num_tokens;
         Chunk<T, VB> x0[2][S], x1[2][S];
-        auto load = [&](int u, Row x) {
-            if (x.t >= ntok) return;
-            const bool is_query = x.h < Hq, is_value = x.h >= Hq + Hk;
+        auto load = [&](int u, int h) {  // row h: queries, keys, values
+            if (h >= rows || !there) return;
+            const bool is_query = h < Hq, is_value = h >= Hq + Hk;
             const T* src = static_cast<const T*>(is_query ? r.query : is_value ? r.value : r.key);
-            src += (tok0 + x.t) * (is_query ? r.q_stride : is_value ? r.v_stride : r.k_stride);
-            src += (x.h - (is_query ? 0 : is_value ? Hq + Hk : Hq)) * d;
+            src += tok * (is_query ? r.q_stride : is_value ? r.v_stride : r.k_stride);
+            src += (h - (is_query ? 0 : is_value ? Hq + Hk : Hq)) * d;
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (in_row + s * LPR < slots) {
@@ -156,8 +147,42 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const 
                     x1[u][s].load(src + e1[s]);
                 }
         };
-        auto work = [&](int u, Row x) {
-            const bool live = x.t < ntok;
+        load(0, sub);  // (the first rows are on their way while the turns are made)
+        load(1, sub + RPW);
+        const int pos = there ? a.positions[tok] : 0;
+        const long long slot = there ? a.slot_mapping[tok] : -1;
+        if (first) {
+            for (int i = tid; i < half; i += blockDim.x) steps[i] = turn_step(r.inv_freq[i]);
+            for (int i = tid; i < 2 * d; i += blockDim.x) {
+                const void* w = i < d ? a.q_weight : a.k_weight;
+                weights[i] = w ? weight_at(w, a.weight_dtype, i < d ? i : i - d) + a.weight_offset : 1.f;
+            }
+            __syncthreads();
+            first = false;
+            if (!there) return;
+        }
+        long long to = -1;  // in rows of the cache, without the head
+        if (slot >= (long long)r.num_blocks * r.block_size) {
+            if (lane == 0) atomicOr(r.err, kErrBadSlot);
+        } else if (slot >= 0) {
+            const long long blk = slot / r.block_size;
+            to = blk * Hk * r.block_size + (slot - blk * r.block_size);
+        }
+        for (int pair = lane; pair < pairs; pair += 32) {
+            const bool turns = pair < half;
+            const float2 cs = turns ? turn(steps[pair], pos, r.factor) : make_float2(1.f, 0.f);
+            // the pair's elements
+            const int still = 2 * V * (pair / V) + pair % V;
+            const int ex = !turns ? still : INTERLEAVED ? 2 * pair : pair, ey = !turns ? still + V : INTERLEAVED ? 2 * pair + 1 : pair + half;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float wx = weights[k * d + ex], wy = weights[k * d + ey];
+                put_turn<V>(reinterpret_cast<float*>(table + k * pairs), pair, slots, make_float4(cs.x * wx, -cs.y * wy, cs.y * wx, cs.x * wy));
+            }
+        }
+        __syncwarp();
+        auto work = [&](int u, int h) {
+            const bool live = h < rows;
             float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
             for (int s = 0; s < S; ++s) {
@@ -176,26 +201,25 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const 
             float sum = sums.x + sums.y;
             for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (!live) return;
-            const bool is_query = x.h < Hq, is_value = x.h >= Hq + Hk;
+            const bool is_query = h < Hq, is_value = h >= Hq + Hk;
             T* dst;
             if (is_query) {
-                dst = static_cast<T*>(r.query_out) + ((tok0 + x.t) * Hq + x.h) * d;
+                dst = static_cast<T*>(r.query_out) + (tok * Hq + h) * d;
             } else {
-                const long long to = dest[x.t];
                 if (to < 0) return;
-                dst = static_cast<T*>(is_value ? a.value_cache : a.key_cache) + (to + (long long)(x.h - (is_value ? Hq + Hk : Hq)) * r.block_size) * d;
+                dst = static_cast<T*>(is_value ? a.value_cache : a.key_cache) + (to + (long long)(h - (is_value ? Hq + Hk : Hq)) * r.block_size) * d;
             }
             if (!is_value) {
                 const float norm = __frsqrt_rn(fmaf(sum, per_element, a.eps));
-                const float* table = reinterpret_cast<const float*>(tables + (x.t * 2 + (is_query ? 0 : 1)) * pairs);
+                const float* turns = reinterpret_cast<const float*>(table + (is_query ? 0 : pairs));
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     const int sl = in_row + s * LPR;
                     if (sl >= slots) continue;
                     if (sl < half / V)
-                        turn_pairs<T, VB, INTERLEAVED>(x0[u][s], x1[u][s], table, sl, slots, norm);
+                        turn_pairs<T, VB, INTERLEAVED>(x0[u][s], x1[u][s], turns, sl, slots, norm);
                     else
-                        scale_pairs<T, VB>(x0[u][s], x1[u][s], table, sl, slots, norm);
+                        scale_pairs<T, VB>(x0[u][s], x1[u][s], turns, sl, slots, norm);
                 }
             }
 #pragma unroll
@@ -205,53 +229,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_write_kv_kernel(const 
                     x1[u][s].store(dst + e1[s]);
                 }
         };
-        Row p{0, (tid >> 5) * RPW + sub};
-        while (p.h >= per_token) p.h -= per_token, ++p.t;
-        Row q = next(p);
-        load(0, p);  // (the first rows are on their way while the turns are made)
-        load(1, q);
-        if (tok0 == tok_begin) {
-            for (int i = tid; i < half; i += kNormThreads) steps[i] = turn_step(r.inv_freq[i]);
-            for (int i = tid; i < 2 * d; i += kNormThreads) {
-                const void* w = i < d ? a.q_weight : a.k_weight;
-                weights[i] = w ? weight_at(w, a.weight_dtype, i < d ? i : i - d) + a.weight_offset : 1.f;
-            }
+        for (int h = 0; h < rows; h += 2 * RPW) {
+            work(0, h + sub);
+            load(0, h + 2 * RPW + sub);
+            if (h + RPW < rows) work(1, h + RPW + sub);
+            load(1, h + 3 * RPW + sub);
         }
-        __syncthreads();
-        if (tid < ntok) {
-            const long long slot = a.slot_mapping[tok0 + tid];
-            long long to = -1;  // in rows of the cache, without the head
-            if (slot >= (long long)r.num_blocks * r.block_size) {
-                atomicOr(r.err, kErrBadSlot);
-            } else if (slot >= 0) {
-                const long long blk = slot / r.block_size;
-                to = blk * Hk * r.block_size + (slot - blk * r.block_size);
-            }
-            dest[tid] = to;
-        }
-        for (int i = tid; i < ntok * pairs; i += kNormThreads) {
-            const int t = i / pairs, pair = i - t * pairs;
-            const bool turns = pair < half;
-            const float2 cs = turns ? turn(steps[pair], a.positions[tok0 + t], r.factor) : make_float2(1.f, 0.f);
-            // the pair's elements
-            const int still = 2 * V * (pair / V) + pair % V;
-            const int ex = !turns ? still : INTERLEAVED ? 2 * pair : pair, ey = !turns ? still + V : INTERLEAVED ? 2 * pair + 1 : pair + half;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float wx = weights[k * d + ex], wy = weights[k * d + ey];
-                put_turn<V>(reinterpret_cast<float*>(tables + (t * 2 + k) * pairs), pair, slots, make_float4(cs.x * wx, -cs.y * wy, cs.y * wx, cs.x * wy));
-            }
-        }
-        __syncthreads();
-        // (a warp's lanes go on together: the first one's row is the first)
-        while (__any_sync(0xffffffffu, p.t < ntok)) {
-            work(0, p);
-            p = next(q);
-            load(0, p);
-            work(1, q);
-            q = next(p);
-            load(1, q);
-        }
+        __syncwarp();
     }
 }
 
@@ -261,13 +245,15 @@ template <typename T, int VB, int S>
 cudaError_t norm_typed(const NormRopeArgs& a, cudaStream_t stream) {
     const int slots = a.r.head_dim / (2 * (VB / (int)sizeof(T)));
     int lpr = 1;
-    while (lpr < slots && lpr < 32) lpr *= 2;
+    while (lpr * kNormSlots < slots && lpr < 32) lpr *= 2;
     if ((slots + lpr - 1) / lpr > S) return cudaErrorInvalidValue;
-    const int ctas = kNormCtasPerSm * a.num_sms, per = (int)(((long long)a.r.num_tokens + ctas - 1) / ctas);
-    const unsigned grid = (unsigned)((a.r.num_tokens + per - 1) / per);
-    const size_t smem = (size_t)kNormTokens * a.r.head_dim * sizeof(float4) + (size_t)(a.r.rotary_dim / 2) * sizeof(uint64_t) + (size_t)2 * a.r.head_dim * sizeof(float);
+    const int threads = a.r.head_dim <= 256 ? kNormThreads : kNormThreads / 2;  // (so that the turns take 32 KB at most)
+    const long long ctas = ((long long)a.r.num_tokens + threads / 32 - 1) / (threads / 32);
+    const unsigned grid = (unsigned)std::min(ctas, (long long)kNormCtasPerSm * a.num_sms);
+    const size_t smem = (size_t)(threads / 32) * a.r.head_dim * sizeof(float4) + (size_t)(a.r.rotary_dim / 2) * sizeof(uint64_t) +
+                        (size_t)2 * a.r.head_dim * sizeof(float);
     auto* kernel = a.r.interleaved ? norm_rope_write_kv_kernel<T, VB, S, true> : norm_rope_write_kv_kernel<T, VB, S, false>;
-    return launch_pdl(kernel, dim3(grid), dim3(kNormThreads), smem, stream, a, lpr, per);
+    return launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, a, lpr);
 }
 
 // Whether a row splits into chunks of 16 bytes: aligned bases and strides, slots of two chunks that do not straddle the end of the pairs.
@@ -285,8 +271,8 @@ bool splits(const NormRopeArgs& a, int eb) {
 cudaError_t norm_rope_write_kv_launch(const NormRopeArgs& a, cudaStream_t stream) {
     switch (a.r.dtype) {  // (head_dim <= 512: at most 64 slots of 8 floats, 32 of 16 halves, 256 of 2)
         case 0: return splits(a, 4) ? norm_typed<float, 16, 2>(a, stream) : norm_typed<float, 4, 8>(a, stream);
-        case 1: return splits(a, 2) ? norm_typed<__half, 16, 1>(a, stream) : norm_typed<__half, 2, 8>(a, stream);
-        default: return splits(a, 2) ? norm_typed<__nv_bfloat16, 16, 1>(a, stream) : norm_typed<__nv_bfloat16, 2, 8>(a, stream);
+        case 1: return splits(a, 2) ? norm_typed<__half, 16, 2>(a, stream) : norm_typed<__half, 2, 8>(a, stream);
+        default: return splits(a, 2) ? norm_typed<__nv_bfloat16, 16, 2>(a, stream) : norm_typed<__nv_bfloat16, 2, 8>(a, stream);
     }
 }
 

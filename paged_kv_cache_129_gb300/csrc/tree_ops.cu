@@ -112,12 +112,14 @@ constexpr int kCompactThreads = 256, kCompactCtasPerSm = 16;
 __device__ __forceinline__ bool is_path(const CompactArgs& a, int b, int n, int count) {
     if (count < 0 || count > n || count > a.max_accepted) return false;
     int before = -1;
-    for (int j = 0; j < count; ++j) {
+    bool ok = true;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {  // (loads that do not wait for the comparisons)
         const int node = a.accepted[(long long)b * a.max_accepted + j];
-        if (node <= before || node >= n) return false;
+        ok = ok && node > before && node < n;
         before = node;
     }
-    return true;
+    return ok;
 }
 
 // New lengths, and the blocks given back: one CTA, a contiguous run of requests per thread.
@@ -149,22 +151,38 @@ __device__ __forceinline__ void trim(const CompactArgs& a) {
         *length = L - n + k;
         return had - *keep;
     };
-    int keep, length, mine = 0;
-    for (int b = b0; b < b1; ++b) mine += max(0, give(b, &keep, &length));
+    int keep = 0, length = 0, gives = 0, mine = 0;  // (of one request per thread, as nearly always, kept until it is written)
+    for (int b = b0; b < b1; ++b) {
+        gives = give(b, &keep, &length);
+        mine += max(0, gives);
+    }
     if (tid == 0) sums[0] = 0;
     sums[tid + 1] = mine;
     __syncthreads();
-    if (tid == 0)
-        for (int i = 0; i < kCompactThreads; ++i) sums[i + 1] += sums[i];
+    if (tid < 32) {  // a run of the threads' sums per lane
+        constexpr int kRun = kCompactThreads / 32;
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) sum += sums[tid * kRun + i + 1];
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, before, o);
+            if (tid >= o) before += x;
+        }
+        before -= sum;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) sums[tid * kRun + i + 1] = before += sums[tid * kRun + i + 1];
+    }
     __syncthreads();
     const int total = sums[kCompactThreads];
     const bool room = free0 >= 0 && (long long)free0 + total <= a.num_blocks;
     if (!room) bits |= kErrBadTable;
     int at = free0 + sums[tid];
     for (int b = b0; b < b1; ++b) {
-        const int n = give(b, &keep, &length);
+        if (per > 1) gives = give(b, &keep, &length);
         if (room)
-            for (int j = 0; j < n; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + keep + j];
+            for (int j = 0; j < gives; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + keep + j];
         a.context_lens_out[b] = room ? length : a.context_lens[b];
     }
     if (tid == 0) *a.num_free_out = room ? free0 + total : free0;

@@ -7,8 +7,8 @@ that device's current stream.
 """
 from __future__ import annotations
 
-import ctypes
 import math
+from array import array
 from typing import NamedTuple, Optional
 
 import torch
@@ -188,19 +188,22 @@ def accept_tree(parents: torch.Tensor, tokens: torch.Tensor, choices: torch.Tens
 
 
 def _layer_pointers(caches, name: str):
-    """(pointers, shape, dtype, device) of the layers' caches: one [L, N, H_kv, bs, d] tensor, or a sequence of [N, H_kv, bs, d]."""
+    """(addresses of the layers' caches, shape, dtype, device): one [L, N, H_kv, bs, d] tensor, or a sequence of [N, H_kv, bs, d]."""
     if isinstance(caches, torch.Tensor):
         _cuda(caches, name)
-        _need(caches.dim() == 5 and caches.shape[0] >= 1, f"{name}: [layers, N, H_kv, bs, d], or a sequence of [N, H_kv, bs, d]")
-        first, step = caches.data_ptr(), caches[0].numel() * caches.element_size()
-        return [first + l * step for l in range(caches.shape[0])], caches.shape[1:], caches.dtype, caches.device
+        shape = caches.shape
+        if len(shape) != 5 or shape[0] < 1:
+            raise ValueError(f"{name}: [layers, N, H_kv, bs, d], or a sequence of [N, H_kv, bs, d]")
+        first, step = caches.data_ptr(), caches.stride(0) * caches.element_size()
+        # (a layer without elements has no stride to speak of: the library refuses its sizes)
+        return array("Q", range(first, first + shape[0] * step, step) if step else [first] * shape[0]), shape[1:], caches.dtype, caches.device
     _need(len(caches) >= 1, f"{name}: a cache per layer")
     like = caches[0]
     for c in caches:
         _cuda(c, name)
         if c.dim() != 4 or c.shape != like.shape or c.dtype is not like.dtype or c.device != like.device:
             raise ValueError(f"{name}: caches [N, H_kv, bs, d] of one shape, dtype and device")
-    return [c.data_ptr() for c in caches], like.shape, like.dtype, like.device
+    return array("Q", [c.data_ptr() for c in caches]), like.shape, like.dtype, like.device
 
 
 def compact_tree(key_caches, value_caches, slot_mapping: torch.Tensor, q_offsets: torch.Tensor, accepted: torch.Tensor,
@@ -229,9 +232,7 @@ def compact_tree(key_caches, value_caches, slot_mapping: torch.Tensor, q_offsets
     _need(free_blocks.shape == (num_blocks,) and num_free.numel() == 1, "free_blocks: int32 [num_blocks], num_free: int32 [1]")
     out = _outputs(out, TreeState, (((b,), torch.int32), (tuple(num_free.shape), torch.int32)), dev, stream)
     _one_device(dev, slot_mapping, q_offsets, accepted, num_accepted, block_tables, context_lens, free_blocks, num_free, *out)
-    n = len(keys)
-    arr = ctypes.c_void_p * n
-    _launch(library().pa_compact_tree, dev, stream, arr(*keys), arr(*values), n, slot_mapping.data_ptr(), q_offsets.data_ptr(),
+    _launch(library().pa_compact_tree, dev, stream, keys.buffer_info()[0], values.buffer_info()[0], len(keys), slot_mapping.data_ptr(), q_offsets.data_ptr(),
             accepted.data_ptr(), num_accepted.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), free_blocks.data_ptr(),
             num_free.data_ptr(), out.context_lens.data_ptr(), out.num_free.data_ptr(), b, slot_mapping.shape[0], accepted.shape[1],
             hkv, d, bs, width, num_blocks, _TORCH_DTYPES[dtype])
