@@ -31,9 +31,11 @@ __device__ __forceinline__ int nodes_of(const int32_t* q_offsets, int b, int num
 constexpr int kMaskThreads = 128;
 
 // A CTA per request, a thread per node: the ancestors of a node come in descending order, so a thread fills one word after the other,
-// from the last, and writes each once.  The CTA behind the last request clears the rows behind its nodes.
+// from the last, and writes each once.  Nodes whose parent is the one before them form runs, cut at multiples of 32 (so that one lies in one
+// word); a thread takes a run at a time: long chains are not followed node by node.  The CTA behind the last request clears the rows behind its
+// nodes.
 __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const TreeMaskArgs a) {
-    __shared__ int parent[kMaxTreeNodes];
+    __shared__ int parent[kMaxTreeNodes], run[kMaxTreeNodes];  // a node's parent; the first node of its run
     griddep_wait();
     griddep_launch_dependents();
     const int b = blockIdx.x, W = a.mask_words;
@@ -48,10 +50,12 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const TreeMask
     const int n = nodes_of(a.q_offsets, b, a.num_tokens, min(kMaxTreeNodes, 64 * W), &first, &bad);
     const int cached = a.context_lens[b] - n;
     if (cached < 0) bad = true;
-    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-        const int p = a.parents[first + i];
-        if (p < -1 || p >= i) bad = true;  // (a node without a parent before it is a root)
-        parent[i] = p < i ? max(p, -1) : -1;
+    for (int i = threadIdx.x; i < (n + 31) / 32 * 32; i += kMaskThreads) {  // (whole warps)
+        int p = i < n ? a.parents[first + i] : -1;
+        if (p < -1 || p >= i) bad = bad || i < n, p = -1;  // (a node without a parent before it is a root)
+        const unsigned starts = __ballot_sync(0xffffffffu, p != i - 1 || i % 32 == 0);
+        parent[i] = p;
+        run[i] = (i & ~31) + 31 - __clz(starts & (0xffffffffu >> (31 - i % 32)));
     }
     if (bad) atomicOr(a.err, kErrBadContext);
     __syncthreads();
@@ -60,7 +64,12 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(const TreeMask
         int node = i, depth = 0;
         for (int w = W - 1; w >= 0; --w) {
             unsigned long long word = 0;
-            for (; node >= 64 * w; node = parent[node], ++depth) word |= 1ull << (node - 64 * w);
+            while (node >= 64 * w) {
+                const int from = run[node];
+                word |= (~0ull >> (63 - (node - from))) << (from - 64 * w);
+                depth += node - from + 1;
+                node = parent[from];
+            }
             row[w] = (int64_t)word;
         }
         a.positions[first + i] = max(0, cached) + depth - 1;
