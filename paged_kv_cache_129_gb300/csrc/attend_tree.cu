@@ -192,7 +192,7 @@ struct Smem {
     uint64_t job_full[kPieces], job_free[kPieces], side_full[Tile<D>::kRing], copied[Tile<D>::kRing];
     uint64_t q_full[2], q_free[2], kv_full[Tile<D>::kBuffers], kv_empty[Tile<D>::kBuffers];
     uint64_t dirty_full[Tile<D>::kCleanRing], clean_full[Tile<D>::kCleanRing];
-    uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], join_full, join_done, drain[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -225,19 +225,24 @@ __device__ __forceinline__ int value_fill(bool paired, int n, int tile) {
 // The first key tile whose V is cleaned: the one with the request's first node (or the context's end).
 __device__ __forceinline__ int first_cleaned(const Job& j) { return max(0, j.L - j.n) / kTile; }
 
-// Tensor memory: per stream 64 columns of scores, then twice 32 of the weights P made of them, in turn; behind both streams' D columns of
-// output each.  The next scores can be made as soon as these are in registers, and are ready when their turn comes.  (P in the scores'
-// place, scores of a pair in products of 128 columns, 66 cycles where two of 64 take 100: every tile waited for its products,
-// 4570 cycles a tile, and as long with the streams taking turns.)
-constexpr int kWeightsAt = 64;
+// Tensor memory: per stream two buffers of 64 columns, used in turn, for the scores of a half and then, over the first of them, the 32 columns of
+// weights P made of them; behind both streams' D columns of output each.  The scores of a half are issued right behind the output of the half
+// before the last, which has then read the P that they overwrite, and are ready when their turn comes.  (Scores of a pair in products of 128
+// columns, 66 cycles where two of 64 take 100: every tile waited for its products, 4570 cycles a tile, and as long with the streams
+// taking turns.)
 template <int D>
 __device__ __forceinline__ uint32_t output_at(int t) { return 256 + t * D; }
+
+// A bounded wait by a whole warp: all lanes go on, or none.  (Tried once before warp_wait()'s loop: 157 to 150 us for wide trees.)
+__device__ __forceinline__ bool ready(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait(bar, parity, err, abort);
+}
 
 // Piece i of the share, for a warp of any role but the look-ahead's, which writes them; false if a wait gave up.
 constexpr int kReaders = kQueryWarp;  // (all roles' warps but one)
 template <int D>
 __device__ __forceinline__ bool read_job(Smem<D>& sm, unsigned i, Job* job, unsigned* err) {
-    if (!warp_wait(&sm.job_full[i % kPieces], (i / kPieces) & 1, err, &sm.abort)) return false;
+    if (!ready(&sm.job_full[i % kPieces], (i / kPieces) & 1, err, &sm.abort)) return false;
     *job = sm.jobs[i % kPieces];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.job_free[i % kPieces]);
@@ -291,7 +296,7 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, Seam* seams,
             more = unit < start.stop && seq < a.num_seqs;
         }
         const bool have = j.begin < j.end;
-        if (i >= kPieces && !warp_wait(&sm.job_free[i % kPieces], (i / kPieces - 1) & 1, a.err, &sm.abort)) return;
+        if (i >= kPieces && !ready(&sm.job_free[i % kPieces], (i / kPieces - 1) & 1, a.err, &sm.abort)) return;
         if (lane == 0) {
             sm.jobs[i % kPieces] = j;
             mbar_arrive(&sm.job_full[i % kPieces]);
@@ -311,7 +316,7 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, Seam* seams,
             const unsigned masked = __ballot_sync(0xffffffffu, mine && !in) | (tile >= cleaned ? 1u << 31 : 0u);
             if (tiles >= AHEAD) {
                 const unsigned before = tiles - AHEAD;
-                if (!warp_wait(&sm.copied[before % RING], (before / RING) & 1, a.err, &sm.abort)) return;
+                if (!ready(&sm.copied[before % RING], (before / RING) & 1, a.err, &sm.abort)) return;
             }
             const int slot = tiles % RING;
             if (lane < 8) sm.place[slot][lane] = place;
@@ -350,8 +355,8 @@ __device__ __forceinline__ void copy_tiles(const TreeAttendArgs& a, Smem<D>& sm,
             const Fill f = fill_of(job.paired, n, i);
             const int buf = fills % N;
             const unsigned tile = tiles + f.tile, side = tile % RING;
-            ok = f.value || warp_wait(&sm.side_full[side], (tile / RING) & 1, a.err, &sm.abort);
-            ok = ok && warp_wait(&sm.kv_empty[buf], ((fills / N) & 1) ^ 1, a.err, &sm.abort);
+            ok = f.value || ready(&sm.side_full[side], (tile / RING) & 1, a.err, &sm.abort);
+            ok = ok && ready(&sm.kv_empty[buf], ((fills / N) & 1) ^ 1, a.err, &sm.abort);
             if (!ok) break;
             const bool clean = f.value && (sm.masked[side] >> 31);
             uint64_t* bar = clean ? &sm.dirty_full[cleaned % kCleanRing] : &sm.kv_full[buf];
@@ -410,7 +415,7 @@ __device__ __forceinline__ void clean_tiles(const TreeAttendArgs& a, Smem<D>& sm
         for (int tile = max(it.begin, first_cleaned(it)); tile < it.end; ++tile, ++cleaned) {
             const unsigned fill = fills + value_fill(it.paired, n, tile - it.begin), slot = cleaned % kCleanRing;
             unsigned char* v = sm.kv[fill % N];
-            if (!warp_wait(&sm.dirty_full[slot], (cleaned / kCleanRing) & 1, a.err, &sm.abort)) return;
+            if (!ready(&sm.dirty_full[slot], (cleaned / kCleanRing) & 1, a.err, &sm.abort)) return;
             const int p0 = tile * kTile, end = min(kTile, it.L - p0), first = max(0, base - p0);
             const int block_end = min(kTile, (end + BS - 1) / BS * BS);
             for (int r = end + sub; r < block_end; r += RPP) *reinterpret_cast<uint4*>(v + Tile<D>::at(r, u)) = make_uint4(0u, 0u, 0u, 0u);
@@ -465,37 +470,31 @@ __device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>&
     constexpr uint32_t kHalf = Tile<D>::kOperand / 2 >> 4;
     const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // the query rows are negated instead of the scale
     unsigned buf = 0, phase = 0, query = 0;  // the next fill's buffer and the parity of its phase; the piece's first query tile
-    unsigned p_phase = 0, free_phase = 0;    // parities of the next phases: bit b of P buffer b's
+    unsigned p_phase = 0;                    // parities of the next phases of p_full: bit b of buffer b's
     // waits for the next fill; its buffer, or -1
     auto take = [&] {
-        if (!warp_wait(&sm.kv_full[buf], phase, a.err, abort)) return -1;
+        if (!ready(&sm.kv_full[buf], phase, a.err, abort)) return -1;
         tc_fence_after();
         const int got = (int)buf;
         if (++buf == N) buf = 0, phase ^= 1;
         return got;
     };
-    // scores of 64 rows of K, once those before are in registers
+    // scores of 64 rows of K, into buffer b
     const uint32_t desc = idesc_of(kTile / 2, false, kBf16) | negate;
-    auto scores = [&](uint64_t qd, uint64_t kd, bool first) {
-        if (!first) {
-            if (!warp_wait(&sm.s_free[t], free_phase, a.err, abort)) return false;
-            free_phase ^= 1;
-            tc_fence_after();
-        }
+    auto scores = [&](int b, uint64_t qd, uint64_t kd) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            mma_ss(s_at, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4), desc, k > 0);
-        tc_commit(&sm.s_full[t]);
-        return true;
+            mma_ss(s_at + 64 * b, qd + (((k / 4) * kPanel + (k % 4) * 32) >> 4), kd + (((k / 4) * 1024 + (k % 4) * 32) >> 4), desc, k > 0);
+        tc_commit(&sm.s_full[t][b]);
     };
     // output of P buffer b times 64 rows of V
     auto output = [&](int b, uint64_t vd, bool add) {
-        if (!warp_wait(&sm.p_full[t][b], p_phase >> b & 1, a.err, abort)) return false;
+        if (!ready(&sm.p_full[t][b], p_phase >> b & 1, a.err, abort)) return false;
         p_phase ^= 1u << b;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
-            mma_ts(o_at, s_at + kWeightsAt + 32 * b + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), add || k > 0);
+            mma_ts(o_at, s_at + 64 * b + 8 * k, vd + (k * 2 * Tile<D>::kGroup >> 4), idesc_of(D, true, kBf16), add || k > 0);
         tc_commit(&sm.pv_done[t][b]);
         return true;
     };
@@ -507,45 +506,29 @@ __device__ __forceinline__ void issue_products(const TreeAttendArgs& a, Smem<D>&
         const unsigned mine = query + (job.paired ? t : 0), qbuf = mine & 1;
         query += job.paired ? 2 : 1;
         // (a stream that skips a pair's other tile: the phase before the one that it waits for is over, staged before one that it has seen)
-        if (!warp_wait(&sm.q_full[qbuf], mine >> 1 & 1, a.err, abort)) return;
+        if (!ready(&sm.q_full[qbuf], mine >> 1 & 1, a.err, abort)) return;
         const uint64_t qd = q0 + (qbuf * Tile<D>::kOperand >> 4);
-        int at = take();
-        if (at < 0) return;
-        // (the last scores of the piece before are in registers: their weights, which came later, were waited for)
-        uint64_t kd = k0 + (at * Tile<D>::kOperand >> 4);
-        if (job.paired) {
-            scores(qd, kd, true);
+        // (both buffers are free: their weights were waited for, and the outputs that read them issued)
+        // Step u of a pair is half u % 2 of tile u / 2; of a split piece this stream's half of tile u.  Its scores are issued two steps ahead.
+        const int steps = job.paired ? 2 * n : n;
+        int k_at = 0, v_at = 0;
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                if (!scores(qd, kd + kHalf, false)) return;
-                tc_commit(&sm.kv_empty[at]);
-                const int v = take();
-                if (v < 0) return;
-                const uint64_t vd = v0 + (v * Tile<D>::kOperand >> 4);
-                if (!output(0, vd, i > 0)) return;
-                if (i + 1 < n) {
-                    if ((at = take()) < 0) return;
-                    kd = k0 + (at * Tile<D>::kOperand >> 4);
-                    if (!scores(qd, kd, false)) return;
-                }
-                if (!output(1, vd + kHalf, true)) return;
-                tc_commit(&sm.kv_empty[v]);
+        for (int u = -2; u < steps; ++u) {
+            const int b = u & 1;
+            const bool second = job.paired && b == 1;  // the tile is there already, and done with behind this half
+            const uint32_t half = (job.paired ? b : t) * kHalf;
+            if (u >= 0) {
+                if (!second && (v_at = take()) < 0) return;
+                if (!output(b, v0 + (v_at * Tile<D>::kOperand >> 4) + half, u > 0)) return;
+                if (!job.paired || second) tc_commit(&sm.kv_empty[v_at]);
             }
-            tc_commit(&sm.q_free[qbuf]);
-        } else {
-            scores(qd, kd + t * kHalf, true);
-            tc_commit(&sm.kv_empty[at]);
-#pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                if (i + 1 < n) {
-                    if ((at = take()) < 0 || !scores(qd, k0 + (at * Tile<D>::kOperand >> 4) + t * kHalf, false)) return;
-                    tc_commit(&sm.kv_empty[at]);
-                }
-                const int v = take();
-                if (v < 0 || !output(i & 1, v0 + (v * Tile<D>::kOperand >> 4) + t * kHalf, i > 0)) return;
-                tc_commit(&sm.kv_empty[v]);
+            if (u + 2 < steps) {
+                if (!second && (k_at = take()) < 0) return;
+                scores(b, qd, k0 + (k_at * Tile<D>::kOperand >> 4) + half);
+                if (!job.paired || second) tc_commit(&sm.kv_empty[k_at]);
             }
         }
+        if (job.paired) tc_commit(&sm.q_free[qbuf]);
         tc_commit(&sm.q_free[qbuf]);
         tc_commit(&sm.o_full[t]);
     }
@@ -566,7 +549,7 @@ __device__ __forceinline__ void stage_queries(const TreeAttendArgs& a, Smem<D>& 
 #pragma unroll 1
         for (int k = 0; k < (job.paired ? 2 : 1); ++k, ++tile) {
             const int buf = tile & 1, first = job.row0 + k * kTile, rows = min(kTile, job.n * group - first);
-            if (!warp_wait(&sm.q_free[buf], ((tile >> 1) & 1) ^ 1, a.err, &sm.abort)) return;
+            if (!ready(&sm.q_free[buf], ((tile >> 1) & 1) ^ 1, a.err, &sm.abort)) return;
 #pragma unroll 1
             for (int b = 0; b < rows; b += 32) {
                 const int v = first + b + lane, node = v / group;  // this lane's row; its address goes to the lanes that copy it
@@ -620,15 +603,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
     return m;
 }
-__device__ __forceinline__ float row_max(const uint32_t (&s)[64]) {
-    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
-#pragma unroll
-    for (int i = 0; i < 64; i += 8)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
-    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-}
-
 template <typename T>
 __device__ __forceinline__ uint32_t round2(float2 x);
 template <>
@@ -640,25 +614,6 @@ template <>
 __device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float2 x) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// P of 64 scores: exp2(score * factor - mu), rounded, over the scores in tensor memory; returns the sum of the exponentials.
-template <typename T>
-__device__ __forceinline__ float row_exp(uint32_t (&s)[64], uint32_t s_at, float factor, float mu) {
-    float2 sum = make_float2(0.f, 0.f);
-    const float2 f = make_float2(factor, factor), m = make_float2(-mu, -mu);
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-#pragma unroll
-        for (int i = c; i < c + 32; i += 2) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f, m);
-            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-            sum = add2(sum, e);
-            s[i / 2] = round2<T>(e);
-        }
-        tmem_st16(s_at + c / 2, *reinterpret_cast<uint32_t(*)[16]>(&s[c / 2]));
-    }
-    return sum.x + sum.y;
 }
 
 // Eight 16-byte units of a row per lane become, in groups of eight lanes, one unit of each of the group's rows: x[r] is unit lane % 8 of
@@ -692,7 +647,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
     // (kept above zero, so that masked scores stay -inf)
     const float factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-38f);
     unsigned pieces = 0, joins = 0, tiles_before = 0, cleaned = 0;  // so far
-    unsigned s_phase = 0, pv_phase = 3;  // parity of the next phase of s_full; of the last one of pv_done: bit b of P buffer b's
+    unsigned s_phase = 0, pv_phase = 3;  // parities of the next phases of s_full, of the last ones of pv_done: bit b of buffer b's
 #pragma unroll 1
     for (unsigned piece = 0;; ++piece) {
         Job job;
@@ -711,53 +666,57 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
         for (int step = 0; step < steps; ++step) {
             const int half = paired ? step & 1 : t, local = paired ? step >> 1 : step, b = step & 1;
             const int p0 = (job.begin + local) * kTile;
-            if (!warp_wait(&sm.s_full[t], s_phase, a.err, abort)) return;
-            s_phase ^= 1;
+            if (!ready(&sm.s_full[t][b], s_phase >> b & 1, a.err, abort)) return;
+            s_phase ^= 1u << b;
             tc_fence_after();
-            const bool last = step + 1 == steps;
             const unsigned masked = sm.masked[(tiles_before + local) % RING];
             const bool clean = (masked >> 31) && (!paired || half == 1);  // V of this tile is cleaned
             if (!warp_live) {  // rows that nobody reads: whatever lies there may be multiplied
                 if (clean) {
-                    if (!warp_wait(&sm.clean_full[cleaned % kCleanRing], (cleaned / kCleanRing) & 1, a.err, abort)) return;
+                    if (!ready(&sm.clean_full[cleaned % kCleanRing], (cleaned / kCleanRing) & 1, a.err, abort)) return;
                     ++cleaned;
                 }
-                if (lane == 0) {
-                    if (!last) mbar_arrive(&sm.s_free[t]);
-                    mbar_arrive(&sm.p_full[t][b]);
-                }
+                if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
                 pv_phase ^= 1u << b;
                 continue;
             }
-            // The half's weights, from its scores.  (A body for either case: where only the masking is conditional, the 64 scores are moved to
-            // other registers on the way around it, 135 instructions of 456.)
+            // The half's weights, from its scores, in two passes of two chunks of 32 columns; the second reads the scores again.  (Softmax warps run
+            // through this code once a step, and fetching it is what bounds them: all 64 scores in registers, one pass, 145 us
+            // for wide trees; two steps unrolled 183.)  A body for either case of edge.
             auto weigh = [&](auto edge) {
-                uint32_t s[64];
-                tmem_ld32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                tmem_ld32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                tc_wait_ld(s);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && !last) mbar_arrive(&sm.s_free[t]);
-                if constexpr (decltype(edge)::value) {
-                    const uint64_t mine =
-                        live ? seen_from<BS>(words, word0, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
+                constexpr bool kEdge = decltype(edge)::value;
+                const uint32_t at = s_at + 64 * b;
+                uint64_t mine = ~0ull;
+                if constexpr (kEdge) {
+                    mine = live ? seen_from<BS>(words, word0, a.mask_words, p0 + 64 * half, base, job.n, (masked & 0xffu) >> (half * (64 / BS))) : 0ull;
                     if (half == 0) seen0 = mine;
                     else seen1 = mine;
-                    const uint32_t lo = (uint32_t)mine, hi = (uint32_t)(mine >> 32);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (!(lo >> i & 1)) s[i] = 0xff800000u;
-                        if (!(hi >> i & 1)) s[32 + i] = 0xff800000u;
-                    }
                 }
-                const float top = row_max(s) * factor;
+                auto chunk = [&](int c, uint32_t (&s)[32]) {
+                    tmem_ld32(at + 32 * c, s);
+                    tc_wait_ld(s);
+                    if constexpr (kEdge) {
+                        const uint32_t w = (uint32_t)(mine >> (32 * c));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(w >> i & 1)) s[i] = 0xff800000u;
+                    }
+                };
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t s[32];
+                    chunk(c, s);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) x[i / 2 % 4] = max3(x[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                }
+                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * factor;
                 if (step == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > m + 8.f)) {
                     // The output so far has to be there.  (The phase before the one that is meant is over: these scores were issued behind the
                     // output before the last, and a commit waits for all products before it.  So P's place is free too.)
-                    if (!warp_wait(&sm.pv_done[t][b ^ 1], pv_phase >> (b ^ 1) & 1, a.err, abort)) return false;
+                    if (!ready(&sm.pv_done[t][b ^ 1], pv_phase >> (b ^ 1) & 1, a.err, abort)) return false;
                     tc_fence_after();
                     const float mn = fmaxf(m, top);
                     const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
@@ -773,15 +732,32 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
                         tmem_st16(o_at + c, o);
                     }
                 }
-                l += row_exp<T>(s, s_at + kWeightsAt + 32 * b, factor, m == -INFINITY ? 0.f : m);
+                // P: exp2(score * factor - mu), rounded, over the scores of the first chunk, which are in registers by then
+                const float mu = m == -INFINITY ? 0.f : m;
+                float2 sum = make_float2(0.f, 0.f);
+                const float2 f2 = make_float2(factor, factor), m2 = make_float2(-mu, -mu);
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t s[32];
+                    chunk(c, s);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2, m2);
+                        const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                        sum = add2(sum, e);
+                        s[i / 2] = round2<T>(e);
+                    }
+                    tmem_st16(at + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
+                }
+                l += sum.x + sum.y;
                 return true;
             };
             // edge: a block that is not there, or (bit 31) a tile with nodes or the context's end
-            if (!(masked ? weigh(std::true_type{}) : weigh(std::false_type{}))) return;
+            if (!masked) { if (!weigh(std::false_type{})) return; } else { if (!weigh(std::true_type{})) return; }
             pv_phase ^= 1u << b;
             if (clean) {
                 const unsigned note = cleaned % kCleanRing;
-                if (!warp_wait(&sm.clean_full[note], (cleaned / kCleanRing) & 1, a.err, abort)) return;
+                if (!ready(&sm.clean_full[note], (cleaned / kCleanRing) & 1, a.err, abort)) return;
                 ++cleaned;
                 if (sm.special[note]) {
                     const int from = max(0, base - p0);
@@ -809,7 +785,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
 
         // the piece's result
         const bool cut = job.begin > 0 || job.end < job.tiles, join = !paired;
-        if (!warp_wait(&sm.o_full[t], pieces & 1, a.err, abort)) return;
+        if (!ready(&sm.o_full[t], pieces & 1, a.err, abort)) return;
         tc_fence_after();
         ++pieces;
         float f0 = 1.f, f1 = 0.f;  // factors of this stream's output and of the other's
@@ -819,7 +795,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.join_full);
-            if (!warp_wait(&sm.join_full, joins & 1, a.err, abort)) return;
+            if (!ready(&sm.join_full, joins & 1, a.err, abort)) return;
             tc_fence_after();
             const float2 o = sm.state[t ^ 1][r];
             const float ol = __uint_as_float(__float_as_uint(o.y) & 0x7fffffffu);
@@ -920,7 +896,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
         if (join) {  // neither stream's output is written again before both have read it
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.join_done);
-            if (!warp_wait(&sm.join_done, joins & 1, a.err, abort)) return;
+            if (!ready(&sm.join_done, joins & 1, a.err, abort)) return;
             ++joins;
         }
     }
@@ -941,9 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_free[i], 2);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_free[i], 4);
             for (int h = 0; h < 2; ++h) {
+                mbar_init(&sm.s_full[i][h], 1);
                 mbar_init(&sm.p_full[i][h], 4);
                 mbar_init(&sm.pv_done[i][h], 1);
             }
