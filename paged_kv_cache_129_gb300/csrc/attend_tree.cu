@@ -34,18 +34,18 @@ namespace pa {
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 __host__ __device__ inline size_t record_floats(int D) { return (size_t)kTile * (D + 2); }
 
 constexpr int kSoftmaxWarps = 8;  // four per stream
 constexpr int kIssueWarp = kSoftmaxWarps;  // two, one per stream
 constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp = kLookWarp + 1, kQueryWarp = kCleanWarp + 1;
-constexpr int kThreads = 512;  // four warpgroups, so that registers can go from the others' to the softmax's
+constexpr int kThreads = (kQueryWarp + 1) * 32;
 constexpr int kPieces = 4;  // pieces of the share that the look-ahead warp may be ahead of the others
 
 // Cost of work in shares: of a key tile of a pair and of a split piece, and of a unit besides its tiles.
-constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 16;
+constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 12;
 constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
 
 // A request as the shares see it: n nodes on L positions.
@@ -703,7 +703,7 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
                     }
                 };
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t s[32];
                     chunk(c, s);
@@ -753,7 +753,11 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
                 return true;
             };
             // edge: a block that is not there, or (bit 31) a tile with nodes or the context's end
-            if (!masked) { if (!weigh(std::false_type{})) return; } else { if (!weigh(std::true_type{})) return; }
+            if (!masked) {
+                if (!weigh(std::false_type{})) return;
+            } else if (!weigh(std::true_type{})) {
+                return;
+            }
             pv_phase ^= 1u << b;
             if (clean) {
                 const unsigned note = cleaned % kCleanRing;
@@ -913,37 +917,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+    if (warp == 0) {  // a lane per place
+        const int i = threadIdx.x;
+        if (i < 2) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_free[i], 2);
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(&sm.s_full[i][h], 1);
-                mbar_init(&sm.p_full[i][h], 4);
-                mbar_init(&sm.pv_done[i][h], 1);
-            }
             mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.drain[i], 1);
+            mbar_init(i ? &sm.join_full : &sm.join_done, kSoftmaxWarps);
         }
-        for (int i = 0; i < kPieces; ++i) {
+        if (i < 4) {
+            mbar_init(&sm.s_full[i >> 1][i & 1], 1);
+            mbar_init(&sm.p_full[i >> 1][i & 1], 4);
+            mbar_init(&sm.pv_done[i >> 1][i & 1], 1);
+        }
+        if (i < kPieces) {
             mbar_init(&sm.job_full[i], 1);
             mbar_init(&sm.job_free[i], kReaders);
         }
-        for (int i = 0; i < Tile<D>::kRing; ++i) {
+        if (i < Tile<D>::kRing) {
             mbar_init(&sm.side_full[i], 1);
             mbar_init(&sm.copied[i], 1);
         }
-        for (int i = 0; i < Tile<D>::kBuffers; ++i) {
+        if (i < Tile<D>::kBuffers) {
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 2);
         }
-        for (int i = 0; i < Tile<D>::kCleanRing; ++i) {
+        if (i < Tile<D>::kCleanRing) {
             mbar_init(&sm.dirty_full[i], 1);
             mbar_init(&sm.clean_full[i], 1);
         }
-        mbar_init(&sm.join_full, kSoftmaxWarps);
-        mbar_init(&sm.join_done, kSoftmaxWarps);
-        mbar_init(&sm.drain[0], 1);
-        mbar_init(&sm.drain[1], 1);
         sm.abort = 0;
         fence_barrier_init();
     }
@@ -955,12 +958,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
     const Start start = find_share(a, *reinterpret_cast<Scratch*>(&sm.state));  // (synchronises the CTA)
     tc_fence_after();
     Notes<D>& notes = all_notes[blockIdx.x];
-    // 512 threads may have 128 registers each.  Of 16 warps' 2048, the softmax's eight take 168, with which they spill none (wide trees 176
-    // to 161 us), and the others 80.
-    if (warp < kSoftmaxWarps)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp < kSoftmaxWarps) {
         softmax_rows<T, D, BS>(a, records, sm, notes);
     } else if (warp == kCopyWarp) {
@@ -971,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
         clean_tiles<T, D, BS>(a, sm, notes);
     } else if (warp == kQueryWarp) {
         stage_queries<T, D>(a, sm);
-    } else if (warp < kCopyWarp) {
+    } else {
         const int t = __shfl_sync(0xffffffffu, warp - kIssueWarp, 0);
         issue_products<T, D>(a, sm, t);
         if (__any_sync(0xffffffffu, sm.abort)) {  // products still in flight read shared and tensor memory
@@ -989,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const TreeAtte
 
 // Joins the partial results of the units that share boundaries cut: CTA (boundary, rows), a warp per row, D / 32 elements per lane.  The
 // parts' maxima and sums are read by a lane each.
-constexpr int kJoinRows = kJoinThreads / 32, kJoinSplit = 16;
+constexpr int kJoinRows = kJoinThreads / 32, kJoinSplit = 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeAttendArgs a, const Seam* seams, const float* records) {
     griddep_wait();
@@ -1012,7 +1009,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeAtten
             const int c = c0 + lane, from = cut(c);
             const bool has = c <= s.last && from < cut(c + 1);
             const size_t at = ((size_t)c * 4 + (from > 0 ? 0 : 2) + tile) * record_floats(D);
+            unsigned left = __ballot_sync(0xffffffffu, has);
+            constexpr int kAtOnce = 4;
+            alignas(16) float x[kAtOnce][E];
+            int part[kAtOnce];  // whose; -1: none
+            auto fetch = [&] {
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    part[k] = left ? __ffs(left) - 1 : -1;
+                    const size_t of = __shfl_sync(0xffffffffu, at, max(0, part[k]));
+                    if (part[k] >= 0) *reinterpret_cast<Vec*>(x[k]) = *reinterpret_cast<const Vec*>(records + of + 2 * kTile + (size_t)rr * D + lane * E);
+                    left &= left - 1;
+                }
+            };
             const float mc = has ? records[at + rr] : -INFINITY, lc = has ? records[at + kTile + rr] : 0.f;
+            fetch();  // (on their way while the weights are made)
             float mn = mc;
 #pragma unroll
             for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
@@ -1026,25 +1037,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeAtten
             m = mn;
 #pragma unroll
             for (int i = 0; i < E; ++i) o[i] *= f;
-            unsigned left = __ballot_sync(0xffffffffu, has);
-            while (left) {
-                constexpr int kAtOnce = 4;
-                alignas(16) float x[kAtOnce][E], wj[kAtOnce];
+            for (;;) {
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
-                    const int j = left ? __ffs(left) - 1 : 0;
-                    wj[k] = left ? __shfl_sync(0xffffffffu, weight, j) : 0.f;
-                    const size_t part = __shfl_sync(0xffffffffu, at, j);
-                    if (left) *reinterpret_cast<Vec*>(x[k]) = *reinterpret_cast<const Vec*>(records + part + 2 * kTile + (size_t)rr * D + lane * E);
-                    else
+                    const float wk = __shfl_sync(0xffffffffu, weight, max(0, part[k]));
+                    if (part[k] >= 0)
 #pragma unroll
-                        for (int i = 0; i < E; ++i) x[k][i] = 0.f;
-                    left &= left - 1;
+                        for (int i = 0; i < E; ++i) o[i] = fmaf(x[k][i], wk, o[i]);
                 }
-#pragma unroll
-                for (int k = 0; k < kAtOnce; ++k)
-#pragma unroll
-                    for (int i = 0; i < E; ++i) o[i] = fmaf(x[k][i], wj[k], o[i]);
+                if (!left) break;
+                fetch();
             }
         }
         const int v = s.row0 + r, node = v / group;

@@ -231,6 +231,9 @@ ATTEND = [
     (2, 1, 64, 16, [10] * 300, [1, 0, 3, 2, 5, 7] * 50),
     (2, 2, 128, 32, [40], [1024]),
     (64, 1, 128, 16, [200, 0], [9, 5]),
+    (2, 1, 64, 16, [60000], [3]),  # one unit in the shares of more than 32 SMs
+    (3, 1, 64, 32, [5, 130, 0] * 600, [1, 0, 2] * 600),  # several requests to a thread that adds up costs
+    (300, 1, 128, 16, [40, 700], [2, 1]),  # more heads to a node than rows to a tile
 ]
 
 
@@ -390,6 +393,24 @@ def test_attend_tree_refuses_a_small_workspace_and_repeats_bit_for_bit():
         assert torch.equal(again, first)
     pa.check_error()
     check(c, first)
+
+
+def test_attend_tree_leaves_everything_as_it_was_without_nodes_and_with_overlapping_runs():
+    rng = np.random.default_rng(14)
+    c = attend_case(rng, 4, 2, 128, 16, "bf16", [100, 300], [5, 20], fill=0.0)
+    c["off"] = np.zeros(3, np.int32)
+    assert (attend(c) == 9.0).all()
+    pa.check_error()
+    c["off"], c["lens"] = np.zeros(1, np.int32), np.zeros(0, np.int32)
+    c["tables"] = np.zeros((0, 3), np.int32)
+    assert (attend(c) == 9.0).all()
+    pa.check_error()
+    # more rows in the runs than there are tokens: nothing is done
+    c = attend_case(rng, 4, 2, 128, 16, "bf16", [100] * 3, [5, 5, 5], pad=0, fill=0.0)
+    c["off"] = np.array([0, 14, 1, 15], np.int32)
+    out = []
+    assert status(lambda: out.append(attend(c))) == 7
+    assert (out[0] == 9.0).all()
 
 
 def test_attend_tree_of_one_node_is_a_decode_step():
