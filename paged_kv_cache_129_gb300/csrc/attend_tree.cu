@@ -1000,29 +1000,38 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeAtten
     bool parts = false;  // (a boundary inside the cost may still fall before the first tile or behind the last)
     for (int c = s.first + 1; c <= s.last; ++c) parts |= cut(c) > 0 && cut(c) < s.tiles;
     if (!parts) return;
+    // Lane i has part i of 32: whether it is there, and where its record is (nearly always there is no second round of 32).
+    int at = 0;
+    auto look = [&](int c0) {
+        const int c = c0 + lane, from = cut(c);
+        at = (int)((c * 4 + (from > 0 ? 0 : 2)) * record_floats(D));
+        return __ballot_sync(0xffffffffu, c <= s.last && from < cut(c + 1));
+    };
+    unsigned there = look(s.first);
     for (int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5); r < s.rows; r += gridDim.y * kJoinRows) {
-        const int tile = r / kTile, rr = r % kTile;
+        const int rr = r % kTile;
+        const float* of_tile = records + (r / kTile) * record_floats(D);
+        const float* of_row = of_tile + 2 * kTile + (size_t)rr * D + lane * E;
         float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) o[i] = 0.f;
         for (int c0 = s.first; c0 <= s.last; c0 += 32) {
-            const int c = c0 + lane, from = cut(c);
-            const bool has = c <= s.last && from < cut(c + 1);
-            const size_t at = ((size_t)c * 4 + (from > 0 ? 0 : 2) + tile) * record_floats(D);
-            unsigned left = __ballot_sync(0xffffffffu, has);
-            constexpr int kAtOnce = 4;
+            if (s.last - s.first >= 32) there = look(c0);
+            unsigned left = there;
+            constexpr int kAtOnce = 2;
             alignas(16) float x[kAtOnce][E];
             int part[kAtOnce];  // whose; -1: none
             auto fetch = [&] {
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
-                    part[k] = left ? __ffs(left) - 1 : -1;
-                    const size_t of = __shfl_sync(0xffffffffu, at, max(0, part[k]));
-                    if (part[k] >= 0) *reinterpret_cast<Vec*>(x[k]) = *reinterpret_cast<const Vec*>(records + of + 2 * kTile + (size_t)rr * D + lane * E);
+                    part[k] = __ffs(left) - 1;
+                    const int of = __shfl_sync(0xffffffffu, at, max(0, part[k]));
+                    if (part[k] >= 0) *reinterpret_cast<Vec*>(x[k]) = *reinterpret_cast<const Vec*>(of_row + of);
                     left &= left - 1;
                 }
             };
-            const float mc = has ? records[at + rr] : -INFINITY, lc = has ? records[at + kTile + rr] : 0.f;
+            const bool has = there >> lane & 1;
+            const float mc = has ? of_tile[at + rr] : -INFINITY, lc = has ? of_tile[at + kTile + rr] : 0.f;
             fetch();  // (on their way while the weights are made)
             float mn = mc;
 #pragma unroll
