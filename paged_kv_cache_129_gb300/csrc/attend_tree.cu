@@ -19,9 +19,13 @@
 // context are zeros; in the tiles that hold nodes or the context's end a warp clears the rows behind the end, and looks for infinities and
 // NaN in the nodes' V: these are taken out, noted, and put into the outputs of the rows that see them.
 // Numbers.  Scores, maxima, sums and the output accumulate in float32.  A weight is rounded to the cache's type for the second
-// product (half a step: bf16 2^-9 of it, as many bits as the output has; f16 2^-12, and 2^-25 of the reference below 2^-14).  The
+// product (half a step: bf16 2^-8 of it, as the output; f16 2^-11, and 2^-25 of the reference below 2^-14).  The
 // reference of the exponents follows the true maximum by steps of 2^8 at least: rescaling the output in tensor memory is rare that way, and weights stay
 // below 2^8.
+// Bound.  Long contexts (eight requests of 32k - 128k positions with 1 - 8 nodes) HBM: 475 us, 7.0 TB/s.  Steps (64 requests of 512 - 4096 with 16
+// nodes) 68 us, 4.6 TB/s: of an SM's 120 000 cycles 85 000 are its share of HBM's time, 15 000 pass before the first scores and the rest at the
+// pieces' ends.  Wide trees (16 requests of 2k - 8k with 48 - 128 nodes) 134 us, 0.90 PFLOP/s, tensor pipe 51 % busy: the softmax warps, whose code is
+// fetched as slowly as it is run.  Short mixed requests of D = 64 28 us: the same 15 000 cycles, the pieces' ends, the second launch.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -35,7 +39,7 @@ namespace pa {
 namespace {
 
 constexpr int kJoinThreads = 128;
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 __host__ __device__ inline size_t record_floats(int D) { return (size_t)kTile * (D + 2); }
 
 constexpr int kSoftmaxWarps = 8;  // four per stream
@@ -44,7 +48,9 @@ constexpr int kCopyWarp = kIssueWarp + 2, kLookWarp = kCopyWarp + 1, kCleanWarp 
 constexpr int kThreads = (kQueryWarp + 1) * 32;
 constexpr int kPieces = 4;  // pieces of the share that the look-ahead warp may be ahead of the others
 
-// Cost of work in shares: of a key tile of a pair and of a split piece, and of a unit besides its tiles.
+// Cost of work in shares: of a key tile of a pair and of a split piece, and of a unit besides its tiles.  Measured when chosen (steps / wide
+// trees / short mixed D = 64, us): 6, 4, 12: 68.8 / 137 / 27.8; 6, 4, 16: 69.2 / 136 / 30.5; 6, 4, 20: 69.2 / 137 / 31.4; 5, 4, 16: 69.0 / 138 / 31.3;
+// 7, 4, 16: 68.9 / 135 / 30.8.  (By the clock of an SM a split tile takes 2100 - 2600 cycles, a paired one 3000 - 3400, a piece 7000 - 9500 besides.)
 constexpr int kPairedCost = 6, kSplitCost = 4, kUnitCost = 12;
 constexpr int kMinShare = kUnitCost + 4 * kSplitCost;  // a CTA's share is not worth less than the pieces' overhead
 
@@ -73,7 +79,8 @@ struct Request {
 };
 
 // Key tiles of a unit before cost position x inside it (a cut falls between tiles; both sides of a boundary round alike).  A cut so near to
-// an end of the unit that the piece would cost more than its tiles goes to the end.
+// an end of the unit that the piece would cost more than its tiles goes to the end (1, that is not at all: 74.5 / 158 / 36.9 us where 3 took 72.5 / 157 /
+// 35.2, 2 72.1 / 158 / 37.1, 4 73.4 / 157 / 35.1).
 constexpr int kSnap = 3;
 __device__ __forceinline__ int tiles_in(long long x, int tiles, bool paired) {  // (a unit's tiles: below 2^24)
     const unsigned cost = (unsigned)max(0ll, min(x - kUnitCost, (long long)tiles * (paired ? kPairedCost : kSplitCost)));
@@ -233,7 +240,7 @@ __device__ __forceinline__ int first_cleaned(const Job& j) { return max(0, j.L -
 template <int D>
 __device__ __forceinline__ uint32_t output_at(int t) { return 256 + t * D; }
 
-// A bounded wait by a whole warp: all lanes go on, or none.  (Tried once before warp_wait()'s loop: 157 to 150 us for wide trees.)
+// A bounded wait by a whole warp: all lanes go on, or none.  (Tried once before warp_wait()'s loop: 157 to 150 us for wide trees when added.)
 __device__ __forceinline__ bool ready(uint64_t* bar, unsigned parity, unsigned* err, volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait(bar, parity, err, abort);
 }
@@ -617,8 +624,8 @@ __device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float2 x) {
 }
 
 // Eight 16-byte units of a row per lane become, in groups of eight lanes, one unit of each of the group's rows: x[r] is unit lane % 8 of
-// row r.  Stores of x[r] then write whole 128-byte lines; a row to a lane, each store of a warp touched 32 of them, and the results of
-// a piece took 4000 cycles.
+// row r.  Stores of x[r] then write whole 128-byte lines (a row to a lane, each store of a warp touched 32 of them, and the results of
+// a piece took 4000 cycles).
 __device__ __forceinline__ void transpose8(uint4 (&x)[8]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll

