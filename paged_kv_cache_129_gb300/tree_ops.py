@@ -41,21 +41,29 @@ class TreeState(NamedTuple):
     num_free: torch.Tensor  # int32 [1]
 
 
+def _int32s(names: str, *tensors) -> None:
+    """``_int32`` of several tensors, named only where one is none: these checks are much of a small call's time."""
+    for t in tensors:
+        if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+            for name, x in zip(names.split(), tensors):
+                _int32(x, name)
+
+
 def _outputs(out, kind, wanted, device, stream):
     """The outputs of a call: fresh ones, or the given ones if they have these shapes and dtypes."""
     if out is None:
         return kind(*[_fresh(shape, dtype, device, stream) for shape, dtype in wanted])
-    out = kind(*out)
+    if type(out) is not kind:
+        out = kind(*out)
     for t, (shape, dtype) in zip(out, wanted):
-        _cuda(t, "out")
-        if t.dtype is not dtype or t.shape != shape:
+        if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+            _cuda(t, "out")
             raise ValueError(f"out: {list(shape)} of {dtype}")
     return out
 
 
 def _nodes(parents: torch.Tensor, q_offsets: torch.Tensor) -> tuple:
-    _int32(parents, "parents")
-    _int32(q_offsets, "q_offsets")
+    _int32s("parents q_offsets", parents, q_offsets)
     if parents.dim() != 1 or q_offsets.dim() != 1 or q_offsets.shape[0] < 1:
         raise ValueError("parents: int32 [T], q_offsets: int32 [B + 1]")
     return parents.shape[0], q_offsets.shape[0] - 1
@@ -88,31 +96,37 @@ def norm_rope_write_kv(query: torch.Tensor, key: torch.Tensor, value: torch.Tens
     multiplied by ``q_weight + weight_offset`` or ``k_weight + weight_offset`` ([d], float32 or the queries' dtype; None:
     the norm alone) before its rotation, in the same pass.  ``inv_freq`` None: no rotation.  Returns the queries.
     """
-    for name, t in (("key_cache", key_cache), ("value_cache", value_cache), ("positions", positions),
-                    ("slot_mapping", slot_mapping)):
-        _cuda(t, name)
-    _need(key_cache.dim() == 4 and value_cache.shape == key_cache.shape, "caches must be [N, H_kv, bs, d]")
-    num_blocks, hkv, bs, d = key_cache.shape
+    _cuda(key_cache, "key_cache")
+    _cuda(value_cache, "value_cache")
+    _cuda(positions, "positions")
+    _cuda(slot_mapping, "slot_mapping")
+    shape, dtype = key_cache.shape, query.dtype
+    if len(shape) != 4 or value_cache.shape != shape:
+        raise ValueError("caches must be [N, H_kv, bs, d]")
+    num_blocks, hkv, bs, d = shape
     query_out, strides, rot, code = _rope_inputs(query, key, value, inv_freq, layout, query_out, hkv, d, stream)
     t = query.shape[0]
-    _need(query.dtype == key_cache.dtype == value_cache.dtype, "query, key, value and caches must share a dtype")
-    _need(positions.dtype == torch.int32 and positions.shape == (t,), "positions: int32 [T]")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (t,), "slot_mapping: int64 [T]")
-    weight_code = None
+    if key_cache.dtype is not dtype or value_cache.dtype is not dtype:
+        raise ValueError("query, key, value and caches must share a dtype")
+    if positions.dtype is not torch.int32 or positions.shape != (t,):
+        raise ValueError("positions: int32 [T]")
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (t,):
+        raise ValueError("slot_mapping: int64 [T]")
+    weight_dtype = None
     for w in (q_weight, k_weight):
         if w is None:
             continue
         _cuda(w, "weights")
-        _need(w.shape == (d,) and w.dtype in (torch.float32, query.dtype), "weights: [d], float32 or the queries' dtype")
-        _need(weight_code in (None, _dtype_code(w)), "q_weight and k_weight must share a dtype")
-        weight_code = _dtype_code(w)
+        if w.shape != (d,) or (w.dtype is not torch.float32 and w.dtype is not dtype) or weight_dtype not in (None, w.dtype):
+            raise ValueError("weights: [d], float32 or the queries' dtype, the same for both")
+        weight_dtype = w.dtype
     dev = key_cache.device
     _one_device(dev, query, key, value, value_cache, q_weight, k_weight, inv_freq, positions, slot_mapping, query_out)
     _launch(library().pa_norm_rope_write_kv, dev, stream, query_out.data_ptr(), query.data_ptr(), key.data_ptr(),
             value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
             None if k_weight is None else k_weight.data_ptr(), inv_freq.data_ptr() if rot else None, positions.data_ptr(),
             slot_mapping.data_ptr(), *strides, t, query.shape[1], hkv, d, rot, code, float(factor), float(eps),
-            float(weight_offset), weight_code or 0, bs, num_blocks, _dtype_code(query))
+            float(weight_offset), _TORCH_DTYPES.get(weight_dtype, 0), bs, num_blocks, _dtype_code(query))
     return query_out
 
 
@@ -173,13 +187,14 @@ def accept_tree(parents: torch.Tensor, tokens: torch.Tensor, choices: torch.Tens
     choice at the node (``choices`` [T]; int32 or int64, as ``tokens``), up to ``max_accepted`` nodes; and the choice at the last one.
     """
     t, b = _nodes(parents, q_offsets)
-    for name, x in (("tokens", tokens), ("choices", choices)):
-        _cuda(x, name)
-        if x.dtype not in (torch.int32, torch.int64) or x.dtype is not tokens.dtype or x.shape != (t,):
-            raise ValueError("tokens and choices: int32 or int64 [T], of one dtype")
+    _cuda(tokens, "tokens")
+    _cuda(choices, "choices")
+    dtype = tokens.dtype
+    if (dtype is not torch.int64 and dtype is not torch.int32) or choices.dtype is not dtype or tokens.shape != (t,) or choices.shape != (t,):
+        raise ValueError("tokens and choices: int32 or int64 [T], of one dtype")
     dev, depth = parents.device, int(max_accepted)
     _need(1 <= depth <= MAX_TREE_NODES, "max_accepted must be 1 to 1024")
-    out = _outputs(out, TreePath, (((b, depth), torch.int32), ((b,), torch.int32), ((b,), tokens.dtype)), dev, stream)
+    out = _outputs(out, TreePath, (((b, depth), torch.int32), ((b,), torch.int32), ((b,), dtype)), dev, stream)
     _one_device(dev, tokens, choices, q_offsets, *out)
     _launch(library().pa_accept_tree, dev, stream, out.accepted.data_ptr(), out.num_accepted.data_ptr(),
             out.next_tokens.data_ptr(), parents.data_ptr(), tokens.data_ptr(), choices.data_ptr(), q_offsets.data_ptr(), b, t,
@@ -217,19 +232,23 @@ def compact_tree(key_caches, value_caches, slot_mapping: torch.Tensor, q_offsets
     """
     keys, shape, dtype, dev = _layer_pointers(key_caches, "key_caches")
     values, vshape, vdtype, vdev = _layer_pointers(value_caches, "value_caches")
-    _need(len(keys) == len(values) and shape == vshape and dtype == vdtype and dev == vdev, "key_caches and value_caches must match")
-    _need(dtype in (torch.float32, torch.float16, torch.bfloat16), "caches: float32, float16 or bfloat16")
+    if len(keys) != len(values) or shape != vshape or dtype is not vdtype or dev != vdev:
+        raise ValueError("key_caches and value_caches must match")
+    if dtype is not torch.bfloat16 and dtype is not torch.float16 and dtype is not torch.float32:
+        raise ValueError("caches: float32, float16 or bfloat16")
     num_blocks, hkv, bs, d = shape
-    for name, t in (("q_offsets", q_offsets), ("accepted", accepted), ("num_accepted", num_accepted), ("block_tables", block_tables),
-                    ("context_lens", context_lens), ("free_blocks", free_blocks), ("num_free", num_free)):
-        _int32(t, name)
+    _int32s("q_offsets accepted num_accepted block_tables context_lens free_blocks num_free", q_offsets, accepted, num_accepted,
+            block_tables, context_lens, free_blocks, num_free)
     _cuda(slot_mapping, "slot_mapping")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1, "slot_mapping: int64 [T]")
-    _need(block_tables.dim() == 2 and accepted.dim() == 2, "block_tables: int32 [B, max_blocks], accepted: int32 [B, depth]")
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping: int64 [T]")
+    if block_tables.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("block_tables: int32 [B, max_blocks], accepted: int32 [B, depth]")
     b, width = block_tables.shape
-    _need(accepted.shape[0] == b and num_accepted.shape == (b,) and context_lens.shape == (b,) and q_offsets.shape == (b + 1,),
-          "accepted [B, depth], num_accepted and context_lens [B], q_offsets [B + 1]")
-    _need(free_blocks.shape == (num_blocks,) and num_free.numel() == 1, "free_blocks: int32 [num_blocks], num_free: int32 [1]")
+    if accepted.shape[0] != b or num_accepted.shape != (b,) or context_lens.shape != (b,) or q_offsets.shape != (b + 1,):
+        raise ValueError("accepted [B, depth], num_accepted and context_lens [B], q_offsets [B + 1]")
+    if free_blocks.shape != (num_blocks,) or num_free.numel() != 1:
+        raise ValueError("free_blocks: int32 [num_blocks], num_free: int32 [1]")
     out = _outputs(out, TreeState, (((b,), torch.int32), (tuple(num_free.shape), torch.int32)), dev, stream)
     _one_device(dev, slot_mapping, q_offsets, accepted, num_accepted, block_tables, context_lens, free_blocks, num_free, *out)
     _launch(library().pa_compact_tree, dev, stream, keys.buffer_info()[0], values.buffer_info()[0], len(keys), slot_mapping.data_ptr(), q_offsets.data_ptr(),
