@@ -658,11 +658,11 @@ int pa_accept_tree(int32_t* accepted, int32_t* num_accepted, void* next_tokens, 
  * device pointers, as pa_write_kv_layers'; all caches of a block geometry; dtype PA_F32, PA_F16 or PA_BF16.  Requests'
  * blocks must be their own (as pa_advance_tables').
  * accepted is any ascending choice of a request's nodes (pa_accept_tree's, or a sampling rule's).  A
- * request whose accepted nodes are not, or whose length is below n_b or outside its table, keeps its length and
- * blocks (of the latter two, nodes may have moved) and sets PA_ERR_BAD_CONTEXT; one with an id outside
- * [0, num_blocks) among the blocks that it would give back keeps them and its length and sets PA_ERR_BAD_TABLE; a node whose own or new slot
- * lies outside the pool does not move and sets PA_ERR_BAD_SLOT.  A stack without room for what is given back
- * sets PA_ERR_BAD_TABLE, and lengths and count stay as they are.
+ * request whose accepted nodes are not, or whose length is below n_b or outside its table, keeps its length, blocks
+ * and rows and sets PA_ERR_BAD_CONTEXT; one with an id outside [0, num_blocks) among the blocks that it would give back keeps them
+ * too and sets PA_ERR_BAD_TABLE; a stack without room for what is given back, or a negative count, sets PA_ERR_BAD_TABLE, and lengths,
+ * count, stack and all rows stay as they are.  (What is left whole can be compacted by another call.)  A node whose own
+ * or new slot lies outside the pool does not move and sets PA_ERR_BAD_SLOT.
  */
 int pa_compact_tree(void* const* key_caches, void* const* value_caches, int num_layers, const int64_t* slot_mapping,
                     const int32_t* q_offsets, const int32_t* accepted, const int32_t* num_accepted,

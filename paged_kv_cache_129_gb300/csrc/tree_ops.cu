@@ -117,55 +117,69 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_tree_kernel(const Accep
 
 // ---- compaction ----------------------------------------------------------------------------------------
 
-constexpr int kCompactThreads = 256, kCompactCtasPerSm = 16;
+// CTAs per SM of the rows' parts: 256 requests of 28 layers (see below) 15.8 us with 12, 16.6 with 10, 16.9 with 16.
+constexpr int kCompactThreads = 256, kCompactCtasPerSm = 12;
 
 // Whether request b's accepted nodes are some of its n nodes in ascending order.  Any number of threads, each for itself.
 __device__ __forceinline__ bool is_path(const CompactArgs& a, int b, int n, int count) {
     if (count < 0 || count > n || count > a.max_accepted) return false;
+    const int32_t* path = a.accepted + (long long)b * a.max_accepted;
+    constexpr int kAtOnce = 8;
     int before = -1;
     bool ok = true;
-#pragma unroll 4
-    for (int j = 0; j < count; ++j) {  // (loads that do not wait for the comparisons)
-        const int node = a.accepted[(long long)b * a.max_accepted + j];
-        ok = ok && node > before && node < n;
-        before = node;
+    for (int j0 = 0; j0 < count; j0 += kAtOnce) {
+        int node[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) node[k] = j0 + k < count ? path[j0 + k] : INT_MAX;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            ok = ok && (j0 + k >= count || (node[k] > before && node[k] < n));
+            before = node[k];
+        }
     }
     return ok;
+}
+
+__device__ __forceinline__ int blocks_of(int positions, int block_size) { return (int)(((unsigned)positions + block_size - 1) / (unsigned)block_size); }
+
+// What becomes of request b: its new length, and how many blocks from which on go back; gives -1: it is left as it is, with these errors.
+struct Rest {
+    int length, keep, gives;
+    unsigned errors;
+};
+__device__ __forceinline__ Rest rest_of(const CompactArgs& a, int b) {
+    int first;
+    bool bad;
+    const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), L = a.context_lens[b], k = a.num_accepted[b], bs = a.block_size;
+    if (bad || L < n || L > (long long)a.max_blocks * bs || !is_path(a, b, n, k)) return Rest{L, 0, -1, kErrBadContext};
+    const int keep = blocks_of(L - n + k, bs), had = blocks_of(L, bs);
+    const int32_t* table = a.block_tables + (long long)b * a.max_blocks;
+    constexpr int kAtOnce = 4;
+    bool ids = true;
+    for (unsigned j0 = keep; j0 < (unsigned)had; j0 += kAtOnce) {
+        int id[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) id[k] = j0 + k < (unsigned)had ? table[j0 + k] : 0;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) ids = ids && id[k] >= 0 && id[k] < a.num_blocks;
+    }
+    if (!ids) return Rest{L, 0, -1, kErrBadTable};
+    return Rest{L - n + k, keep, had - keep, 0u};
 }
 
 // New lengths, and the blocks given back: one CTA, a contiguous run of requests per thread.
 __device__ __forceinline__ void trim(const CompactArgs& a) {
     __shared__ int sums[kCompactThreads + 1];
-    const int tid = threadIdx.x, B = a.num_seqs, bs = a.block_size;
+    const int tid = threadIdx.x, B = a.num_seqs;
     const int per = (B + kCompactThreads - 1) / kCompactThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
     const int free0 = *a.num_free;
     unsigned bits = 0;
-    // blocks that request b gives back, from which on; -1: it keeps its length
-    auto give = [&](int b, int* keep, int* length) {
-        int first;
-        bool bad;
-        const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), L = a.context_lens[b], k = a.num_accepted[b];
-        *length = L;
-        if (bad || L < n || L > (long long)a.max_blocks * bs || !is_path(a, b, n, k)) {
-            bits |= kErrBadContext;
-            return -1;
-        }
-        *keep = (int)(((long long)L - n + k + bs - 1) / bs);
-        const int had = (int)(((long long)L + bs - 1) / bs);
-        for (int j = *keep; j < had; ++j) {
-            const int id = a.block_tables[(long long)b * a.max_blocks + j];
-            if (id < 0 || id >= a.num_blocks) {
-                bits |= kErrBadTable;
-                return -1;
-            }
-        }
-        *length = L - n + k;
-        return had - *keep;
-    };
-    int keep = 0, length = 0, gives = 0, mine = 0;  // (of one request per thread, as nearly always, kept until it is written)
+    Rest rest{};  // (of one request per thread, as nearly always, kept until it is written)
+    int mine = 0;
     for (int b = b0; b < b1; ++b) {
-        gives = give(b, &keep, &length);
-        mine += max(0, gives);
+        rest = rest_of(a, b);
+        bits |= rest.errors;
+        mine += max(0, rest.gives);
     }
     if (tid == 0) sums[0] = 0;
     sums[tid + 1] = mine;
@@ -191,39 +205,76 @@ __device__ __forceinline__ void trim(const CompactArgs& a) {
     if (!room) bits |= kErrBadTable;
     int at = free0 + sums[tid];
     for (int b = b0; b < b1; ++b) {
-        if (per > 1) gives = give(b, &keep, &length);
+        if (per > 1) rest = rest_of(a, b);
         if (room)
-            for (int j = 0; j < gives; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + keep + j];
-        a.context_lens_out[b] = room ? length : a.context_lens[b];
+            for (int j = 0; j < rest.gives; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + rest.keep + j];
+        a.context_lens_out[b] = room ? rest.length : a.context_lens[b];
     }
     if (tid == 0) *a.num_free_out = room ? free0 + total : free0;
     if (bits) atomicOr(a.err, bits);
 }
 
+// Whether the stack has room for all that goes back, by the requests themselves; a whole CTA.  (Only of a stack that holds more than the
+// blocks in use leave, see below.)
+__device__ __noinline__ bool has_room(const CompactArgs& a, int free0) {
+    __shared__ long long sums[kCompactThreads / 32];
+    long long sum = 0;
+    for (int b = threadIdx.x; b < a.num_seqs; b += kCompactThreads) sum += max(0, rest_of(a, b).gives);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = free0;
+#pragma unroll
+    for (int w = 0; w < kCompactThreads / 32; ++w) sum += sums[w];
+    return sum <= a.num_blocks;
+}
+
 // Row (node a_j, layer, K or V, kv head) goes to the place of node j, for the nodes that are not there already: those behind the first that is
 // not.  CTA (request, part of its rows); a thread has columns of sizeof(Vec) bytes and takes the nodes in order, kCompactBatch at a time:
-// a node's place is written behind every read of it, since a_j >= j.  CTA 0 has the lengths and the blocks.
+// a node's place is written behind every read of it, since a_j >= j.  lead 1: CTA 0 has the lengths and the blocks; 0: a launch behind this
+// one has them, since they replace what every CTA reads.
+// Nothing of a request moves that keeps its length (moved twice, a branch would be lost), so each CTA decides for itself what trim() will.
+// What all requests give back matters only for the room on the stack.  Request b gives at most n_b / block_size blocks, rounded up,
+// and holds as many at least, so that a stack of the blocks that nobody holds has room for this bound; the sum of it costs less than the
+// exact one, which is left to stacks without.
 // The rows are 64 - 512 bytes here and there, each read and written once: HBM bounds many requests, latency few (28 layers of 4 heads of 128, bf16,
-// on the GPU: 256 requests with up to 16 accepted nodes 19 us, 64 with up to 5 7.2 us; a CTA per request and a node at a time 168 and 51).
+// captured calls: 256 requests with up to 16 accepted nodes 15.8 us, 64 with up to 5 5.5 us, in place 19.2 and 8.0; without the CTAs' own
+// verdicts, moving first, 15.0 and 4.8; a CTA per request and a node at a time was 168 and 51 with the launch).
 constexpr int kCompactBatch = 8;
 template <typename Vec>
-__global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const CompactArgs a, const __grid_constant__ CachePtrs caches, int parts) {
+__global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const CompactArgs a, const __grid_constant__ CachePtrs caches, int parts,
+                                                                       int lead) {
     __shared__ long long from[kMaxTreeNodes], to[kMaxTreeNodes];  // bytes, of kv head 0
     __shared__ int moving[kCompactThreads / 32];
+    __shared__ long long most[kCompactThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
-    if (blockIdx.x == 0) {
+    if ((int)blockIdx.x < lead) {
         trim(a);
         return;
     }
-    const int b = (blockIdx.x - 1) / parts, part = (blockIdx.x - 1) - b * parts, H = a.num_kv_heads, bs = a.block_size, tid = threadIdx.x;
+    const int at = (int)blockIdx.x - lead, b = at / parts, part = at - b * parts, H = a.num_kv_heads, bs = a.block_size, tid = threadIdx.x;
+    auto may_give = [&](int i) {  // blocks that request i may give back
+        const int lo = a.q_offsets[i], hi = a.q_offsets[i + 1];
+        return is_run(lo, hi, a.num_tokens) ? blocks_of(hi - lo, bs) : 0;
+    };
+    long long back = tid < a.num_seqs ? may_give(tid) : 0;  // (read beside what follows)
     int first;
     bool bad;
-    const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), count = a.num_accepted[b];
-    if (bad || count <= 0 || count > n || count > a.max_accepted) return;
+    const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), count = a.num_accepted[b], L = a.context_lens[b], free0 = *a.num_free;
+    if (bad || count <= 0 || count > n || count > a.max_accepted || L < n || L > (long long)a.max_blocks * bs || free0 < 0) return;
     const long long slots = (long long)a.num_blocks * bs;
     const int32_t* path = a.accepted + (long long)b * a.max_accepted;
+    const int32_t* table = a.block_tables + (long long)b * a.max_blocks;
     bool wrong = false;
+    if (tid >= kCompactThreads - 32) {  // a warp that hardly ever has nodes
+        const unsigned keep = blocks_of(L - n + count, bs), had = blocks_of(L, bs);
+        for (unsigned j = keep + tid % 32; j < had; j += 32) {
+            const int id = table[j];
+            wrong |= id < 0 || id >= a.num_blocks;
+        }
+    }
     int still = 0;  // nodes that are in their place
     for (int j = tid; j < count; j += kCompactThreads) {
         const int node = path[j], before = j > 0 ? path[j - 1] : -1;
@@ -234,7 +285,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const Com
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const long long slot = a.slot_mapping[first + (k ? j : node)];
-            const long long blk = slot >= 0 ? slot / bs : 0;
+            const long long blk = slot < 0 ? 0 : (slot >> 32) == 0 ? (unsigned)slot / (unsigned)bs : slot / bs;
             at[k] = slot < 0 || slot >= slots ? -1 : (blk * H * bs + (slot - blk * bs)) * a.row_bytes;
         }
         if (at[0] < 0 || at[1] < 0) {
@@ -244,14 +295,16 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const Com
         from[j] = at[0];
         to[j] = at[1];
     }
-    if (__syncthreads_or(wrong)) return;
+    for (int i = tid + kCompactThreads; i < a.num_seqs; i += kCompactThreads) back += may_give(i);
     still = __reduce_add_sync(0xffffffffu, still);
-    if ((tid & 31) == 0) moving[tid >> 5] = still;
-    __syncthreads();
+    back = __reduce_add_sync(0xffffffffu, (unsigned)back & 0xffffu) + ((long long)__reduce_add_sync(0xffffffffu, (unsigned)(back >> 16)) << 16);
+    if ((tid & 31) == 0) moving[tid >> 5] = still, most[tid >> 5] = back;
+    if (__syncthreads_or(wrong)) return;
     still = 0;
+    back = 0;
 #pragma unroll
-    for (int w = 0; w < kCompactThreads / 32; ++w) still += moving[w];
-    if (still == count) return;
+    for (int w = 0; w < kCompactThreads / 32; ++w) still += moving[w], back += most[w];
+    if (still == count || (free0 + back > a.num_blocks && !has_room(a, free0))) return;
     const int columns = a.row_bytes / (int)sizeof(Vec), items = 2 * a.num_layers * H * columns;
     for (int x = part * kCompactThreads + tid; x < items; x += parts * kCompactThreads) {
         const int unit = x / columns, column = x - unit * columns, cache = unit / H, h = unit - cache * H;
@@ -266,6 +319,12 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const Com
                 if (j0 + k < count && from[j0 + k] >= 0) *reinterpret_cast<Vec*>(base + to[j0 + k]) = v[k];
         }
     }
+}
+
+__global__ void __launch_bounds__(kCompactThreads) trim_kernel(const CompactArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    trim(a);
 }
 
 }  // namespace
@@ -286,10 +345,14 @@ cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, c
     const long long items = 2ll * a.num_layers * a.num_kv_heads * (a.row_bytes / vec), most = (items + kCompactThreads - 1) / kCompactThreads;
     const long long wanted = a.num_seqs ? ((long long)kCompactCtasPerSm * a.num_sms + a.num_seqs - 1) / a.num_seqs : 1;
     const int parts = (int)std::max(1ll, std::min(most, wanted));
-    const dim3 grid((unsigned)(1 + (long long)a.num_seqs * parts)), block(kCompactThreads);
-    if (a.vector) return launch_pdl(compact_tree_kernel<uint4>, grid, block, 0, stream, a, caches, parts);
-    if (a.elem_bytes == 4) return launch_pdl(compact_tree_kernel<uint32_t>, grid, block, 0, stream, a, caches, parts);
-    return launch_pdl(compact_tree_kernel<uint16_t>, grid, block, 0, stream, a, caches, parts);
+    const bool in_place = a.context_lens_out == a.context_lens || a.num_free_out == a.num_free;
+    const int lead = in_place && a.num_seqs > 0 ? 0 : 1;
+    const dim3 grid((unsigned)(lead + (long long)a.num_seqs * parts)), block(kCompactThreads);
+    cudaError_t e;
+    if (a.vector) e = launch_pdl(compact_tree_kernel<uint4>, grid, block, 0, stream, a, caches, parts, lead);
+    else if (a.elem_bytes == 4) e = launch_pdl(compact_tree_kernel<uint32_t>, grid, block, 0, stream, a, caches, parts, lead);
+    else e = launch_pdl(compact_tree_kernel<uint16_t>, grid, block, 0, stream, a, caches, parts, lead);
+    return e != cudaSuccess || lead ? e : launch_pdl(trim_kernel, dim3(1), block, 0, stream, a);
 }
 
 }  // namespace pa
