@@ -169,13 +169,13 @@ __device__ __forceinline__ Rest rest_of(const CompactArgs& a, int b) {
 
 // New lengths, and the blocks given back: one CTA, a contiguous run of requests per thread.
 __device__ __forceinline__ void trim(const CompactArgs& a) {
-    __shared__ int sums[kCompactThreads + 1];
+    __shared__ long long sums[kCompactThreads + 1];  // (runs that overlap may give back more blocks than 31 bits count)
     const int tid = threadIdx.x, B = a.num_seqs;
     const int per = (B + kCompactThreads - 1) / kCompactThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
     const int free0 = *a.num_free;
     unsigned bits = 0;
     Rest rest{};  // (of one request per thread, as nearly always, kept until it is written)
-    int mine = 0;
+    long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         rest = rest_of(a, b);
         bits |= rest.errors;
@@ -186,13 +186,13 @@ __device__ __forceinline__ void trim(const CompactArgs& a) {
     __syncthreads();
     if (tid < 32) {  // a run of the threads' sums per lane
         constexpr int kRun = kCompactThreads / 32;
-        int sum = 0;
+        long long sum = 0;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) sum += sums[tid * kRun + i + 1];
-        int before = sum;
+        long long before = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, before, o);
+            const long long x = __shfl_up_sync(0xffffffffu, before, o);
             if (tid >= o) before += x;
         }
         before -= sum;
@@ -200,17 +200,17 @@ __device__ __forceinline__ void trim(const CompactArgs& a) {
         for (int i = 0; i < kRun; ++i) sums[tid * kRun + i + 1] = before += sums[tid * kRun + i + 1];
     }
     __syncthreads();
-    const int total = sums[kCompactThreads];
-    const bool room = free0 >= 0 && (long long)free0 + total <= a.num_blocks;
+    const long long total = sums[kCompactThreads];
+    const bool room = free0 >= 0 && free0 + total <= a.num_blocks;
     if (!room) bits |= kErrBadTable;
-    int at = free0 + sums[tid];
+    int at = (int)(free0 + sums[tid]);  // (of use where there is room)
     for (int b = b0; b < b1; ++b) {
         if (per > 1) rest = rest_of(a, b);
         if (room)
             for (int j = 0; j < rest.gives; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + rest.keep + j];
         a.context_lens_out[b] = room ? rest.length : a.context_lens[b];
     }
-    if (tid == 0) *a.num_free_out = room ? free0 + total : free0;
+    if (tid == 0) *a.num_free_out = room ? (int)(free0 + total) : free0;
     if (bits) atomicOr(a.err, bits);
 }
 

@@ -95,3 +95,20 @@ def test_a_stack_with_just_enough_room(requests, over, in_place):
     got = []
     assert status(lambda: got.append(compact(c, keys, values, in_place))) == (5 if over else 7)
     compare(c, [] if over else served, keys, values, *got[0])
+
+
+def test_more_blocks_given_back_than_31_bits_count():
+    """Offsets that descend between runs that overlap: 2048 requests give back 2^20 blocks each, 2^31 in all, on a stack with room for 8."""
+    run, requests = 1 << 20, 4095
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    off = torch.tensor([0, run], **i32).repeat(requests // 2 + 1)
+    tables = torch.zeros(requests, run, **i32)
+    lens = torch.full((requests,), run, **i32)
+    around = torch.full((24,), 7, **i32)
+    keys, values = (torch.zeros(8, 1, 1, 4, device="cuda") for _ in range(2))
+    got = []
+    assert status(lambda: got.append(pa.compact_tree(
+        [keys], [values], torch.zeros(run, dtype=torch.int64, device="cuda"), off, torch.zeros(requests, 1, **i32), torch.zeros(requests, **i32),
+        tables, lens, around[8:16], torch.zeros(1, **i32)))) == 5
+    assert torch.equal(got[0].context_lens, lens) and int(got[0].num_free) == 0
+    assert (around == 7).all()
