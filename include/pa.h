@@ -655,7 +655,8 @@ int pa_accept_tree(int32_t* accepted, int32_t* num_accepted, void* next_tokens, 
  * num_accepted[b], and the blocks behind that go back: pushed onto free_blocks, by request, in table
  * order, with num_free_out [1] the new count.  context_lens_out and num_free_out may be context_lens and
  * num_free.  Table entries of blocks given back stay; nothing reads them.  key_caches and value_caches are HOST arrays of num_layers
- * device pointers, as pa_write_kv_layers'; all caches of a block geometry; dtype PA_F32, PA_F16 or PA_BF16.  Requests'
+ * device pointers, as pa_write_kv_layers'; all caches of a block geometry, none listed twice or overlapping another (a cache
+ * that layers share is listed once: compacted twice it would lose rows); dtype PA_F32, PA_F16 or PA_BF16.  Requests'
  * blocks must be their own (as pa_advance_tables').
  * accepted is any ascending choice of a request's nodes (pa_accept_tree's, or a sampling rule's).  A
  * request whose accepted nodes are not, or whose length is below n_b or outside its table, keeps its length, blocks

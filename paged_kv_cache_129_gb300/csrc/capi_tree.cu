@@ -1,4 +1,5 @@
 // C-ABI entry points of a speculative step with a drafted tree: argument checks in front of the kernels of tree_ops.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -44,6 +45,18 @@ int rows_ok(const char* fn, int num_seqs, int num_tokens) {
     if (num_tokens < 0 || num_tokens > kMaxStepRows)
         return fail(PA_ERR_INVALID_ARG, "%s: num_tokens=%d outside [0, %d]", fn, num_tokens, kMaxStepRows);
     return PA_OK;
+}
+
+// Whether two of the caches of the layers, of `bytes` each, share a byte.
+bool caches_overlap(const CachePtrs& caches, int num_layers, unsigned long long bytes) {
+    uintptr_t at[2 * kMaxLayers];
+    uintptr_t* end = at;
+    for (const auto* list : {&caches.key, &caches.value})
+        for (int l = 0; l < num_layers; ++l) *end++ = reinterpret_cast<uintptr_t>((*list)[l]);
+    if (!std::is_sorted(at, end)) std::sort(at, end);
+    for (const uintptr_t* p = at + 1; p < end; ++p)
+        if (*p - p[-1] < bytes) return true;
+    return false;
 }
 
 bool attend_sizes_ok(int num_heads, int num_kv_heads, int head_dim) {
@@ -138,6 +151,8 @@ int pa_compact_tree(void* const* key_caches, void* const* value_caches, int num_
         caches.key[l] = static_cast<char*>(key_caches[l]);
         caches.value[l] = static_cast<char*>(value_caches[l]);
     }
+    if (caches_overlap(caches, num_layers, (unsigned long long)num_blocks * block_size * num_kv_heads * row_bytes))
+        return fail(PA_ERR_INVALID_ARG, "pa_compact_tree: caches overlap (each is listed once: a cache compacted twice loses rows)");
     CompactArgs a{slot_mapping, q_offsets, accepted, num_accepted, block_tables, context_lens, free_blocks, num_free, context_lens_out,
                   num_free_out, num_layers, num_seqs, num_tokens, max_accepted, num_kv_heads, row_bytes, block_size, max_blocks_per_seq,
                   num_blocks, vector ? 1 : 0, eb, 0, nullptr};

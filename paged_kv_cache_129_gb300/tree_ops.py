@@ -226,7 +226,7 @@ def compact_tree(key_caches, value_caches, slot_mapping: torch.Tensor, q_offsets
                  num_free: torch.Tensor, out: Optional[TreeState] = None, stream=None) -> TreeState:
     """``pa_compact_tree``: moves the accepted nodes (``accepted`` int32 [B, depth], ascending, ``num_accepted`` [B] of them) to
     the places behind the request's cached positions in every layer's caches (one tensor [layers, N, H_kv, bs, d], or a sequence of
-    [N, H_kv, bs, d] tensors, each for keys and values), shortens the requests to them and gives the blocks behind back to ``free_blocks``.
+    [N, H_kv, bs, d] tensors, each for keys and values; a cache that layers share is listed once), shortens the requests to them and gives the blocks behind back to ``free_blocks``.
     ``slot_mapping`` and ``q_offsets`` are ``advance_tables``'.  ``out``: two tensors as ``TreeState`` to write to, which may be
     ``context_lens`` and ``num_free``.
     """
