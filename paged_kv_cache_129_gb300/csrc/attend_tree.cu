@@ -278,29 +278,38 @@ __device__ __forceinline__ void look_ahead(const TreeAttendArgs& a, Seam* seams,
     const int behind = a.num_blocks * a.num_kv_heads * (BS / 8);  // the first group behind the pool: copied as zeros
     int seq = start.seq, kvh = start.kvh, e = start.entry;
     long long unit = start.unit;  // where the unit begins
-    bool more = seq >= 0;
+    bool more = seq >= 0, taken = false;  // taken: the unit at hand is behind us
     Request r = start.r;
     unsigned tiles = 0;
+    // The unit behind the one at hand; false: there is none.  Requests without nodes, which a captured batch may hold by the thousand, are
+    // passed 32 at a time, a lane each, and behind the end of the share not at all (32 requests alone 46 us, in front of 8160 empty slots 56; passed
+    // one by one, before the piece at hand was given to the other roles, 747).
+    auto next_unit = [&] {
+        if (++e < r.entries()) return true;
+        e = 0;
+        if (++kvh < a.num_kv_heads) return true;
+        kvh = 0;
+        for (++seq; seq < a.num_seqs; seq += 32) {
+            const unsigned nodes = __ballot_sync(0xffffffffu, seq + lane < a.num_seqs && Request(a, min(seq + lane, a.num_seqs - 1)).rows > 0);
+            if (nodes) {
+                seq += __ffs(nodes) - 1;
+                r = Request(a, seq);
+                return true;
+            }
+        }
+        return false;
+    };
 #pragma unroll 1
     for (unsigned i = 0;; ++i) {
         Job j{};
         while (more && j.begin == j.end) {  // the next unit with tiles in the share
+            if (taken && !next_unit()) break;
             const bool pair = r.paired(e);
-            const long long cost = r.cost(pair);
             j = Job{r.L, r.n, r.first_token, seq, e * 2 * kTile, kvh, r.tiles, tiles_in(start.pos - unit, r.tiles, pair),
                     tiles_in(start.stop - unit, r.tiles, pair), pair};
-            unit += cost;
-            if (++e == r.entries()) {
-                e = 0;
-                if (++kvh == a.num_kv_heads) {
-                    kvh = 0;
-                    do {
-                        if (++seq == a.num_seqs) break;
-                        r = Request(a, seq);
-                    } while (r.rows == 0);
-                }
-            }
-            more = unit < start.stop && seq < a.num_seqs;
+            unit += r.cost(pair);
+            more = unit < start.stop;
+            taken = true;
         }
         const bool have = j.begin < j.end;
         if (i >= kPieces && !ready(&sm.job_free[i % kPieces], (i / kPieces - 1) & 1, a.err, &sm.abort)) return;
