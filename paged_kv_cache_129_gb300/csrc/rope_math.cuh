@@ -1,4 +1,4 @@
-// Rotary angles and the slots of a head row that the rotary kernels work on.
+// Rotary angles and the chunks of a head row that the rotary kernels work on.
 //
 // Angles of far positions: p * inv_freq in float32 is off by p * 2^-24 radians, useless at p = 10^6.  A turn is
 // therefore a 64-bit fixed-point fraction: u = frac(inv_freq / 2 pi) * 2^64, rounded to half a unit (a double alone would be off
@@ -104,80 +104,5 @@ struct Chunk {
         else w[0] = pack2<T>(make_float2(x, 0.f));
     }
 };
-
-// (cos, sin) of a token's pairs in shared memory, for slots of V pairs: two pairs to 16 bytes, those of neighbouring slots
-// next to each other, so that the lanes of a row read without bank conflicts.
-template <int V>
-__device__ __forceinline__ int turn_place(int pair, int slots) {
-    return V == 1 ? pair : (((pair % V) / 2) * slots + pair / V) * 2 + pair % 2;
-}
-template <int V>
-__device__ __forceinline__ void load_turns(float2 (&cs)[V], const float2* of_token, int slot, int slots) {
-    if constexpr (V == 1) {
-        cs[0] = of_token[slot];
-    } else {
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-            const float4 w = *reinterpret_cast<const float4*>(of_token + (j * slots + slot) * 2);
-            cs[2 * j] = make_float2(w.x, w.y);
-            cs[2 * j + 1] = make_float2(w.z, w.w);
-        }
-    }
-}
-
-// One slot of a head row, two chunks of V elements, in float32.
-template <typename T, int VB>
-__device__ __forceinline__ void widen_slot(const Chunk<T, VB>& x0, const Chunk<T, VB>& x1, float* y0, float* y1) {
-    constexpr int V = Chunk<T, VB>::V;
-    if constexpr (V == 1) {
-        y0[0] = x0.one();
-        y1[0] = x1.one();
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const float2 a = x0.pair(i), b = x1.pair(i);
-            y0[2 * i] = a.x, y0[2 * i + 1] = a.y;
-            y1[2 * i] = b.x, y1[2 * i + 1] = b.y;
-        }
-    }
-}
-
-// Turns the V pairs of one slot in float32: y0[i] with y1[i], or neighbours.
-template <int V>
-__device__ __forceinline__ void turn_slot(float* y0, float* y1, const float2* cs, bool interleaved) {
-    if (V > 1 && interleaved) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float* y = 2 * i < V ? y0 : y1;
-            const int e = (2 * i) % V;
-            const float p = y[e], q = y[e + (V > 1 ? 1 : 0)];
-            y[e] = p * cs[i].x - q * cs[i].y;
-            y[e + (V > 1 ? 1 : 0)] = p * cs[i].y + q * cs[i].x;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float p = y0[i], q = y1[i];
-            y0[i] = p * cs[i].x - q * cs[i].y;
-            y1[i] = p * cs[i].y + q * cs[i].x;
-        }
-    }
-}
-
-// The slot back in chunks, each element rounded once.
-template <typename T, int VB>
-__device__ __forceinline__ void pack_slot(const float* y0, const float* y1, Chunk<T, VB>& x0, Chunk<T, VB>& x1) {
-    constexpr int V = Chunk<T, VB>::V;
-    if constexpr (V == 1) {
-        x0.put_one(y0[0]);
-        x1.put_one(y1[0]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            x0.put(i, make_float2(y0[2 * i], y0[2 * i + 1]));
-            x1.put(i, make_float2(y1[2 * i], y1[2 * i + 1]));
-        }
-    }
-}
 
 }  // namespace pa

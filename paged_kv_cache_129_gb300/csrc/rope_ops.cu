@@ -175,12 +175,60 @@ __device__ __forceinline__ uint32_t codes_of(float y0, float y1, float y2, float
            ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3) << 16);
 }
 
+// (cos, sin) of a token's pairs in shared memory, for slots of V pairs: two pairs to 16 bytes, those of neighbouring slots
+// next to each other, so that the lanes of a row read without bank conflicts.
+template <int V>
+__device__ __forceinline__ int turn_place(int pair, int slots) {
+    return V == 1 ? pair : (((pair % V) / 2) * slots + pair / V) * 2 + pair % 2;
+}
+template <int V>
+__device__ __forceinline__ void load_turns(float2 (&cs)[V], const float2* of_token, int slot, int slots) {
+    if constexpr (V == 1) {
+        cs[0] = of_token[slot];
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            const float4 w = *reinterpret_cast<const float4*>(of_token + (j * slots + slot) * 2);
+            cs[2 * j] = make_float2(w.x, w.y);
+            cs[2 * j + 1] = make_float2(w.z, w.w);
+        }
+    }
+}
+
 // The V pairs of one slot in float32: first[] and second[], rotated where TURNS is set.  Interleaved slots hold V pairs too.
 template <typename T, int VB>
 __device__ __forceinline__ void turned(const Chunk<T, VB>& x0, const Chunk<T, VB>& x1, const float2* cs, bool turns, bool interleaved,
                                        float* y0, float* y1) {
-    widen_slot<T, VB>(x0, x1, y0, y1);
-    if (turns) turn_slot<Chunk<T, VB>::V>(y0, y1, cs, interleaved);
+    constexpr int V = Chunk<T, VB>::V;
+    if constexpr (V == 1) {
+        y0[0] = x0.one();
+        y1[0] = x1.one();
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 a = x0.pair(i), b = x1.pair(i);
+            y0[2 * i] = a.x, y0[2 * i + 1] = a.y;
+            y1[2 * i] = b.x, y1[2 * i + 1] = b.y;
+        }
+    }
+    if (!turns) return;
+    if (V > 1 && interleaved) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float* y = 2 * i < V ? y0 : y1;
+            const int e = (2 * i) % V;
+            const float p = y[e], q = y[e + (V > 1 ? 1 : 0)];
+            y[e] = p * cs[i].x - q * cs[i].y;
+            y[e + (V > 1 ? 1 : 0)] = p * cs[i].y + q * cs[i].x;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float p = y0[i], q = y1[i];
+            y0[i] = p * cs[i].x - q * cs[i].y;
+            y1[i] = p * cs[i].y + q * cs[i].x;
+        }
+    }
 }
 
 template <int V>
