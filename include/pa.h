@@ -616,7 +616,7 @@ int pa_norm_rope_write_kv(void* query_out, const void* query, const void* key, c
  * bits: pa_tree_masks gives those of a tree; a chain's are those of causal runs, one node is a decode
  * step).  A row that sees nothing gets zeros; rows behind q_offsets[num_seqs] are left as they were.  What a row does not
  * see does not reach it, whatever its K and V hold (infinities and NaN too), nor does what lies behind a context.
- * Scores, softmax and sums are float32; the weights that multiply V are rounded to dtype, relative to an
+ * Scores, softmax and sums are float32; the weights, rounded to dtype before they are multiplied and summed, are relative to an
  * exponential of the row's that is at most 2^8 below its largest (f16: weights below 2^-14 of it lose bits).  query and out f16 or bf16, contiguous, 16-byte aligned; caches
  * [num_blocks, num_kv_heads, block_size, head_dim] of the same type, 16-byte aligned.  Compiled for head_dim 64
  * and 128, block_size 16 and 32 (PA_ERR_UNSUPPORTED otherwise).  Nodes past 64 * mask_words are seen by no row

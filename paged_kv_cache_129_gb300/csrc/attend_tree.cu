@@ -19,9 +19,11 @@
 // context are zeros; in the tiles that hold nodes or the context's end a warp clears the rows behind the end, and looks for infinities and
 // NaN in the nodes' V: these are taken out, noted, and put into the outputs of the rows that see them.
 // Numbers.  Scores, maxima, sums and the output accumulate in float32.  A weight is rounded to the cache's type for the second
-// product (half a step: bf16 2^-8 of it, as the output; f16 2^-11, and 2^-25 of the reference below 2^-14).  The
-// reference of the exponents follows the true maximum by steps of 2^8 at least: rescaling the output in tensor memory is rare that way, and weights stay
-// below 2^8.
+// product (half a step: bf16 2^-8 of it, as the output; f16 2^-11, and 2^-25 of the reference below 2^-14).  The sum that divides takes the
+// rounded weights, so that those that multiply V sum to one: a row over equal values returns them, and a dominant weight's rounding cancels (what weights
+// alone put in, restated in float64: as much as with the sum of the unrounded ones where scores are flat, half of it and less where their deviation
+// is 3 or 6).  The reference of a row's exponents is its maximum when it was last moved: all rows of a warp move to their maxima once
+// one of them is 2^8 above its own, so that rescaling the output in tensor memory is rare, and weights are 2^8 at most.
 // Bound.  Long contexts (eight requests of 32k - 128k positions with 1 - 8 nodes) HBM: 475 us, 7.0 TB/s.  Steps (64 requests of 512 - 4096 with 16
 // nodes) 68 us, 4.6 TB/s: of an SM's 120 000 cycles 85 000 are its share of HBM's time, 15 000 pass before the first scores and the rest at the
 // pieces' ends.  Wide trees (16 requests of 2k - 8k with 48 - 128 nodes) 134 us, 0.90 PFLOP/s, tensor pipe 51 % busy: the softmax warps, whose code is
@@ -632,6 +634,15 @@ __device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float2 x) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// sum += the halves of w, in float32.  (Additions that take 16-bit operands: wide trees 134.3 us; widened first 137.6; the unrounded weights 133.4.)
+template <typename T>
+__device__ __forceinline__ void add_halves(uint32_t w, float2& sum) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.f16 %0, x, %0;\n\tadd.rn.f32.f16 %1, y, %1;\n\t}" : "+f"(sum.x), "+f"(sum.y) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}" : "+f"(sum.x), "+f"(sum.y) : "r"(w));
+}
+
 // Eight 16-byte units of a row per lane become, in groups of eight lanes, one unit of each of the group's rows: x[r] is unit lane % 8 of
 // row r.  Stores of x[r] then write whole 128-byte lines (a row to a lane, each store of a warp touched 32 of them, and the results of
 // a piece took 4000 cycles).
@@ -760,8 +771,8 @@ __device__ __forceinline__ void softmax_rows(const TreeAttendArgs& a, float* rec
                     for (int i = 0; i < 32; i += 2) {
                         const float2 y = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), f2, m2);
                         const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                        sum = add2(sum, e);
                         s[i / 2] = round2<T>(e);
+                        add_halves<T>(s[i / 2], sum);
                     }
                     tmem_st16(at + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
                 }
