@@ -167,67 +167,71 @@ __device__ __forceinline__ Rest rest_of(const CompactArgs& a, int b) {
     return Rest{L - n + k, keep, had - keep, 0u};
 }
 
-// New lengths, and the blocks given back: one CTA, a contiguous run of requests per thread.
-__device__ __forceinline__ void trim(const CompactArgs& a) {
-    __shared__ long long sums[kCompactThreads + 1];  // (runs that overlap may give back more blocks than 31 bits count)
-    const int tid = threadIdx.x, B = a.num_seqs;
-    const int per = (B + kCompactThreads - 1) / kCompactThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    const int free0 = *a.num_free;
-    unsigned bits = 0;
-    Rest rest{};  // (of one request per thread, as nearly always, kept until it is written)
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        rest = rest_of(a, b);
-        bits |= rest.errors;
-        mine += max(0, rest.gives);
-    }
-    if (tid == 0) sums[0] = 0;
-    sums[tid + 1] = mine;
-    __syncthreads();
-    if (tid < 32) {  // a run of the threads' sums per lane
-        constexpr int kRun = kCompactThreads / 32;
-        long long sum = 0;
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) sum += sums[tid * kRun + i + 1];
-        long long before = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, before, o);
-            if (tid >= o) before += x;
-        }
-        before -= sum;
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) sums[tid * kRun + i + 1] = before += sums[tid * kRun + i + 1];
-    }
-    __syncthreads();
-    const long long total = sums[kCompactThreads];
-    const bool room = free0 >= 0 && free0 + total <= a.num_blocks;
-    if (!room) bits |= kErrBadTable;
-    int at = (int)(free0 + sums[tid]);  // (of use where there is room)
-    for (int b = b0; b < b1; ++b) {
-        if (per > 1) rest = rest_of(a, b);
-        if (room)
-            for (int j = 0; j < rest.gives; ++j) a.free_blocks[at++] = a.block_tables[(long long)b * a.max_blocks + rest.keep + j];
-        a.context_lens_out[b] = room ? rest.length : a.context_lens[b];
-    }
-    if (tid == 0) *a.num_free_out = room ? (int)(free0 + total) : free0;
-    if (bits) atomicOr(a.err, bits);
+// Blocks that request b may give back: at most n_b / block_size, rounded up.
+__device__ __forceinline__ int may_give(const CompactArgs& a, int b) {
+    const int lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
+    return is_run(lo, hi, a.num_tokens) ? blocks_of(hi - lo, a.block_size) : 0;
+}
+
+// Sums over a warp of what 48 bits hold, in two parts of 32.
+__device__ __forceinline__ long long warp_sum(long long x) {
+    return __reduce_add_sync(0xffffffffu, (unsigned)x & 0xffffu) + ((long long)__reduce_add_sync(0xffffffffu, (unsigned)(x >> 16)) << 16);
 }
 
 // Whether the stack has room for all that goes back, by the requests themselves; a whole CTA.  (Only of a stack that holds more than the
-// blocks in use leave, see below.)
+// blocks in use leave, see below.  Runs that overlap may give back more blocks than 31 bits count.)
 __device__ __noinline__ bool has_room(const CompactArgs& a, int free0) {
-    __shared__ long long sums[kCompactThreads / 32];
+    __shared__ long long sums[32];
     long long sum = 0;
-    for (int b = threadIdx.x; b < a.num_seqs; b += kCompactThreads) sum += max(0, rest_of(a, b).gives);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x) sum += max(0, rest_of(a, b).gives);
+    sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
     __syncthreads();
     sum = free0;
-#pragma unroll
-    for (int w = 0; w < kCompactThreads / 32; ++w) sum += sums[w];
+    for (int w = 0; w < blockDim.x / 32; ++w) sum += sums[w];
     return sum <= a.num_blocks;
+}
+
+// New lengths, and the blocks given back: one CTA, a request per thread, in rounds.  (8192 requests of 16 nodes, captured: the call 134 us, in place 170;
+// with a contiguous run of requests per thread, passed twice, 163 and 255.)
+__device__ __forceinline__ void trim(const CompactArgs& a) {
+    __shared__ long long most[32];
+    __shared__ int sums[2][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x / 32, free0 = *a.num_free;
+    long long back = 0;
+    for (int b = tid; b < a.num_seqs; b += blockDim.x) back += may_give(a, b);
+    back = warp_sum(back);
+    if (lane == 0) most[warp] = back;
+    __syncthreads();
+    back = 0;
+    for (int w = 0; w < warps; ++w) back += most[w];
+    const bool room = free0 >= 0 && (free0 + back <= a.num_blocks || has_room(a, free0));
+    unsigned bits = room ? 0 : kErrBadTable;
+    int at = free0;
+    for (int b0 = 0, round = 0; b0 < a.num_seqs; b0 += blockDim.x, round ^= 1) {
+        const int b = b0 + tid;
+        const Rest rest = b < a.num_seqs ? rest_of(a, b) : Rest{};
+        bits |= rest.errors;
+        const int gives = room ? max(0, rest.gives) : 0;
+        int upto = gives;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (lane == 31) sums[round][warp] = upto;
+        __syncthreads();
+        int to = at + upto - gives;
+        for (int w = 0; w < warps; ++w) {
+            const int x = sums[round][w];
+            if (w < warp) to += x;
+            at += x;
+        }
+        for (int j = 0; j < gives; ++j) a.free_blocks[to + j] = a.block_tables[(long long)b * a.max_blocks + rest.keep + j];
+        if (b < a.num_seqs) a.context_lens_out[b] = room ? rest.length : a.context_lens[b];
+    }
+    if (tid == 0) *a.num_free_out = at;
+    if (bits) atomicOr(a.err, bits);
 }
 
 // Row (node a_j, layer, K or V, kv head) goes to the place of node j, for the nodes that are not there already: those behind the first that is
@@ -235,9 +239,9 @@ __device__ __noinline__ bool has_room(const CompactArgs& a, int free0) {
 // a node's place is written behind every read of it, since a_j >= j.  lead 1: CTA 0 has the lengths and the blocks; 0: a launch behind this
 // one has them, since they replace what every CTA reads.
 // Nothing of a request moves that keeps its length (moved twice, a branch would be lost), so each CTA decides for itself what trim() will.
-// What all requests give back matters only for the room on the stack.  Request b gives at most n_b / block_size blocks, rounded up,
-// and holds as many at least, so that a stack of the blocks that nobody holds has room for this bound; the sum of it costs less than the
-// exact one, which is left to stacks without.
+// What all requests give back matters only for the room on the stack.  Request b holds at least as many blocks as it may give back,
+// so that a stack of the blocks that nobody holds has room for the sum of these bounds; it costs less than the exact one, which is left to stacks
+// without.
 // The rows are 64 - 512 bytes here and there, each read and written once: HBM bounds many requests, latency few (28 layers of 4 heads of 128, bf16,
 // captured calls: 256 requests with up to 16 accepted nodes 15.8 us, 64 with up to 5 5.5 us, in place 19.2 and 8.0; without the CTAs' own
 // verdicts, moving first, 15.0 and 4.8; a CTA per request and a node at a time was 168 and 51 with the launch).
@@ -255,11 +259,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const Com
         return;
     }
     const int at = (int)blockIdx.x - lead, b = at / parts, part = at - b * parts, H = a.num_kv_heads, bs = a.block_size, tid = threadIdx.x;
-    auto may_give = [&](int i) {  // blocks that request i may give back
-        const int lo = a.q_offsets[i], hi = a.q_offsets[i + 1];
-        return is_run(lo, hi, a.num_tokens) ? blocks_of(hi - lo, bs) : 0;
-    };
-    long long back = tid < a.num_seqs ? may_give(tid) : 0;  // (read beside what follows)
+    long long back = tid < a.num_seqs ? may_give(a, tid) : 0;  // (read beside what follows)
     int first;
     bool bad;
     const int n = nodes_of(a.q_offsets, b, a.num_tokens, INT_MAX, &first, &bad), count = a.num_accepted[b], L = a.context_lens[b], free0 = *a.num_free;
@@ -295,9 +295,9 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const Com
         from[j] = at[0];
         to[j] = at[1];
     }
-    for (int i = tid + kCompactThreads; i < a.num_seqs; i += kCompactThreads) back += may_give(i);
+    for (int i = tid + kCompactThreads; i < a.num_seqs; i += kCompactThreads) back += may_give(a, i);
     still = __reduce_add_sync(0xffffffffu, still);
-    back = __reduce_add_sync(0xffffffffu, (unsigned)back & 0xffffu) + ((long long)__reduce_add_sync(0xffffffffu, (unsigned)(back >> 16)) << 16);
+    back = warp_sum(back);
     if ((tid & 31) == 0) moving[tid >> 5] = still, most[tid >> 5] = back;
     if (__syncthreads_or(wrong)) return;
     still = 0;
@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kernel(const Com
     }
 }
 
-__global__ void __launch_bounds__(kCompactThreads) trim_kernel(const CompactArgs a) {
+constexpr int kTrimThreads = 1024;
+__global__ void __launch_bounds__(kTrimThreads) trim_kernel(const CompactArgs a) {
     griddep_wait();
     griddep_launch_dependents();
     trim(a);
@@ -352,7 +353,7 @@ cudaError_t compact_tree_launch(const CompactArgs& a, const CachePtrs& caches, c
     if (a.vector) e = launch_pdl(compact_tree_kernel<uint4>, grid, block, 0, stream, a, caches, parts, lead);
     else if (a.elem_bytes == 4) e = launch_pdl(compact_tree_kernel<uint32_t>, grid, block, 0, stream, a, caches, parts, lead);
     else e = launch_pdl(compact_tree_kernel<uint16_t>, grid, block, 0, stream, a, caches, parts, lead);
-    return e != cudaSuccess || lead ? e : launch_pdl(trim_kernel, dim3(1), block, 0, stream, a);
+    return e != cudaSuccess || lead ? e : launch_pdl(trim_kernel, dim3(1), dim3((unsigned)std::min(kTrimThreads, (a.num_seqs + 31) / 32 * 32)), 0, stream, a);
 }
 
 }  // namespace pa
